@@ -70,7 +70,8 @@ typedef enum {
 
 typedef enum {
   W4A4_Y_F32 = 0,    /* fp32 output */
-  W4A4_Y_F16 = 1     /* fp16 output, round to nearest even from the fp32 result */
+  W4A4_Y_F16 = 1,    /* fp16 output, round to nearest even from the fp32 result */
+  W4A4_Y_BF16 = 2    /* bf16, round to nearest even (the 8-bit calls, w8a8_* and kv8_*, only) */
 } w4a4_ydtype_t;
 
 /* Human-readable name of a status code (static string, never NULL). */
@@ -396,6 +397,52 @@ w4a4_status_t nvfp4_gemm_debug_partials(const uint8_t* xq, const uint8_t* xs,
                                         int64_t M, int64_t N, int64_t K,
                                         int64_t m0, int64_t mc, int64_t n0, int64_t nc,
                                         int32_t* partials, void* stream);
+
+/*
+ * ---- 8-bit linear layers --------------------------------------------------
+ * For the layers that do not survive 4 bits: INT8 codes with one fp32 scale per
+ * token (activations) and per output channel (weights). The scales do not vary
+ * along K, so the reduction is one exact int32 sum.
+ */
+
+/*
+ * Symmetric INT8 quantization of activations, per row: a = max|x|;
+ * s = fl32(a / 127); q = rne(fl32(x / s)) with correctly rounded binary32
+ * divisions, in [-127, 127]; an all-zero row gives s = 0 and codes 0. x finite.
+ *
+ *   x       [M][ldx] row-major, 16-byte aligned, ldx >= K, ldx % 8 == 0, of
+ *           x_dtype W4A4_Y_F16 or W4A4_Y_BF16
+ *   M, K    K > 0, K % 16 == 0, K <= 2^30, M < 2^31
+ *   xq      out: int8 [M][K], 16-byte aligned;  xs  out: f32 [M]
+ */
+w4a4_status_t w8a8_quantize_act(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                                int8_t* xq, float* xs, void* stream);
+
+/* Offline weight quantization: the same rule on the rows of W[N][K] (ldw = K). */
+w4a4_status_t w8a8_pack_weight(const void* w, int32_t w_dtype, int64_t N, int64_t K,
+                               int8_t* wq, float* ws, void* stream);
+
+/*
+ * W8A8 GEMM:
+ *   P[m,n] = sum_k xq[m,k] * wq[n,k]    (exact: 128^2 K < 2^31)
+ *   Y[m,n] = fl32(fl32(P) * fl32(xs[m] * ws[n])) (+ bias[n]), as y_dtype
+ *
+ *   xq, wq   int8 [M][K], [N][K] (any code, -128 included), 16-byte aligned
+ *   xs, ws   f32 [M], [N];  bias  f32 [N] or NULL
+ *   M, N, K  M, N >= 0, < 2^31; K > 0, K % 16 == 0, K <= 131056
+ *   y        out: [M][ldy] fp32, fp16 or bf16, ldy >= N, aligned to its element
+ *   workspace  device memory of at least w8a8_gemm_workspace(M, N, K) bytes,
+ *            16-byte aligned, owned by the caller, overwritten; may be NULL
+ *            when that size is 0 (K split across workgroups where the tiles
+ *            alone leave the chip idle; int32 sums, so Y does not depend on
+ *            the split)
+ */
+w4a4_status_t w8a8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, const float* bias,
+                        int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                        void* y, int32_t y_dtype, int64_t ldy, void* stream);
+
+/* Workspace bytes w8a8_gemm needs, or -1 for invalid extents. Host-only. */
+int64_t w8a8_gemm_workspace(int64_t M, int64_t N, int64_t K);
 
 /*
  * ---- Storage conversions ------------------------------------------------

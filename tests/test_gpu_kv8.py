@@ -1,0 +1,539 @@
+"""The INT8 key/value cache and attention over it against their definitions.
+
+Codes, scales and read-back values are exact. Attention is compared with a
+64-bit softmax on the cached values, within a bound made of, per output,
+  A = sum_j p_j |v_j|                  (p the softmax weights)
+  S = max_j scale sum_d |q_d k_jd|     (what a score's sum runs through)
+  * the rounding of each weight to fp16: 2^-11 A
+  * a score's fp32 sum of D products and three more roundings moves its weight
+    by (D + 4) 2^-24 S, in numerator and denominator: 2 (D + 4) 2^-24 S A
+  * exp2 (2 ulp), the scale factors and the sums over L positions and the
+    joins of splits, numerator and denominator: 2 (L + 32) 2^-24 A
+  * weights under 2^-29 of the largest scale met, to 2^-40 of it: L 127 2^-40
+    times the largest scale
+  * the output's own rounding: 2^-11 |o| (fp16), 2^-8 (bf16).
+"""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+
+def ops():
+    from w4a4_quantized_gemm_quantize_amd import ops as o
+    return o
+
+
+class Batch:
+    """A pool with garbage in every page (NaN scales where no sequence is) and
+    ragged sequences: lens[b] cached positions, the last new[b] of them new."""
+
+    def __init__(self, new, lens, heads=2, dim=64, page=16, dtype="float16", seed=0, spare=3, tail=2, width=None):
+        import torch
+        self.new, self.lens, self.heads, self.dim, self.page = new, lens, heads, dim, page
+        self.dtype = getattr(torch, dtype)
+        g = self.g = torch.Generator(device="cuda").manual_seed(seed)
+        need = [-(-n // page) for n in lens]
+        pages = sum(need) + spare
+        perm = torch.randperm(pages, generator=g, device="cuda").int().cpu()
+        width = max(max(need, default=0), 1) if width is None else width
+        table = torch.full((len(lens), width), -7, dtype=torch.int32)
+        at = 0
+        for b, m in enumerate(need):
+            table[b, :m] = perm[at:at + m]
+            at += m
+        self.table_host, self.table = table, table.cuda()
+        self.kc = torch.randint(-127, 128, (pages, heads, page, dim), generator=g, device="cuda", dtype=torch.int8)
+        self.vc = torch.randint(-127, 128, (pages, heads, dim, page), generator=g, device="cuda", dtype=torch.int8)
+        self.ks = torch.rand(pages, heads, generator=g, device="cuda") * 0.02 + 0.002
+        self.vs = torch.exp(2 * torch.randn(pages, heads, generator=g, device="cuda")) * 0.01
+        self.ks[perm[at:].long().cuda()] = float("nan")
+        self.vs[perm[at:].long().cuda()] = float("nan")
+        cu = np.concatenate([[0], np.cumsum(new)])
+        self.cu_host = [int(c) for c in cu]
+        self.cu = torch.tensor(self.cu_host, dtype=torch.int32, device="cuda")
+        self.sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.total = self.cu_host[-1] + tail            # rows behind the last sequence
+        self.max_new, self.max_len = max(new, default=0), max(lens, default=0)
+
+    @property
+    def pool(self):
+        return self.kc, self.vc, self.ks, self.vs, self.table, self.cu, self.sl
+
+    def rand(self, heads, gain=1.0):
+        import torch
+        return (gain * torch.randn(self.total, heads, self.dim, generator=self.g, device="cuda")).to(self.dtype)
+
+    def values(self, b, real):
+        """K, V [heads, L, dim] of a sequence."""
+        n = self.lens[b]
+        pg = self.table[b, :-(-n // self.page)].long()
+        k = self.kc[pg].to(real) * self.ks[pg].to(real)[:, :, None, None]
+        v = self.vc[pg].to(real) * self.vs[pg].to(real)[:, :, None, None]
+        k = k.permute(1, 0, 2, 3).reshape(self.heads, -1, self.dim)[:, :n]
+        return k, v.permute(1, 0, 3, 2).reshape(self.heads, -1, self.dim)[:, :n]
+
+
+def attention_ref(B, q, causal, window, scale, hidden=None):
+    """(o, lse, bound of o without the output's rounding) in 64 bits; hidden:
+    {sequence: positions that count as masked}."""
+    import torch
+    hq = q.shape[1]
+    grp = hq // B.heads
+    o = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    bound = torch.zeros_like(o)
+    lse = torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device="cuda")
+    for b, (n, length) in enumerate(zip(B.new, B.lens)):
+        t0 = B.cu_host[b]
+        if n == 0 or length == 0:
+            continue
+        k, v = B.values(b, torch.float64)
+        key = torch.arange(length, device="cuda")[None, :]
+        pos = torch.arange(length - n, length, device="cuda")[:, None]
+        hide = torch.zeros((n, length), dtype=torch.bool, device="cuda")
+        if causal:
+            hide |= key > pos
+        if window:
+            hide |= key <= pos - window
+        for lo, hi in (hidden or {}).get(b, []):
+            hide |= (key >= lo) & (key < hi)
+        top = torch.nan_to_num(B.vs[B.table[b, :-(-length // B.page)].long()].double()).max()
+        k, v = torch.nan_to_num(k), torch.nan_to_num(v)
+        for h in range(hq):
+            qq = q[t0:t0 + n, h].double()
+            s = (qq @ k[h // grp].t() * scale).masked_fill(hide, -math.inf)
+            big = (qq.abs() @ k[h // grp].abs().t() * abs(scale)).masked_fill(hide, 0).amax(dim=1, keepdim=True)
+            seen = ~hide.all(dim=1)
+            p = torch.nan_to_num(torch.softmax(s, dim=1))
+            o[t0:t0 + n, h] = p @ v[h // grp]
+            lse[t0:t0 + n, h] = torch.where(seen, torch.logsumexp(s, dim=1), lse[t0:t0 + n, h])
+            a = p @ v[h // grp].abs()
+            rel = 2.0 ** -11 + 2 * (B.dim + 4) * 2.0 ** -24 * big + 2 * (length + 32) * 2.0 ** -24
+            bound[t0:t0 + n, h] = rel * a + length * 127 * 2.0 ** -40 * top
+    return o, lse, bound
+
+
+STEP = {"float32": 2.0 ** -24, "float16": 2.0 ** -11, "bfloat16": 2.0 ** -8}
+
+
+def check(B, heads, causal=True, window=0, out_dtype=None, scale=None, hidden=None, gain=2.0, q=None, **kw):
+    import torch
+    q = B.rand(heads, gain) if q is None else q
+    sc = B.dim ** -0.5 if scale is None else scale
+    y, lse = ops().kv8_attention(q, *B.pool, B.max_new, B.max_len, scale=scale, causal=causal, window=window,
+                                 out_dtype=out_dtype, return_lse=True, **kw)
+    o, l, bound = attention_ref(B, q, causal, window, sc, hidden)
+    t = B.cu_host[-1]
+    assert y.dtype == (out_dtype or q.dtype) and y.shape == q.shape
+    step = STEP[str(y.dtype).split(".")[1]]
+    err = (y.double() - o)[:t].abs()
+    bad = ~(err <= (bound + step * (o.abs() + bound) + 2.0 ** -25)[:t])
+    if y.dtype == torch.float16:
+        # past 65520, half way from the largest fp16 value to 2^16, the nearest fp16 value is an infinity
+        bad &= ~((o.abs() + bound >= 65520)[:t] & torch.isinf(y[:t]) & (torch.sign(y[:t]) == torch.sign(o[:t])))
+    assert not bool(bad.any()), (f"{int(bad.sum())} of {bad.numel()} out of tolerance, first "
+                                 f"{torch.nonzero(bad)[:4].tolist()}, worst {float(err.max()):.3g}")
+    l, got = l[:t], lse[:t].double()
+    assert torch.equal(torch.isinf(l), torch.isinf(got)), "rows that see nothing"
+    fin = ~torch.isinf(l)
+    # a score is off by (D + 4) 2^-24 S at most; |s| <= S
+    k_big = (q.double().abs().sum(-1).amax() * 127 * torch.nan_to_num(B.ks).max().double() * abs(sc))
+    tol = (B.dim + 4) * 2.0 ** -24 * k_big + (B.max_len + 32) * 2.0 ** -24 + l[fin].abs() * 2.0 ** -22
+    assert bool(((l[fin] - got[fin]).abs() <= tol).all())
+    return y
+
+
+# ------------------------------------------------------------------ storing
+
+def rne(x):
+    return np.rint(x).astype(np.float32)
+
+
+def store_ref(B, x, codes, scale):
+    """The definition on host copies; codes [pages, heads, page, dim]."""
+    f32 = np.float32
+    x = x.float().cpu().numpy()
+    P = B.page
+    for b, (n, length) in enumerate(zip(B.new, B.lens)):
+        p0, t0 = length - n, B.cu_host[b]
+        for j in range(max(p0, 0) // P, -(-length // P)):
+            pg = int(B.table_host[b, j])
+            if n == 0 or not 0 <= pg < codes.shape[0]:
+                continue
+            lo, hi = max(j * P, p0, 0), min(length, (j + 1) * P)
+            for h in range(B.heads):
+                rows = x[t0 + lo - p0:t0 + hi - p0, h]
+                old = lo - j * P
+                s = np.abs(rows).max().astype(f32) / f32(127)
+                if old > 0 and scale[pg, h] >= s:
+                    s = scale[pg, h]
+                elif old > 0:
+                    codes[pg, h, :old] = rne(codes[pg, h, :old].astype(f32) * (scale[pg, h] / s))
+                with np.errstate(divide="ignore", invalid="ignore"):
+                    codes[pg, h, old:hi - j * P] = rne(rows / s) if s > 0 else 0
+                scale[pg, h] = s
+
+
+def check_append(B, k, v):
+    import torch
+    kc, vc = B.kc.cpu().numpy().copy(), B.vc.transpose(2, 3).cpu().numpy().copy()
+    ks, vs = B.ks.cpu().numpy().copy(), B.vs.cpu().numpy().copy()
+    store_ref(B, k, kc, ks)
+    store_ref(B, v, vc, vs)
+    ops().kv8_append(k, v, *B.pool, B.max_new)
+    assert np.array_equal(B.ks.cpu().numpy(), ks, equal_nan=True), "key scales"
+    assert np.array_equal(B.vs.cpu().numpy(), vs, equal_nan=True), "value scales"
+    assert np.array_equal(B.kc.cpu().numpy(), kc), "key codes"
+    assert np.array_equal(B.vc.transpose(2, 3).cpu().numpy(), vc), "value codes"
+    del torch
+
+
+CASES = [  # new, lens, heads, dim, page
+    ([1], [1], 1, 64, 16),
+    ([1, 1, 1], [1, 17, 64], 2, 128, 16),
+    ([3, 0, 5], [3, 9, 40], 3, 64, 32),
+    ([70, 1, 33], [70, 130, 95], 2, 128, 64),
+    ([129, 4], [300, 4], 1, 192, 128),
+    ([20, 257], [50, 257], 2, 256, 256),
+    ([16, 15, 17, 31], [32, 31, 33, 47], 5, 64, 16),
+    ([5, 2], [3, 1], 2, 64, 16),                        # more new tokens than positions
+]
+
+
+@pytest.mark.parametrize("new,lens,heads,dim,page", CASES)
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_append_matches_definition(new, lens, heads, dim, page, dtype):
+    B = Batch(new, lens, heads, dim, page, dtype, seed=sum(lens))
+    check_append(B, B.rand(heads, 0.5), B.rand(heads, 0.05))
+
+
+def test_append_token_by_token_rescales():
+    """Decode steps with growing values: earlier codes are rescaled each time."""
+    import torch
+    B = Batch([1, 1], [1, 14], 2, 64, 16, seed=3)
+    for step in range(12):
+        gain = 2.0 ** (step - 4) if step % 3 else 0.01
+        check_append(B, B.rand(2, gain), B.rand(2, 0.3))
+        B.lens = [n + 1 for n in B.lens]
+        B.sl = torch.tensor(B.lens, dtype=torch.int32, device="cuda")
+        if B.lens[1] % 16 == 1:                         # the next page of sequence 1
+            B.table_host = torch.cat([B.table_host, torch.full((2, 1), -7, dtype=torch.int32)], dim=1)
+            B.table_host[1, 1] = int(torch.nonzero(torch.isnan(B.ks[:, 0]))[0])
+            B.table = B.table_host.cuda()
+        if B.lens[0] % 16 == 1:
+            break
+
+
+def test_append_zero_tokens_and_strided_views():
+    B = Batch([4, 20], [9, 33], 2, 64, 16, seed=4)
+    qkv = B.rand(8)
+    check_append(B, qkv[:, 4:6], qkv[:, 6:8])
+    B = Batch([4, 20], [9, 33], 2, 64, 16, seed=5)
+    zero = B.rand(2) * 0
+    check_append(B, zero, zero)
+
+
+def test_append_skips_bad_pages():
+    import torch
+    B = Batch([40, 3], [40, 50], 2, 64, 16, seed=6)
+    B.table_host[0, 1] = 1 << 30
+    B.table_host[1, 3] = -1
+    B.table = B.table_host.cuda()
+    check_append(B, B.rand(2), B.rand(2))
+    k, v = ops().kv8_gather(*B.pool, B.total, B.max_new)
+    assert bool((k[16:32] == 0).all()) and bool((v[16:32] == 0).all()) and bool((k[0:16] != 0).any())
+    assert bool((k[41:43] == 0).all()) and not bool(torch.isnan(k[:43]).any())
+
+
+@pytest.mark.parametrize("new,lens,heads,dim,page", CASES)
+@pytest.mark.parametrize("dtype", ["float32", "float16", "bfloat16"])
+def test_gather_reads_values(new, lens, heads, dim, page, dtype):
+    import torch
+    B = Batch(new, lens, heads, dim, page, seed=7)
+    dt = getattr(torch, dtype)
+    k = torch.full((B.total, heads, dim), 9.0, dtype=dt, device="cuda")
+    v = k.clone()
+    ops().kv8_gather(*B.pool, B.total, B.max_new, out=(k, v))
+    for b, (n, length) in enumerate(zip(new, lens)):
+        for got, real in zip((k, v), B.values(b, torch.float32)):
+            rows = got[B.cu_host[b]:B.cu_host[b + 1]]
+            miss = max(n - length, 0)
+            assert bool((rows[:miss] == 0).all())
+            assert torch.equal(rows[miss:], real[:, max(length - n, 0):].transpose(0, 1).to(dt))
+    assert bool((k[B.cu_host[-1]:] == 9).all()) and bool((v[B.cu_host[-1]:] == 9).all())
+
+
+# ---------------------------------------------------------------- attention
+
+@pytest.mark.parametrize("new,lens", [([1], [1]), ([1], [64]), ([1, 1, 1, 1], [65, 1, 700, 63]),
+                                      ([1, 0, 1], [257, 40, 0]), ([3, 1, 6], [40, 2000, 6]), ([17, 64], [17, 300]),
+                                      ([130, 0, 55], [130, 9, 413]), ([5, 2], [3, 1])])
+@pytest.mark.parametrize("heads,kv,dim,page", [(2, 2, 64, 16), (8, 1, 128, 64), (14, 2, 128, 32), (3, 3, 192, 128),
+                                               (10, 5, 256, 256), (16, 1, 64, 64), (40, 2, 128, 16)])
+def test_attention(new, lens, heads, kv, dim, page):
+    B = Batch(new, lens, kv, dim, page, "bfloat16" if dim % 128 else "float16", seed=len(lens) + heads)
+    check(B, heads)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 1), (True, 7), (True, 64), (True, 100), (False, 0), (False, 33),
+                                           (True, 100000)])
+@pytest.mark.parametrize("new,lens", [([1, 1], [130, 900]), ([5, 2], [600, 2]), ([150, 33], [400, 33])])
+def test_masks(causal, window, new, lens):
+    B = Batch(new, lens, 2, 128, 32, seed=window + 1)
+    check(B, 6, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("out", ["float32", "float16", "bfloat16"])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_types_and_scale(out, dtype):
+    import torch
+    for new, lens in (([1, 4], [90, 333]), ([140], [200])):
+        B = Batch(new, lens, 2, 128, 64, dtype, seed=11)
+        check(B, 8, out_dtype=getattr(torch, out), scale=0.03)
+
+
+@pytest.mark.parametrize("length,page,batch", [(20000, 64, 1), (20000, 16, 3), (70001, 128, 1)])
+def test_long_context_is_split(length, page, batch):
+    B = Batch([1] * batch, [length - 1000 * b for b in range(batch)], 2, 128, page, "bfloat16", seed=12)
+    check(B, 16)
+
+
+def test_sharp_and_flat_scores():
+    """One key that takes all the weight; equal scores; scores far below zero; large queries."""
+    import torch
+    for gain in (0.0, 300.0):
+        B = Batch([1, 150], [500, 300], 2, 128, 64, seed=13)
+        check(B, 4, gain=gain)
+        B = Batch([1, 150], [500, 300], 2, 128, 64, "bfloat16", seed=13)
+        check(B, 4, gain=gain)
+    # every key is -3 times the query: scores near -3000, none of them masked
+    B = Batch([1, 80], [200, 80], 1, 64, 16, seed=14)
+    B.kc.fill_(-100)
+    q = torch.full((B.total, 2, 64), 5.0, dtype=torch.float16, device="cuda")
+    check(B, 2, q=q, scale=1.0)
+
+
+def test_bf16_queries_of_any_size():
+    """A row's power of two: tiny, huge and mixed elements."""
+    import torch
+    for exp in (-120, -40, 0, 60):
+        B = Batch([1, 70], [300, 200], 1, 128, 64, "bfloat16", seed=15)
+        q = B.rand(2) * 2.0 ** exp
+        q[..., ::5] *= 2.0 ** -12
+        check(B, 2, q=q, scale=2.0 ** -exp * 0.1)
+    B = Batch([1, 70], [300, 200], 1, 128, 64, "bfloat16", seed=15)
+    check(B, 2, q=B.rand(2) * 0)
+    del torch
+
+
+def test_page_scales_far_apart():
+    """Values of pages whose scales differ by 2^20, and pages of zeros."""
+    for lens in ([640], [64, 65]):
+        B = Batch([1] * len(lens), lens, 1, 64, 64, seed=16)
+        B.vs[:] = 2.0 ** -10
+        B.vs[::3] = 2.0 ** 10
+        B.vs[1::4] = 0.0
+        B.vc[1::4] = 0
+        check(B, 4)
+        B = Batch([64 + 6] * len(lens), [n + 70 for n in lens], 1, 64, 64, seed=17)
+        B.vs[::3] *= 2.0 ** -20
+        B.ks[::5] = 0.0
+        check(B, 4)
+
+
+def test_bad_pages_are_masked():
+    for new in (1, 100):
+        B = Batch([new, new], [300, 130], 2, 64, 32, seed=18)
+        B.table_host[0, 2], B.table_host[0, 9], B.table_host[1, 0] = 1 << 29, -1, B.kc.shape[0]
+        B.table = B.table_host.cuda()
+        ref = Batch([new, new], [300, 130], 2, 64, 32, seed=18)     # the same pool, masked instead
+        q = B.rand(4)
+        y = ops().kv8_attention(q, *B.pool, B.max_new, B.max_len)
+        o, _, bound = attention_ref(ref, q, True, 0, 64 ** -0.5, {0: [(64, 96), (288, 300)], 1: [(0, 32)]})
+        t = B.cu_host[-1]
+        assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -10 * o.abs() + 2.0 ** -24)[:t]).all())
+
+
+def test_rows_of_no_sequence_are_left_alone():
+    import torch
+    for new, lens in (([1, 1], [30, 3000]), ([90, 40], [90, 400])):
+        B = Batch(new, lens, 2, 64, 16, seed=19, tail=5)
+        q = B.rand(4)
+        out = torch.full_like(q, 7.0)
+        ops().kv8_attention(q, *B.pool, B.max_new, B.max_len, out=out)
+        assert bool((out[B.cu_host[-1]:] == 7).all())
+        assert torch.equal(out[:B.cu_host[-1]],
+                           ops().kv8_attention(q, *B.pool, B.max_new, B.max_len)[:B.cu_host[-1]])
+
+
+def test_a_row_of_nan_stays_in_its_row():
+    import torch
+    for new in (3, 100):
+        B = Batch([new], [200], 1, 64, 16, seed=20)
+        q = B.rand(4)
+        clean = ops().kv8_attention(q, *B.pool, B.max_new, B.max_len)[:new]
+        q[1, 2] = float("nan")
+        y = ops().kv8_attention(q, *B.pool, B.max_new, B.max_len)[:new]
+        assert bool(torch.isnan(y[1, 2]).all())
+        keep = torch.ones(new, 4, dtype=torch.bool)
+        keep[1, 2] = False
+        assert torch.equal(y[keep.cuda()], clean[keep.cuda()])
+
+
+def test_strided_queries_and_host_bounds_that_are_loose():
+    import torch
+    B = Batch([1, 3], [333, 500], 2, 128, 64, seed=21)
+    qkv = B.rand(12)
+    y = ops().kv8_attention(qkv[:, :8], *B.pool, B.max_new, B.max_len)
+    assert torch.equal(y[:4], ops().kv8_attention(qkv[:, :8].contiguous(), *B.pool, B.max_new, B.max_len)[:4])
+    check(B, 8, q=qkv[:, 2:10])
+    B.max_new, B.max_len = 40, B.table.shape[1] * 64
+    check(B, 8, q=qkv[:, 2:10])
+
+
+def test_offsets_past_32_bits():
+    """Pages beyond 2^31 bytes of the caches."""
+    import torch
+    heads, page, dim = 8, 256, 256
+    pages = (1 << 31) // (heads * page * dim) + 40
+    kc = torch.empty((pages, heads, page, dim), dtype=torch.int8, device="cuda")
+    vc = torch.empty((pages, heads, dim, page), dtype=torch.int8, device="cuda")
+    B = Batch([2, 300], [500, 300], heads, dim, page, seed=22)
+    n = B.kc.shape[0]
+    kc[-n:], vc[-n:] = B.kc, B.vc
+    for name in ("ks", "vs"):
+        s = torch.full((pages, heads), float("nan"), device="cuda")
+        s[-n:] = getattr(B, name)
+        setattr(B, name, s)
+    B.kc, B.vc, B.table = kc, vc, torch.where(B.table >= 0, B.table + (pages - n), B.table)
+    k, v = B.rand(heads), B.rand(heads)
+    ops().kv8_append(k, v, *B.pool, B.max_new)
+    gk, gv = ops().kv8_gather(*B.pool, B.total, B.max_new)
+    t = B.cu_host[-1]
+    # half a step of the page's scale, and fp16's own half step. The page that held
+    # earlier positions keeps their scale where it is the larger one, so the
+    # step is that of the stored scales, not of the new tokens alone.
+    for x, got, s in ((k, gk, B.ks), (v, gv, B.vs)):
+        step = torch.nan_to_num(s).max()
+        assert bool(((x - got)[:t].float().abs() <= 0.51 * step + 2.0 ** -10 * x[:t].abs().float()).all())
+    check(B, 8)
+
+
+def test_captured_on_another_stream_and_workspaces():
+    import torch
+    o = ops()
+    for new, lens in (([1, 1], [5000, 700]), ([100, 20], [400, 20])):
+        B = Batch(new, lens, 2, 128, 64, seed=23)
+        q, k, v = B.rand(8), B.rand(2), B.rand(2)
+
+        def step():
+            o.kv8_append(k, v, *B.pool, B.max_new)
+            return o.kv8_attention(q, *B.pool, B.max_new, B.max_len)
+        y0 = step()
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            y1 = step()
+        torch.cuda.current_stream().wait_stream(side)
+        t = B.cu_host[-1]
+        assert torch.equal(y0[:t], y1[:t])
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y2 = step()
+        for i in range(3):
+            for x in (q, k, v):
+                x.copy_(B.rand(x.shape[1]))
+            # lengths are read at replay: the sequences shrink
+            B.sl.sub_(1)
+            B.lens = [n - 1 for n in B.lens]
+            graph.replay()
+            torch.cuda.synchronize()
+            got = y2.clone()
+            check(B, 8, q=q)
+            assert torch.equal(got[:t], o.kv8_attention(q, *B.pool, B.max_new, B.max_len)[:t]), f"replay {i}"
+        from w4a4_quantized_gemm_quantize_amd._lib import workspace_bytes
+        need = workspace_bytes("kv8_attention_workspace", 8, 2, 64, 128, len(new), B.total, B.max_new, B.max_len, 1, 0)
+        ws = torch.full((need + 64,), 255, dtype=torch.uint8, device="cuda")
+        assert torch.equal(o.kv8_attention(q, *B.pool, B.max_new, B.max_len, workspace=ws)[:t], got[:t])
+        assert bool((ws[need:] == 255).all())
+        if need:
+            with pytest.raises(ValueError):
+                o.kv8_attention(q, *B.pool, B.max_new, B.max_len, workspace=ws[:need - 1])
+
+
+def test_refusals():
+    import torch
+    o = ops()
+    B = Batch([2], [40], 2, 64, 16, seed=24)
+    q, k = B.rand(4), B.rand(2)
+    for args, exc in [((q[:, :3], B.max_new, B.max_len), ValueError), ((q[..., :32], B.max_new, B.max_len), ValueError),
+                      ((q, -1, B.max_len), ValueError), ((q, B.max_new, 1000), ValueError),
+                      ((q.float(), B.max_new, B.max_len), TypeError)]:
+        with pytest.raises(exc):
+            o.kv8_attention(args[0], *B.pool, *args[1:])
+    for kw, exc in [(dict(window=-1), ValueError), (dict(out=q[:, :2]), ValueError), (dict(out_dtype=torch.int8), TypeError),
+                    (dict(out=q.cpu()), ValueError)]:
+        with pytest.raises(exc):
+            o.kv8_attention(q, *B.pool, B.max_new, B.max_len, **kw)
+    with pytest.raises(ValueError):
+        o.kv8_append(k, k[:-1], *B.pool, B.max_new)
+    with pytest.raises(TypeError):
+        o.kv8_append(k, k.bfloat16(), *B.pool, B.max_new)
+    with pytest.raises(ValueError):
+        o.kv8_append(k, k, B.kc, B.vc.transpose(2, 3).contiguous(), *B.pool[2:], B.max_new)
+    with pytest.raises(TypeError):
+        o.kv8_append(k, k, *B.pool[:4], B.table.long(), *B.pool[5:], B.max_new)
+    with pytest.raises(ValueError):
+        o.kv8_append(k, k, *B.pool[:5], B.cu[:1], B.sl, B.max_new)
+    with pytest.raises(ValueError):
+        o.kv8_gather(*B.pool, B.total, B.max_new, out=(k, k[:-1]))
+
+
+def test_a_layer_as_it_is_used():
+    """Prefill, then decode steps of one attention layer: an 8-bit qkv projection,
+    the cache, attention, an 8-bit output projection; the cached keys and
+    values stay within what INT8 pages can hold of those projected, and the
+    last step's attention is that of the whole history."""
+    import torch
+    o = ops()
+    g = torch.Generator(device="cuda").manual_seed(25)
+    hidden, heads, kv, dim, page, batch = 512, 8, 2, 64, 16, 3
+    n = (heads + 2 * kv) * dim
+    wqkv = o.w8a8_pack_weight((0.05 * torch.randn(n, hidden, generator=g, device="cuda")).half())
+    wo = o.w8a8_pack_weight((0.05 * torch.randn(hidden, heads * dim, generator=g, device="cuda")).half())
+    pool = o.kv8_new_cache(32, kv, page, dim)
+    table = torch.randperm(32, generator=g, device="cuda")[:27].int().view(3, 9).contiguous()
+    lens, said_k, said_v = [0] * batch, [[] for _ in range(batch)], [[] for _ in range(batch)]
+    for new in ([40, 7, 100], [1, 1, 1], [1, 1, 1], [4, 0, 2]):
+        lens = [a + b for a, b in zip(lens, new)]
+        cu = [0, new[0], new[0] + new[1], sum(new)]
+        cu_d = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        x = torch.randn(cu[-1], hidden, generator=g, device="cuda").half()
+        qkv = o.w8a8_linear(x, *wqkv, out_dtype=torch.float16).view(-1, heads + 2 * kv, dim)
+        q, k, v = qkv[:, :heads], qkv[:, heads:heads + kv], qkv[:, heads + kv:]
+        o.kv8_append(k, v, *pool, table, cu_d, sl, max(new))
+        y = o.kv8_attention(q, *pool, table, cu_d, sl, max(new), max(lens))
+        h = o.w8a8_linear(y.view(-1, heads * dim), *wo, out_dtype=torch.float16)
+        assert h.shape == (cu[-1], hidden) and bool(torch.isfinite(h).all())
+        for b in range(batch):
+            said_k[b].append(k[cu[b]:cu[b + 1]])
+            said_v[b].append(v[cu[b]:cu[b + 1]])
+    for b in range(batch):
+        ks, vs = torch.cat(said_k[b]).float(), torch.cat(said_v[b]).float()
+        length = ks.shape[0]
+        cu1 = torch.tensor([0, length], dtype=torch.int32, device="cuda")
+        gk, gv = o.kv8_gather(*pool, table[b:b + 1], cu1, sl[b:b + 1], length, length, out_dtype=torch.float32)
+        # one rounding when stored, one more each time the page is rescaled (at most 3 appends after the first)
+        for x, got in ((ks, gk), (vs, gv)):
+            step = torch.stack([x[i // page * page:i // page * page + page].abs().amax(dim=(0, 2)) for i in range(length)])
+            assert bool(((x - got).abs() <= (2.0 + 2.0 ** -10) * step[:, :, None] / 127).all())
+        if new[b]:
+            s = torch.einsum("qhd,khd->hqk", q[cu[b]:cu[b + 1]].float(), gk.repeat_interleave(4, 1)) * dim ** -0.5
+            pos = torch.arange(length - new[b], length, device="cuda")[:, None]
+            s = s.masked_fill(torch.arange(length, device="cuda")[None] > pos, -math.inf)
+            ref = torch.einsum("hqk,khd->qhd", torch.softmax(s.double(), -1), gv.repeat_interleave(4, 1).double())
+            # fp16 weights and output, each 2^-11 of the largest value
+            assert bool(((y[cu[b]:cu[b + 1]].double() - ref).abs() <= 2.0 ** -9 * gv.abs().max()).all())

@@ -20,12 +20,17 @@ STATUS_NAMES = {
 }
 Y_F32 = 0
 Y_F16 = 1
+Y_BF16 = 2          # the 8-bit calls only
 
 _p = ctypes.c_void_p
 _i64 = ctypes.c_int64
 _i32 = ctypes.c_int32
+_f32 = ctypes.c_float
 
-# name -> argtypes, mirroring include/w4a4.h
+# the pool and batch arguments that the kv8 calls share
+_KV_BATCH = [_i64, _i32, _i32, _i32, _p, _i64, _p, _p, _i64, _i64, _i64, _i64]
+
+# name -> argtypes, mirroring include/w4a4.h and include/kv8.h
 SIGNATURES = {
     "w4a4_quantize_act": [_p, _i64, _i64, _i64, _i32, _p, _p, _p],
     "w4a4_pack_weight": [_p, _i64, _i64, _i32, _p, _p, _p],
@@ -60,6 +65,13 @@ SIGNATURES = {
     "mxfp4_scales_to_rows": [_p, _i64, _i64, _p, _p],
     "nvfp4_scales_to_panels": [_p, _i64, _i64, _p, _p],
     "nvfp4_scales_to_rows": [_p, _i64, _i64, _p, _p],
+    "w8a8_quantize_act": [_p, _i32, _i64, _i64, _i64, _p, _p, _p],
+    "w8a8_pack_weight": [_p, _i32, _i64, _i64, _p, _p, _p],
+    "w8a8_gemm": [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _i32, _i64, _p],
+    "kv8_append": [_p, _p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _p, *_KV_BATCH, _p],
+    "kv8_gather": [_p, _p, _p, _p, *_KV_BATCH, _p, _p, _i32, _p],
+    "kv8_attention": [_p, _i32, _i64, _i64, _i32, _p, _p, _p, _p, *_KV_BATCH, _f32, _i32, _i64, _p, _i64,
+                      _p, _i32, _p, _p],
 }
 
 
@@ -101,6 +113,10 @@ def load_library() -> ctypes.CDLL:
         lib.w4a4_probe_mfma_ops.restype = ctypes.c_int64
         lib.w4a4_gemm_splitk_noalloc_max_bytes.argtypes = []
         lib.w4a4_gemm_splitk_noalloc_max_bytes.restype = ctypes.c_int64
+        lib.w8a8_gemm_workspace.argtypes = [_i64, _i64, _i64]
+        lib.w8a8_gemm_workspace.restype = ctypes.c_int64
+        lib.kv8_attention_workspace.argtypes = [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i32, _i64]
+        lib.kv8_attention_workspace.restype = ctypes.c_int64
         _lib = lib
         return lib
 
@@ -110,6 +126,14 @@ def splitk_workspace_bytes(M: int, N: int, K: int, group_a: int, group_w: int, s
     n = load_library().w4a4_gemm_splitk_workspace(M, N, K, group_a, group_w, splits)
     if n < 0:
         raise W4A4Error("w4a4_gemm_splitk_workspace", 2, "invalid arguments")
+    return n
+
+
+def workspace_bytes(name: str, *args) -> int:
+    """The bytes a host-only workspace query returns; raises on invalid arguments."""
+    n = getattr(load_library(), name)(*args)
+    if n < 0:
+        raise W4A4Error(name, 2, "invalid arguments")
     return n
 
 

@@ -74,4 +74,60 @@ void launch_transpose_f32(const float* in, int64_t rows, int64_t cols, float* ou
 void launch_scale_panels(int fmt, bool to_panels, const uint8_t* in, int64_t rows, int64_t nb, uint8_t* out,
                          hipStream_t stream);
 
+// ---- 8-bit linear layers (w8a8.hip). bf16: x is bf16, else fp16.
+void launch_w8a8_quant(const void* x, int bf16, int64_t M, int64_t K, int64_t ldx, int8_t* q, float* s,
+                       hipStream_t stream);
+
+struct W8GemmArgs {
+  const int8_t* a;
+  const float* sa;
+  const int8_t* w;
+  const float* sw;
+  const float* bias;   // or nullptr
+  int64_t M, N, K;
+  void* y;
+  int ydtype;          // 0 fp32, 1 fp16, 2 bf16
+  int64_t ldy;
+};
+void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream);
+
+// ---- INT8 key/value cache (kv8_cache.hip, kv8_attention.hip)
+struct KvPool {
+  int8_t* k;           // [num_pages][heads][page][dim]
+  int8_t* v;           // [num_pages][heads][dim][page]
+  float* ks;           // [num_pages][heads]
+  float* vs;
+  int num_pages, heads, page, dim, log_page;
+};
+
+struct KvBatch {
+  const int32_t* table;   // [B][table_ld] pages of each sequence
+  int64_t table_ld;
+  const int32_t* cu;      // [B + 1] first token of each sequence in the packed tensors
+  const int32_t* lens;    // [B] positions in the cache, the new tokens included
+  int B, T, max_new, max_len;
+};
+
+struct KvNew {
+  const void* k;
+  const void* v;
+  int64_t k_tok, k_head, v_tok, v_head;   // strides in elements
+  int bf16;
+};
+void launch_kv8_append(const KvPool& c, const KvBatch& b, const KvNew& x, hipStream_t stream);
+void launch_kv8_gather(const KvPool& c, const KvBatch& b, void* k, void* v, int ydt, hipStream_t stream);
+
+struct KvQuery {
+  const void* q;
+  int64_t q_tok, q_head;                  // strides in elements
+  int bf16, heads;                        // query heads: a multiple of the cache's
+  float scale;
+  int causal, window;                     // window 0: none
+  void* y;                                // [T][heads][dim]
+  int ydtype;
+  float* lse;                             // [T][heads] or nullptr
+};
+int64_t kv8_attention_workspace(const KvPool& c, const KvBatch& b, const KvQuery& q);
+void launch_kv8_attention(const KvPool& c, const KvBatch& b, const KvQuery& q, void* workspace, hipStream_t stream);
+
 }  // namespace w4a4

@@ -6,9 +6,11 @@ here.
 """
 from __future__ import annotations
 
+import contextlib
+
 import torch
 
-from ._lib import Y_F16, Y_F32, call
+from ._lib import Y_BF16, Y_F16, Y_F32, call, workspace_bytes
 
 
 def _stream(t: torch.Tensor) -> int:
@@ -473,3 +475,286 @@ def nvfp4_scales_to_panels(s_rows: torch.Tensor):
 def nvfp4_scales_to_rows(s: torch.Tensor, rows: int, K: int):
     """Panel-layout E4M3 bytes (flat, rows*K/16) -> row-major [rows, K/16]."""
     return _panels("nvfp4_scales_to_rows", s, rows, K, 16, False)
+
+
+# ------------------------------------------------------- 8-bit linear layers
+
+_DTYPE8 = {torch.float32: Y_F32, torch.float16: Y_F16, torch.bfloat16: Y_BF16}
+
+
+def _x_dtype8(t, name: str) -> int:
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA (HIP) tensor")
+    if t.dtype not in (torch.float16, torch.bfloat16):
+        raise TypeError(f"{name} must be torch.float16 or torch.bfloat16, got {t.dtype}")
+    return _DTYPE8[t.dtype]
+
+
+def _y_dtype8(dtype) -> int:
+    if dtype not in _DTYPE8:
+        raise TypeError("output dtype must be torch.float32, torch.float16 or torch.bfloat16")
+    return _DTYPE8[dtype]
+
+
+def _same_device(first, **others) -> None:
+    for name, t in others.items():
+        if t is not None and t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+
+
+def _device_of(t):
+    """Makes t's device current for the launches, if it is not."""
+    if t.device.index == torch.cuda.current_device():
+        return contextlib.nullcontext()
+    return torch.cuda.device(t.device)
+
+
+def _rows_stride(x, name: str) -> int:
+    """Row stride of a 2-D tensor of contiguous rows (any stride for one row)."""
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{name} must be 2-D with unit column stride")
+    return x.stride(0) if x.shape[0] > 1 else max(x.shape[1], 1)
+
+
+def _workspace8(workspace, nbytes: int, device):
+    """(tensor or None, pointer, bytes): the caller's workspace, checked, or a new one."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, 0, 0
+        workspace = torch.empty((nbytes,), dtype=torch.uint8, device=device)
+    else:
+        if not isinstance(workspace, torch.Tensor) or workspace.device != device:
+            raise ValueError("workspace must be a tensor on the inputs' device")
+        if not workspace.is_contiguous():
+            raise ValueError("workspace must be contiguous")
+        if workspace.numel() * workspace.element_size() < nbytes:
+            raise ValueError(f"workspace must hold {nbytes} bytes")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _w8_quantize(fn: str, x, out, names):
+    dt = _x_dtype8(x, names[0])
+    ld = _rows_stride(x, names[0])
+    M, K = x.shape
+    if out is None:
+        q = torch.empty((M, K), dtype=torch.int8, device=x.device)
+        s = torch.empty((M,), dtype=torch.float32, device=x.device)
+    else:
+        q, s = out
+        _check_out(q, names[1], (M, K), torch.int8, x.device)
+        _check_out(s, names[2], (M,), torch.float32, x.device)
+    with _device_of(x):
+        call("w8a8_quantize_act", x.data_ptr(), dt, M, K, ld, q.data_ptr(), s.data_ptr(), _stream(x))
+    return q, s
+
+
+def w8a8_quantize_act(x: torch.Tensor, out=None):
+    """Symmetric INT8 quantization per token of fp16 or bf16 X[M, K] (row stride
+    may exceed K): ``(xq int8 [M, K], xs float32 [M])``, ``x ~ xq * xs``."""
+    return _w8_quantize("w8a8_quantize_act", x, out, ("x", "xq", "xs"))
+
+
+def w8a8_pack_weight(w: torch.Tensor, out=None):
+    """Offline INT8 quantization per output channel of fp16 or bf16 W[N, K]:
+    ``(wq int8 [N, K], ws float32 [N])``."""
+    return _w8_quantize("w8a8_pack_weight", w, out, ("w", "wq", "ws"))
+
+
+def w8a8_gemm(xq, xs, wq, ws, bias=None, out_dtype=torch.float32, out=None, workspace=None):
+    """Y[M, N] = (xq @ wq^T) scaled by xs[m] * ws[n], plus ``bias`` float32 [N].
+    The INT8 products are summed exactly. Y is fp32, fp16 or bf16; the
+    workspace (K split across workgroups for small outputs) is allocated here
+    with torch unless given."""
+    for t, dt, n in ((xq, torch.int8, "xq"), (wq, torch.int8, "wq"),
+                     (xs, torch.float32, "xs"), (ws, torch.float32, "ws")):
+        _need(t, dt, n)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    if xq.dim() != 2 or wq.dim() != 2:
+        raise ValueError("xq and wq must be 2-D")
+    M, K = xq.shape
+    N = wq.shape[0]
+    if wq.shape[1] != K:
+        raise ValueError("K of xq and wq differ")
+    if tuple(xs.shape) != (M,) or tuple(ws.shape) != (N,):
+        raise ValueError("xs and ws must hold one scale per row: shapes (M,) and (N,)")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if tuple(bias.shape) != (N,) or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous [N] tensor")
+    _same_device(xq, xs=xs, wq=wq, ws=ws, bias=bias)
+    if out is None:
+        _y_dtype8(out_dtype)
+        y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
+    else:
+        y = out
+        if isinstance(y, torch.Tensor):
+            _y_dtype8(y.dtype)
+        _check_out(y, "out", (M, N), getattr(y, "dtype", None), xq.device, row_stride_ok=True)
+    held, wptr, wbytes = _workspace8(workspace, workspace_bytes("w8a8_gemm_workspace", M, N, K), xq.device)
+    with _device_of(xq):
+        call("w8a8_gemm", xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+             0 if bias is None else bias.data_ptr(), M, N, K, wptr, wbytes, y.data_ptr(), _DTYPE8[y.dtype],
+             y.stride(0) if M > 1 else max(N, 1), _stream(xq))
+    del held
+    return y
+
+
+def w8a8_linear(x: torch.Tensor, wq, ws, bias=None, out_dtype=torch.float32, out=None, workspace=None):
+    """A W8A8 linear layer on fp16 or bf16 activations: X quantized per token
+    here, then :func:`w8a8_gemm`."""
+    xq, xs = w8a8_quantize_act(x)
+    return w8a8_gemm(xq, xs, wq, ws, bias=bias, out_dtype=out_dtype, out=out, workspace=workspace)
+
+
+# ------------------------------------------------------ INT8 key/value cache
+
+def kv8_new_cache(num_pages: int, heads: int, page: int, dim: int, device="cuda"):
+    """An empty pool for :func:`kv8_append`: ``(k_cache int8 [num_pages, heads,
+    page, dim], v_cache int8 [num_pages, heads, dim, page], k_scale, v_scale
+    float32 [num_pages, heads])``, all zero. ``page``: positions per page (16,
+    32, 64, 128 or 256); ``dim``: 64, 128, 192 or 256."""
+    if page not in (16, 32, 64, 128, 256) or dim not in (64, 128, 192, 256):
+        raise ValueError("page must be 16, 32, 64, 128 or 256 and dim 64, 128, 192 or 256")
+    return (torch.zeros((num_pages, heads, page, dim), dtype=torch.int8, device=device),
+            torch.zeros((num_pages, heads, dim, page), dtype=torch.int8, device=device),
+            torch.zeros((num_pages, heads), dtype=torch.float32, device=device),
+            torch.zeros((num_pages, heads), dtype=torch.float32, device=device))
+
+
+def _kv_pool(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens):
+    """Checked pool and batch: (pool pointers, pool extents, batch pointers, B)."""
+    for t, dt, n in ((k_cache, torch.int8, "k_cache"), (v_cache, torch.int8, "v_cache"),
+                     (k_scale, torch.float32, "k_scale"), (v_scale, torch.float32, "v_scale"),
+                     (block_table, torch.int32, "block_table"), (cu_seqlens, torch.int32, "cu_seqlens"),
+                     (seq_lens, torch.int32, "seq_lens")):
+        _need(t, dt, n)
+        if not t.is_contiguous():
+            raise ValueError(f"{n} must be contiguous")
+    _same_device(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
+                 cu_seqlens=cu_seqlens, seq_lens=seq_lens)
+    if k_cache.dim() != 4:
+        raise ValueError("k_cache must be [num_pages, heads, page, dim]")
+    pages, heads, page, dim = k_cache.shape
+    if tuple(v_cache.shape) != (pages, heads, dim, page):
+        raise ValueError("v_cache must be [num_pages, heads, dim, page]")
+    if tuple(k_scale.shape) != (pages, heads) or tuple(v_scale.shape) != (pages, heads):
+        raise ValueError("k_scale and v_scale must be [num_pages, heads]")
+    if seq_lens.dim() != 1 or tuple(cu_seqlens.shape) != (seq_lens.shape[0] + 1,):
+        raise ValueError("cu_seqlens must be [B + 1] for seq_lens [B]")
+    B = seq_lens.shape[0]
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be [B, pages per sequence]")
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()), \
+        (pages, heads, page, dim), (block_table.data_ptr(), block_table.shape[1], cu_seqlens.data_ptr(),
+                                    seq_lens.data_ptr()), B
+
+
+def _need_max(value, name: str) -> int:
+    if isinstance(value, bool) or not isinstance(value, int) or value < 0:
+        raise ValueError(f"{name} must be a non-negative int")
+    return value
+
+
+def _heads_strides(t, name: str, heads: int, dim: int):
+    """(token stride, head stride) of a [T, heads, dim] tensor of contiguous rows."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [T, {heads}, {dim}]")
+    if t.stride(2) != 1 and t.numel():
+        raise ValueError(f"{name} must have a unit stride along its last dimension")
+    return (t.stride(0) if t.shape[0] > 1 else heads * dim), (t.stride(1) if heads > 1 else dim)
+
+
+def kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens, max_new: int):
+    """Quantize the new keys and values (fp16 or bf16 [T, heads, dim], strided
+    views allowed) into the pages of the cache, in place.
+
+    Sequence b's new tokens are rows ``cu_seqlens[b] .. cu_seqlens[b+1] - 1``, and
+    the last positions of its ``seq_lens[b]`` (new tokens included). A page keeps
+    one scale per head: it grows when a new token needs it, and the codes
+    already there are rescaled. Everything but ``max_new`` (at least the largest
+    number of new tokens of a sequence) is read on the device."""
+    ptrs, (pages, heads, page, dim), batch, B = _kv_pool(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                         cu_seqlens, seq_lens)
+    dt = _x_dtype8(k, "k")
+    _need(v, k.dtype, "v")
+    _same_device(k_cache, k=k, v=v)
+    kt, kh = _heads_strides(k, "k", heads, dim)
+    vt, vh = _heads_strides(v, "v", heads, dim)
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k and v hold different numbers of tokens")
+    with _device_of(k_cache):
+        call("kv8_append", k.data_ptr(), v.data_ptr(), dt, kt, kh, vt, vh, *ptrs, pages, heads, page, dim, *batch,
+             B, k.shape[0], _need_max(max_new, "max_new"), batch[1] * page, _stream(k_cache))
+
+
+def kv8_gather(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens, total: int, max_new: int,
+               out_dtype=torch.float16, out=None):
+    """The cached keys and values as numbers: ``(k, v)`` of ``out_dtype``, each
+    [total, heads, dim], rows ``cu_seqlens[b] .. cu_seqlens[b+1] - 1`` holding the last
+    positions of sequence b (the mirror of :func:`kv8_append`). ``out``: a pair
+    of contiguous tensors to fill instead; rows of no sequence are left alone."""
+    ptrs, (pages, heads, page, dim), batch, B = _kv_pool(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                         cu_seqlens, seq_lens)
+    shape = (_need_max(total, "total"), heads, dim)
+    if out is None:
+        _y_dtype8(out_dtype)
+        k, v = (torch.empty(shape, dtype=out_dtype, device=k_cache.device) for _ in range(2))
+    else:
+        k, v = out
+        if isinstance(k, torch.Tensor):
+            _y_dtype8(k.dtype)
+        _check_out(k, "k", shape, getattr(k, "dtype", None), k_cache.device)
+        _check_out(v, "v", shape, k.dtype, k_cache.device)
+    with _device_of(k_cache):
+        call("kv8_gather", *ptrs, pages, heads, page, dim, *batch, B, total, _need_max(max_new, "max_new"),
+             batch[1] * page, k.data_ptr(), v.data_ptr(), _DTYPE8[k.dtype], _stream(k_cache))
+    return k, v
+
+
+def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens, max_new: int,
+                  max_len: int, scale: float | None = None, causal: bool = True, window: int = 0, out_dtype=None,
+                  out=None, return_lse: bool = False, workspace=None):
+    """Attention of the new tokens' queries (fp16 or bf16 [T, q_heads, dim],
+    strided views allowed) over the cache that already holds their keys and
+    values: one new token per sequence (decoding), a few (drafts) or many
+    (prefill), in any mix.
+
+    ``max_new`` / ``max_len``: at least every sequence's new tokens / cached
+    positions (host numbers that size the launch; the true ones are read on the
+    device). ``scale`` defaults to dim ** -0.5; ``window`` w > 0 hides the keys w
+    and more positions back. Returns [T, q_heads, dim] of ``out_dtype`` (default:
+    q's), with ``return_lse`` also float32 [T, q_heads] (natural log). A query that
+    sees no key gives zeros and -inf; rows of no sequence are left alone. The
+    workspace is allocated here with torch unless given."""
+    ptrs, (pages, heads, page, dim), batch, B = _kv_pool(k_cache, v_cache, k_scale, v_scale, block_table,
+                                                         cu_seqlens, seq_lens)
+    dt = _x_dtype8(q, "q")
+    _same_device(k_cache, q=q)
+    if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % heads:
+        raise ValueError(f"q must be [T, q_heads, {dim}] with q_heads a multiple of {heads}")
+    T, hq = q.shape[:2]
+    qt, qh = _heads_strides(q, "q", hq, dim)
+    if isinstance(window, bool) or not isinstance(window, int) or window < 0:
+        raise ValueError("window must be a non-negative int (0: none)")
+    _need_max(max_new, "max_new")
+    if _need_max(max_len, "max_len") > batch[1] * page:
+        raise ValueError(f"max_len {max_len} is past the block table's {batch[1]} pages of {page}")
+    if out is None:
+        _y_dtype8(out_dtype or q.dtype)
+        y = torch.empty((T, hq, dim), dtype=out_dtype or q.dtype, device=q.device)
+    else:
+        y = out
+        if isinstance(y, torch.Tensor):
+            _y_dtype8(y.dtype)
+        _check_out(y, "out", (T, hq, dim), getattr(y, "dtype", None), q.device)
+    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device) if return_lse else None
+    nbytes = workspace_bytes("kv8_attention_workspace", hq, heads, page, dim, B, T, max_new, max_len, int(causal),
+                             window)
+    held, wptr, wbytes = _workspace8(workspace, nbytes, q.device)
+    with _device_of(q):
+        call("kv8_attention", q.data_ptr(), dt, qt, qh, hq, *ptrs, pages, heads, page, dim, *batch, B, T, max_new,
+             max_len, dim ** -0.5 if scale is None else scale, int(causal), window, wptr, wbytes, y.data_ptr(),
+             _DTYPE8[y.dtype], 0 if lse is None else lse.data_ptr(), _stream(q))
+    del held
+    return (y, lse) if return_lse else y
