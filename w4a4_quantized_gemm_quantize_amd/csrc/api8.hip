@@ -110,7 +110,7 @@ w4a4_status_t w8a8_pack_weight(const void* w, int32_t w_dtype, int64_t N, int64_
 int64_t w8a8_gemm_workspace(int64_t M, int64_t N, int64_t K) {
   if (!w8_extents_ok(M, N, K)) return -1;
   if (M == 0 || N == 0) return 0;
-  return 0;
+  return w4a4::w8a8_workspace(M, N, K);
 }
 
 w4a4_status_t w8a8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, const float* bias,
@@ -131,7 +131,7 @@ w4a4_status_t w8a8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, con
   w4a4::W8GemmArgs g = {};
   g.a = xq; g.sa = xs; g.w = wq; g.sw = ws; g.bias = bias;
   g.M = M; g.N = N; g.K = K;
-  g.y = y; g.ydtype = y_dtype; g.ldy = ldy;
+  g.y = y; g.ydtype = y_dtype; g.ldy = ldy; g.workspace = workspace;
   w4a4::launch_w8a8_gemm(g, as_stream(stream));
   return launched();
 }

@@ -88,7 +88,9 @@ struct W8GemmArgs {
   void* y;
   int ydtype;          // 0 fp32, 1 fp16, 2 bf16
   int64_t ldy;
+  void* workspace;     // w8a8_workspace(M, N, K) bytes
 };
+int64_t w8a8_workspace(int64_t M, int64_t N, int64_t K);
 void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream);
 
 // ---- INT8 key/value cache (kv8_cache.hip, kv8_attention.hip)

@@ -21,6 +21,7 @@ namespace {
 typedef int v16i __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
+constexpr int kCUs = 256;      // of an MI355X: launch shapes are planned for it
 
 // The fp32 value of the low / high 16-bit half of w.
 template <bool BF>
@@ -158,6 +159,9 @@ struct W8Params {
   void* y;
   int ydtype;
   int64_t ldy;
+  int32_t* part;              // [splits][M][N] int32 sums, or nullptr
+  int splits;                 // K ranges
+  int stages;                 // 128-k stages per range
 };
 
 // Y value of an exact sum, and its store as ydt (0 fp32, 1 fp16, 2 bf16).
@@ -173,48 +177,44 @@ __device__ __forceinline__ void store_y(void* y, int ydt, int64_t i, float v) {
   else static_cast<uint16_t*>(y)[i] = bf16_rne(v);
 }
 
-// ---- Few tokens: W streamed once from HBM straight into the operands --------
-// A workgroup of NW waves owns 16 MT rows x 16 TN columns and splits K across
-// its waves (contiguous runs of 64-k steps). v_mfma_i32_16x16x64_i8: lane l
-// supplies 16 consecutive k of row l % 16 at k offset 16 (l / 16), so a step is
-// one 16-byte load per operand and lane, with no LDS on the way; RING steps
-// are in flight per wave. The waves' int32 sums meet in LDS (exact in any
-// order). K is a multiple of 16: the last step's lanes beyond K read zeros.
-template <int MT, int TN, int NW, int RING>
+// ---- Up to 16 tokens: W streamed once from HBM straight into the operands -----
+// A workgroup of NW waves owns 16 TN columns and splits K across its waves
+// (contiguous runs of 64-k steps). v_mfma_i32_16x16x64_i8: lane l supplies 16
+// consecutive k of row l % 16 at k offset 16 (l / 16), so a step is one 16-byte
+// load per operand and lane, with no LDS on the way; RING steps are in flight
+// per wave. The waves' int32 sums meet in LDS (exact in any order). K is a
+// multiple of 16: the last step's lanes beyond K read zeros.
+// Bound by the W stream, and with many tokens by the L2 traffic of their codes,
+// which every workgroup reads again (M / (16 TN) of W's bytes): see launch.
+template <int TN, int NW, int RING>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
-  __shared__ int red[NW > 1 ? NW - 1 : 1][MT * TN * 4][64];
+  __shared__ int red[NW - 1][TN * 4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16 * TN, m0 = (int)blockIdx.y * 16 * MT;
-  const int64_t K = p.K;
+  const int n0 = (int)blockIdx.x * 16 * TN;
   const int steps = (p.K + 63) >> 6;
   const int h0 = (int)((int64_t)steps * wave / NW), h1 = (int)((int64_t)steps * (wave + 1) / NW);
-  const int a_rows = min(16 * MT, p.M - m0), w_rows = min(16 * TN, p.N - n0);
-  const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a + m0 * K, a_rows * p.K);
-  const __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w + n0 * K, w_rows * p.K);
-  int offA[MT], offW[TN];
-#pragma unroll
-  for (int i = 0; i < MT; ++i) offA[i] = 16 * i + c < a_rows ? (16 * i + c) * p.K + 16 * g : kDroppedOffset;
+  const int w_rows = min(16 * TN, p.N - n0);
+  const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, p.M * p.K);
+  const __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w + (int64_t)n0 * p.K, w_rows * p.K);
+  const int offA = c < p.M ? c * p.K + 16 * g : kDroppedOffset;
+  int offW[TN];
 #pragma unroll
   for (int j = 0; j < TN; ++j) offW[j] = 16 * j + c < w_rows ? (16 * j + c) * p.K + 16 * g : kDroppedOffset;
   struct Step {
-    v4i a[MT], w[TN];
+    v4i a, w[TN];
   };
   auto load = [&](Step& st, int h) {
-    const bool in = 64 * h + 16 * g < p.K;
+    const int out = 64 * h + 16 * g < p.K ? 0 : kDroppedOffset;
 #pragma unroll
     for (int j = 0; j < TN; ++j)
-      st.w[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, in ? offW[j] : kDroppedOffset, 64 * h, 0));
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-      st.a[i] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, in ? offA[i] : kDroppedOffset, 64 * h, 0));
+      st.w[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, offW[j] | out, 64 * h, 0));
+    st.a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, offA | out, 64 * h, 0));
   };
-  v4i acc[MT][TN];
+  v4i acc[TN];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j) acc[i][j] = v4i{0, 0, 0, 0};
+  for (int j = 0; j < TN; ++j) acc[j] = v4i{0, 0, 0, 0};
   Step ring[RING];
 #pragma unroll
   for (int u = 0; u < RING; ++u)
@@ -224,49 +224,445 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
     for (int u = 0; u < RING; ++u) {
       if (h + u < h1) {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int j = 0; j < TN; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ring[u].a[i], ring[u].w[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < TN; ++j)
+          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ring[u].a, ring[u].w[j], acc[j], 0, 0, 0);
         if (h + u + RING < h1) load(ring[u], h + u + RING);
       }
     }
   }
-  if constexpr (NW > 1) {
-    if (wave > 0) {
+  if (wave > 0) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int j = 0; j < TN; ++j)
 #pragma unroll
-        for (int j = 0; j < TN; ++j)
+      for (int r = 0; r < 4; ++r) red[wave - 1][j * 4 + r][lane] = acc[j][r];
+  }
+  __syncthreads();
+  if (wave != 0) return;
 #pragma unroll
-          for (int r = 0; r < 4; ++r) red[wave - 1][(i * TN + j) * 4 + r][lane] = acc[i][j][r];
+  for (int j = 0; j < TN; ++j) {
+    const int n = n0 + 16 * j + c;
+    const float sw = n < p.N ? p.sw[n] : 0.0f;
+    const float b = p.bias && n < p.N ? p.bias[n] : 0.0f;
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      int v = acc[j][r];
+#pragma unroll
+      for (int w = 0; w < NW - 1; ++w) v += red[w][j * 4 + r][lane];
+      const int m = 4 * g + r;
+      if (m < p.M && n < p.N) store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, p.sa[m], sw, b));
     }
-    __syncthreads();
   }
-  // one (row tile, column tile) pair per wave, in turn
-  const int base = wave;
-  if constexpr (NW > 1) {
-    if (wave != 0) return;
+}
+
+// ---- Tiles ------------------------------------------------------------------
+typedef __attribute__((address_space(3))) void* lds_vptr;
+
+// Direct buffer -> LDS copy: lane l's 16 bytes land at lds + 16 l.
+__device__ __forceinline__ void dma16(__amdgpu_buffer_rsrc_t r, int voff, int soff, uint8_t* lds) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_vptr)lds, 16, voff, soff, 0, 0);
+}
+
+// s_waitcnt on vmcnt only (expcnt/lgkmcnt left at their maxima), gfx9 encoding.
+template <int N>
+__device__ __forceinline__ void wait_vmcnt() {
+  static_assert(N >= 0 && N < 64, "vmcnt range");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+
+// The raster: logical tile t of nblk (consecutive tiles on one XCD, which is
+// workgroup index mod 8, so its L2 holds the rows they share), in groups of
+// kGroupRows tile rows.
+constexpr int kGroupRows = 4;
+
+// What a tile's sums become: fp32, fp16 or bf16 (p.ydtype says which), or the
+// int32 sums of one K range for k_w8a8_join.
+enum { OUT_F32 = 0, OUT_16 = 1, OUT_RAW = 2 };
+
+// Workgroup tile BM tokens x BN channels, waves in a WM x WN grid of TI x TJ
+// blocks of v_mfma_i32_32x32x32_i8 (lane l: 16 consecutive k of row l % 32 at k
+// offset 16 (l / 32)). K stages of 128 bytes per row in an S-deep LDS ring
+// filled by direct loads; a row's eight 16-byte slots are XOR-swizzled with
+// (row >> 1) & 7, so 16 lanes reading one slot of 16 consecutive rows hit 16
+// distinct bank groups. The channels are the instruction's first operand: a
+// lane then holds runs of 4 consecutive channels of one token. 16-bit outputs
+// swap runs between the wave's halves and are stored 16 bytes per lane as well.
+//
+// Each workgroup takes logical tiles b, b + G, b + 2 G, ... (G workgroups). The
+// next tile's first S stages are issued before a tile's outputs are stored, so
+// the stores drain under the next tile's matrix work. WIDE: rows of y take
+// 16-byte stores (N, ldy and y aligned); else element stores, one tile per
+// workgroup.
+template <int BM, int BN, int WM, int WN, int S, int OUT, bool WIDE>
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(WM * WN / 4, WM * WN / 4)))
+void k_w8a8_gemm_tiles(W8Params p) {
+  constexpr int RB = 128;                              // bytes (k) per row and stage
+  constexpr int NWAVE = WM * WN;
+  constexpr int TI = BM / WM / 32, TJ = BN / WN / 32;
+  constexpr int NA = BM / 8 / NWAVE, NW = BN / 8 / NWAVE;   // 1 KB loads per wave and stage
+  constexpr int W_OFF = BM * RB, STAGE = (BM + BN) * RB;
+  constexpr int PER_STAGE = NA + NW;
+  constexpr int NSTEP = RB / 32;
+  constexpr int LPM = (PER_STAGE + TI * TJ - 1) / (TI * TJ);   // direct loads per matrix instruction
+  constexpr int NST = TI * TJ * (OUT == OUT_16 ? 2 : 4);       // stores per wave and tile
+  static_assert(NA * 8 * NWAVE == BM && NW * 8 * NWAVE == BN, "tile rows per wave");
+  __shared__ __align__(16) uint8_t sm0[STAGE];
+  __shared__ __align__(16) uint8_t sm1[STAGE];
+  __shared__ __align__(16) uint8_t sm2[S == 3 ? STAGE : 16];
+  __shared__ __align__(16) float sas[BM], sws[BN], biases[BN];
+  static_assert(BM <= 64 * NWAVE && BN <= 64 * NWAVE, "one row per thread");
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const int l32 = lane & 31, lhi = lane >> 5;
+  const int tiles_m = (p.M + BM - 1) / BM, tiles_n = (p.N + BN - 1) / BN;
+  const int tiles = tiles_m * tiles_n, nblk = tiles * p.splits;
+  const int G = gridDim.x;
+  // consecutive logical tiles on one XCD (workgroup index mod 8)
+  const int xcd = blockIdx.x & 7;
+  int t = xcd * (G >> 3) + min(xcd, G & 7) + (blockIdx.x >> 3);
+
+  // A lane's 16-byte slot of a row is the same in all its loads (their rows
+  // differ by multiples of 8 NWAVE).
+  static_assert(NWAVE % 2 == 0, "slot of a lane");
+  const int seg = 16 * ((lane & 7) ^ ((4 * wave + (lane >> 4)) & 7));
+  int part, tile_m, tile_n, kspan, nk;
+  __amdgpu_buffer_rsrc_t rA, rW;
+  int voffA[NA], voffW[NW];
+  float sa_t, sw_t, bias_t;
+  auto setup = [&](int tt) {
+    part = tt / tiles;
+    tt -= part * tiles;
+    const int grp = tt / (kGroupRows * tiles_n);
+    const int first_m = grp * kGroupRows, gsize = min(tiles_m - first_m, kGroupRows);
+    const int rem = tt - grp * kGroupRows * tiles_n;
+    tile_m = (first_m + rem % gsize) * BM;
+    tile_n = rem / gsize * BN;
+    const int a_rows = min(BM, p.M - tile_m), w_rows = min(BN, p.N - tile_n);
+    rA = buffer_rsrc(p.a + (int64_t)tile_m * p.K, a_rows * p.K);
+    rW = buffer_rsrc(p.w + (int64_t)tile_n * p.K, w_rows * p.K);
+    // The range's stages, rounded up to a multiple of the ring depth: what lies
+    // beyond K is read as zeros (tokens) or as anything (channels).
+    const int k0 = part * p.stages * RB;
+    kspan = min(p.K - k0, p.stages * RB);
+    nk = (kspan + S * RB - 1) / (S * RB) * S;
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      voffA[i] = min(8 * (wave + NWAVE * i) + (lane >> 3), a_rows - 1) * p.K + seg + k0;
+#pragma unroll
+    for (int i = 0; i < NW; ++i)
+      voffW[i] = min(8 * (wave + NWAVE * i) + (lane >> 3), w_rows - 1) * p.K + seg + k0;
+    // the tile's scales and bias, used in its output
+    if constexpr (OUT != OUT_RAW) {
+      const int m = tile_m + (int)threadIdx.x, n = tile_n + (int)threadIdx.x;
+      sa_t = p.sa[min(m, p.M - 1)];
+      sw_t = p.sw[min(n, p.N - 1)];
+      bias_t = p.bias ? p.bias[min(n, p.N - 1)] : 0.0f;
+    }
+  };
+// One of the PER_STAGE direct loads of stage KT into slot SM; OUTK holds the
+// sign bit where the lane's slot of the stage lies beyond K (see
+// kDroppedOffset), else 0.
+#define OUT_OF(KT) (seg >= kspan - (KT) * RB ? kDroppedOffset : 0)
+#define ISSUE1(KT, SM, X, OUTK)                                                                             \
+  {                                                                                                         \
+    if ((X) < NA) dma16(rA, voffA[(X) < NA ? (X) : 0] | (OUTK), (KT) * RB, (SM) + (wave + NWAVE * (X)) * 1024); \
+    else dma16(rW, voffW[(X) < NA ? 0 : (X) - NA], (KT) * RB, (SM) + W_OFF + (wave + NWAVE * ((X) - NA)) * 1024); \
   }
-  (void)base;
+#define ISSUE(KT, SM)                                                                                       \
+  {                                                                                                         \
+    const int out_ = OUT_OF(KT);                                                                            \
+    _Pragma("unroll") for (int x_ = 0; x_ < PER_STAGE; ++x_) ISSUE1(KT, SM, x_, out_)                       \
+  }
+  v16i acc[TI][TJ];
+#define CLEAR()                                                                                             \
+  _Pragma("unroll") for (int i = 0; i < TI; ++i)                                                            \
+  _Pragma("unroll") for (int j = 0; j < TJ; ++j)                                                            \
+  _Pragma("unroll") for (int r = 0; r < 16; ++r) acc[i][j][r] = 0;
+
+  const int rowA = wm * (BM / WM) + l32, rowW = wn * (BN / WN) + l32;
+  int offA[NSTEP], offW[NSTEP];
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+  for (int u = 0; u < NSTEP; ++u) {
+    offA[u] = rowA * RB + 16 * ((2 * u + lhi) ^ ((rowA >> 1) & 7));
+    offW[u] = W_OFF + rowW * RB + 16 * ((2 * u + lhi) ^ ((rowW >> 1) & 7));
+  }
+  v4i av[2][TI], wv[2][TJ];
+// Operand read X of step U (the TI blocks of tokens, then the TJ of channels).
+#define LOAD1(SM, U, B, X)                                                                                  \
+  {                                                                                                         \
+    if ((X) < TI) av[B][(X) < TI ? (X) : 0] = *reinterpret_cast<const v4i*>((SM) + offA[U] + 32 * RB * (X)); \
+    else wv[B][(X) < TI ? 0 : (X) - TI] = *reinterpret_cast<const v4i*>((SM) + offW[U] + 32 * RB * ((X) - TI)); \
+  }
+#define LOAD_OPS(SM, U, B) \
+  _Pragma("unroll") for (int x_ = 0; x_ < TI + TJ; ++x_) LOAD1(SM, U, B, x_)
+// Barrier between stages: each wave has waited for its own direct loads of the
+// stage, and every wave has finished with the slot about to be refilled. No
+// memory fence, which would drain the loads in flight.
+#define STAGE_BARRIER()                                                                                     \
+  {                                                                                                         \
+    __builtin_amdgcn_sched_barrier(0);                                                                      \
+    __builtin_amdgcn_s_barrier();                                                                           \
+    __builtin_amdgcn_sched_barrier(0);                                                                      \
+  }
+// Stage KT in slot CUR, its first step's operands in registers. Behind each
+// matrix instruction goes one operand read of the next step and, in the last
+// step, one direct load of the slot's refill: a wave issues in order, and a
+// burst of loads in front of the matrix work would stall it. Before the last
+// step's matrix work the stage's slot is read out: there the waves meet and go
+// on to the next stage's (slot NXT) first operands, so neither the barrier nor
+// those reads leave the matrix cores idle. LEFT: the stages behind the next
+// one that may still be in flight then.
+#define STAGE_OF(KT, CUR, NXT, MORE, REFILL, LEFT)                                                          \
+  {                                                                                                         \
+    int out_ = 0;                                                                                           \
+    _Pragma("unroll") for (int u_ = 0; u_ < NSTEP; ++u_) {                                                  \
+      if (u_ + 1 == NSTEP && (MORE)) {                                                                      \
+        __builtin_amdgcn_s_waitcnt(0xC07F); /* lgkmcnt(0): this wave has read the slot out */               \
+        wait_vmcnt<(LEFT) * PER_STAGE>();                                                                   \
+        STAGE_BARRIER();                                                                                    \
+        if (REFILL) out_ = OUT_OF((KT) + S);                                                                \
+      }                                                                                                     \
+      _Pragma("unroll") for (int x_ = 0; x_ < TI * TJ; ++x_) {                                              \
+        acc[x_ / TJ][x_ % TJ] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[u_ & 1][x_ % TJ], av[u_ & 1][x_ / TJ], \
+                                                                      acc[x_ / TJ][x_ % TJ], 0, 0, 0);      \
+        if (u_ + 1 < NSTEP) {                                                                               \
+          if (x_ < TI + TJ) LOAD1(CUR, (u_ + 1) % NSTEP, (u_ + 1) & 1, x_);                                 \
+        } else if (MORE) {                                                                                  \
+          if (x_ < TI + TJ) LOAD1(NXT, 0, 0, x_);                                                           \
+          _Pragma("unroll") for (int y_ = x_ * LPM; y_ < x_ * LPM + LPM; ++y_)                              \
+            if (y_ < PER_STAGE && (REFILL)) ISSUE1((KT) + S, CUR, y_, out_);                                \
+        }                                                                                                   \
+        __builtin_amdgcn_sched_barrier(0);                                                                  \
+      }                                                                                                     \
+    }                                                                                                       \
+  }
+  static_assert(TI + TJ <= TI * TJ, "one operand read per matrix instruction");
+  static_assert(NSTEP % 2 == 0, "operand buffers alternate across stages");
+// A tile's first S stages into the ring, which every wave has finished with.
+#define FILL_RING()                                                                                         \
+  {                                                                                                         \
+    ISSUE(0, sm0);                                                                                          \
+    ISSUE(1, sm1);                                                                                          \
+    if constexpr (S == 3) ISSUE(2, sm2);                                                                    \
+  }
+// All of a tile's matrix work, its first stage in the ring. The loop holds no
+// condition around a load or a wait, so the compiler's own waits on the direct
+// loads count exactly as the ones written here.
+#define TILE()                                                                                              \
+  {                                                                                                         \
+    LOAD_OPS(sm0, 0, 0);                                                                                    \
+    if constexpr (S == 2) {                                                                                 \
+      for (int kt = 0; kt + 2 < nk; kt += 2) {                                                              \
+        STAGE_OF(kt, sm0, sm1, true, true, 0)                                                               \
+        STAGE_OF(kt + 1, sm1, sm0, true, true, 0)                                                           \
+      }                                                                                                     \
+      STAGE_OF(nk - 2, sm0, sm1, true, false, 0)                                                            \
+      STAGE_OF(nk - 1, sm1, sm0, false, false, 0)                                                           \
+    } else {                                                                                                \
+      for (int kt = 0; kt + 3 < nk; kt += 3) {                                                              \
+        STAGE_OF(kt, sm0, sm1, true, true, 1)                                                               \
+        STAGE_OF(kt + 1, sm1, sm2, true, true, 1)                                                           \
+        STAGE_OF(kt + 2, sm2, sm0, true, true, 1)                                                           \
+      }                                                                                                     \
+      STAGE_OF(nk - 3, sm0, sm1, true, false, 1)                                                            \
+      STAGE_OF(nk - 2, sm1, sm2, true, false, 0)                                                            \
+      STAGE_OF(nk - 1, sm2, sm0, false, false, 0)                                                           \
+    }                                                                                                       \
+  }
+
+  // Output of the tile at (m0, n0) of K range pt.
+  const int esz = OUT == OUT_16 ? 2 : 4;
+  auto store_tile = [&](int m0, int n0, int pt) {
+    uint8_t* y = OUT == OUT_RAW ? reinterpret_cast<uint8_t*>(p.part + (int64_t)pt * p.M * p.N)
+                                : static_cast<uint8_t*>(p.y);
+    const int64_t ldy = OUT == OUT_RAW ? p.N : p.ldy;
+    // WIDE: y's rows of this tile as one buffer (< 2^31 bytes, checked by the
+    // host); a lane outside M x N gets an offset past it
+    const int ldb = WIDE ? (int)(ldy * esz) : 0;
+    const __amdgpu_buffer_rsrc_t rY = buffer_rsrc(y + (int64_t)m0 * ldy * esz, WIDE ? min(BM, p.M - m0) * ldb : 0);
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      const int n = n0 + 16 * j + c;
-      const float sw = n < p.N ? p.sw[n] : 0.0f;
-      const float b = p.bias && n < p.N ? p.bias[n] : 0.0f;
+    for (int i = 0; i < TI; ++i) {
+      const int row = wm * (BM / WM) + 32 * i + l32;
+      const float sa = OUT == OUT_RAW ? 0.0f : sas[row];
 #pragma unroll
-      for (int r = 0; r < 4; ++r) {
-        int v = acc[i][j][r];
-        if constexpr (NW > 1) {
+      for (int j = 0; j < TJ; ++j) {
+        const int c0 = wn * (BN / WN) + 32 * j + 4 * lhi;      // channel of register 0
+        uint32_t h[4][2];                                      // 16-bit pairs
 #pragma unroll
-          for (int w = 0; w < NW - 1; ++w) v += red[w][(i * TN + j) * 4 + r][lane];
+        for (int q = 0; q < 4; ++q) {
+          v4u w;
+          if constexpr (OUT == OUT_RAW) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = (uint32_t)acc[i][j][4 * q + e];
+          } else {
+            const v4f sw = *reinterpret_cast<const v4f*>(sws + c0 + 8 * q);
+            const v4f bv = *reinterpret_cast<const v4f*>(biases + c0 + 8 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) w[e] = __float_as_uint(scaled(acc[i][j][4 * q + e], sa, sw[e], bv[e]));
+          }
+          if constexpr (!WIDE) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int n = n0 + c0 + 8 * q + e;
+              if (m0 + row < p.M && n < p.N)
+                store_y(y, OUT == OUT_16 ? p.ydtype : 0, (m0 + row) * ldy + n, __uint_as_float(w[e]));
+            }
+          } else if constexpr (OUT == OUT_16) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float f0 = __uint_as_float(w[2 * e]), f1 = __uint_as_float(w[2 * e + 1]);
+              const uint32_t f16 = __half_as_ushort(__float2half_rn(f0)) | (uint32_t)__half_as_ushort(__float2half_rn(f1)) << 16;
+              const uint32_t b16 = bf16_rne(f0) | (uint32_t)bf16_rne(f1) << 16;
+              h[q][e] = p.ydtype == 1 ? f16 : b16;
+            }
+          } else {
+            const int n = n0 + c0 + 8 * q;
+            __builtin_amdgcn_raw_buffer_store_b128(w, rY, n < p.N ? row * ldb + n * 4 : kDroppedOffset, 0, 0);
+          }
         }
-        const int m = m0 + 16 * i + 4 * g + r;
-        if (m < p.M && n < p.N) store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, p.sa[m], sw, b));
+        if constexpr (WIDE && OUT == OUT_16) {
+          // runs q (even) and q + 1: the low half of the wave takes channels
+          // 8 q .. 8 q + 7, the high half 8 q + 8 .. 8 q + 15
+#pragma unroll
+          for (int q = 0; q < 4; q += 2) {
+            const auto s0 = __builtin_amdgcn_permlane32_swap(h[q][0], h[q + 1][0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(h[q][1], h[q + 1][1], false, false);
+            const int n = n0 + wn * (BN / WN) + 32 * j + 8 * q + 8 * lhi;
+            __builtin_amdgcn_raw_buffer_store_b128(v4u{s0[0], s1[0], s0[1], s1[1]}, rY,
+                                                   n < p.N ? row * ldb + n * 2 : kDroppedOffset, 0, 0);
+          }
+        }
       }
     }
+  };
+// The tile's scales into LDS, where its output reads them: every wave is past
+// the last tile's output (it met the others in this tile's stages).
+#define SCALES_TO_LDS()                                                                                     \
+  if constexpr (OUT != OUT_RAW) {                                                                           \
+    if (threadIdx.x < BM) sas[threadIdx.x] = sa_t;                                                          \
+    if (threadIdx.x < BN) sws[threadIdx.x] = sw_t, biases[threadIdx.x] = bias_t;                            \
+  }                                                                                                         \
+  __syncthreads();
+
+  setup(t);
+  FILL_RING()
+  wait_vmcnt<(S - 1) * PER_STAGE>();
+  STAGE_BARRIER();
+  if constexpr (WIDE) {
+    const int count = (nblk - t + G - 1) / G;
+    for (int it = 1; it < count; ++it) {
+      CLEAR()
+      TILE()
+      SCALES_TO_LDS()                                  // and the ring is free
+      const int m0 = tile_m, n0 = tile_n, pt = part;
+      t += G;
+      setup(t);
+      FILL_RING()
+      store_tile(m0, n0, pt);
+      // stage 0 is in: at most the later stages and the stores behind it are out
+      // (memory operations complete in order; every store above is issued)
+      wait_vmcnt<((S - 1) * PER_STAGE + NST < 63 ? (S - 1) * PER_STAGE + NST : 63)>();
+      STAGE_BARRIER();
+    }
+  }
+  CLEAR()
+  TILE()
+  SCALES_TO_LDS()
+  store_tile(tile_m, tile_n, part);
+#undef SCALES_TO_LDS
+#undef TILE
+#undef FILL_RING
+#undef STAGE_OF
+#undef STAGE_BARRIER
+#undef LOAD_OPS
+#undef LOAD1
+#undef CLEAR
+#undef ISSUE
+#undef ISSUE1
+#undef OUT_OF
+}
+
+// Adds the K splits' int32 sums and scales them.
+__global__ __launch_bounds__(kThreads) void k_w8a8_join(W8Params p, int splits) {
+  const int64_t total = (int64_t)p.M * p.N;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    int v = 0;
+    for (int s = 0; s < splits; ++s) v += p.part[s * total + i];
+    const int64_t m = i / p.N;
+    const int n = (int)(i - m * p.N);
+    store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, p.sa[m], p.sw[n], p.bias ? p.bias[n] : 0.0f));
+  }
+}
+
+// splits > 1: only for tiles whose OUT_RAW form is built (SPLIT).
+template <int BM, int BN, int WM, int WN, int S, bool SPLIT>
+void launch_tiles(W8Params p, int splits, hipStream_t stream) {
+  const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+  const int nk = (p.K + 127) / 128;
+  p.stages = (nk + splits - 1) / splits;
+  p.splits = splits = (nk + p.stages - 1) / p.stages;
+  const int64_t blocks = tiles * splits;
+  const dim3 grid((unsigned)std::min<int64_t>(blocks, kCUs)), block(64 * WM * WN);
+  const int64_t ldb = (splits > 1 ? p.N : p.ldy) * (splits > 1 || p.ydtype == 0 ? 4 : 2);
+  const int cols = splits > 1 || p.ydtype == 0 ? 4 : 8;
+  const bool wide = p.N % cols == 0 && ldb % 16 == 0 && BM * ldb < (int64_t{1} << 31) &&
+                    (reinterpret_cast<uintptr_t>(splits > 1 ? static_cast<void*>(p.part) : p.y) & 15) == 0;
+  const dim3 each((unsigned)blocks);                   // the element-store form: one tile per workgroup
+#define W8A8_TILES(OUT)                                                                                         \
+  if (wide) hipLaunchKernelGGL((k_w8a8_gemm_tiles<BM, BN, WM, WN, S, OUT, true>), grid, block, 0, stream, p);   \
+  else hipLaunchKernelGGL((k_w8a8_gemm_tiles<BM, BN, WM, WN, S, OUT, false>), each, block, 0, stream, p)
+  if constexpr (SPLIT) {
+    if (splits > 1) {
+      W8A8_TILES(OUT_RAW);
+      const int64_t jb = std::min<int64_t>(((int64_t)p.M * p.N + kThreads - 1) / kThreads, 8192);
+      hipLaunchKernelGGL(k_w8a8_join, dim3((unsigned)jb), dim3(kThreads), 0, stream, p, splits);
+      return;
+    }
+  }
+  if (p.ydtype == 0) {
+    W8A8_TILES(OUT_F32);
+  } else {
+    W8A8_TILES(OUT_16);
+  }
+#undef W8A8_TILES
+}
+
+// Which kernel, and into how many K ranges.
+//
+// Up to 16 tokens the W stream decides (k_w8a8_gemm_small). Above, the tile
+// whose estimated time is least: rounds of tiles over the CUs times (stages x
+// the tile's time per 128-k stage + its start and output). The times (us) are
+// measured ones: 256 x 256 tiles 1.15 a stage with every CU busy (4096 x 4096
+// x 8192 119 us), 256 x 128 0.8 (2048 x 4096 x 11008: 88 us; 256 x 256 tiles
+// 114, 128 x 128 105), 128 x 128 0.5 (512 x 8192 x 8192: 39 us; 45 and 74 with
+// the larger ones). 128 x 128 tiles may also split K, which costs a launch and
+// 8 bytes per output and range through the caches (64 x 8192 x 8192: 28.6 us
+// whole, 19.6 in four ranges; 256 x 8192 x 8192: 31.0 whole, 32.4 in two).
+enum { TILE_SMALL = 0, TILE_256 = 1, TILE_256_128 = 2, TILE_128 = 3 };
+struct W8Plan {
+  int tile, splits;
+};
+W8Plan plan_w8a8(int64_t M, int64_t N, int64_t K) {
+  if (M <= 16) return W8Plan{TILE_SMALL, 1};
+  const int64_t nk = (K + 127) / 128;
+  W8Plan best{TILE_256, 1};
+  double best_us = 1e30;
+  auto consider = [&](int tile, int64_t bm, int64_t bn, double stage, double start, int splits) {
+    const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
+    const int64_t rounds = (tiles * splits + kCUs - 1) / kCUs;
+    double us = rounds * (((nk + splits - 1) / splits) * stage + start);
+    if (splits > 1) us += 4.0 + 8.0 * splits * M * N / 2.5e6;
+    if (us < best_us) {
+      best_us = us;
+      best = W8Plan{tile, splits};
+    }
+  };
+  consider(TILE_256, 256, 256, 1.15, 3.0, 1);
+  consider(TILE_256_128, 256, 128, 0.8, 2.5, 1);
+  for (int splits = 1; splits <= 16 && splits * 2 <= nk; splits *= 2)
+    consider(TILE_128, 128, 128, 0.5, 2.0, splits);
+  return best;
 }
 
 }  // namespace
@@ -291,9 +687,36 @@ void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream) {
   p.y = a.y;
   p.ydtype = a.ydtype;
   p.ldy = a.ldy;
-  constexpr int MT = 1, TN = 1, NW = 8, RING = 4;
-  const dim3 grid((unsigned)((a.N + 16 * TN - 1) / (16 * TN)), (unsigned)((a.M + 16 * MT - 1) / (16 * MT)));
-  hipLaunchKernelGGL((k_w8a8_gemm_small<MT, TN, NW, RING>), grid, dim3(64 * NW), 0, stream, p);
+  p.part = nullptr;
+  p.splits = 1;
+  p.stages = 0;
+  const W8Plan pl = plan_w8a8(a.M, a.N, a.K);
+  switch (pl.tile) {
+    case TILE_SMALL: {
+      // More columns per workgroup cut the tokens' L2 traffic and leave fewer
+      // workgroups. 16 x 8192 x 28672 (us): TN = 1 53.6, 2 41.9, 4 67.3; 16 x
+      // 28672 x 8192: 52.2, 55.8, 44.0; one token 4096 -> 11008: 9.3, 10.9, 12.8.
+#define W8A8_SMALL(TN, NW, RING)                                                                           \
+  hipLaunchKernelGGL((k_w8a8_gemm_small<TN, NW, RING>), dim3((unsigned)((a.N + 16 * TN - 1) / (16 * TN))), \
+                     dim3(64 * NW), 0, stream, p)
+      if (a.M > 4 && a.N >= 16384) W8A8_SMALL(4, 4, 2);
+      else if (a.M > 4 && a.N >= 8192) W8A8_SMALL(2, 8, 4);
+      else W8A8_SMALL(1, 8, 4);
+#undef W8A8_SMALL
+      return;
+    }
+    case TILE_256: launch_tiles<256, 256, 2, 4, 2, false>(p, 1, stream); return;
+    case TILE_256_128: launch_tiles<256, 128, 4, 2, 3, false>(p, 1, stream); return;
+    default:
+      if (pl.splits > 1) p.part = static_cast<int32_t*>(a.workspace);
+      launch_tiles<128, 128, 2, 2, 3, true>(p, pl.splits, stream);
+      return;
+  }
+}
+
+int64_t w8a8_workspace(int64_t M, int64_t N, int64_t K) {
+  const W8Plan pl = plan_w8a8(M, N, K);
+  return pl.splits > 1 ? (int64_t)pl.splits * M * N * 4 : 0;
 }
 
 }  // namespace w4a4
