@@ -55,10 +55,60 @@ struct AttnParams {
   KvBatch b;
   KvQuery q;
   int group;             // query heads per kv head
+  int tile_rows;         // query rows per workgroup
   int split;             // positions per split (a multiple of 64 times the waves)
   float* part;           // splits' results: [splits][T heads][dim] then [splits][T heads][2]
   int64_t part_rows;     // T heads
 };
+
+typedef float v16f __attribute__((ext_vector_type(16)));
+
+// One query row of D elements over LANES-strided owners: qf[i] holds elements
+// dim(i) .. dim(i) + 7. bf16 rows are scaled by a power of two, returned as the
+// factor that undoes it. XOR: the lane distances over which the row's other
+// elements lie (16 and 32, or 32 alone). A negative softmax scale is moved into
+// the queries (flip), so that every factor of a score is >= 0.
+template <int N, int FIRST_XOR, typename Dim>
+__device__ __forceinline__ float load_query(const uint16_t* qp, bool bf16, bool flip, Dim dim, v8h (&qf)[N]) {
+  uint4 raw[N];
+#pragma unroll
+  for (int i = 0; i < N; ++i) raw[i] = *reinterpret_cast<const uint4*>(qp + dim(i));
+  const uint32_t sign = flip ? 0x80008000u : 0u;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    raw[i].x ^= sign;
+    raw[i].y ^= sign;
+    raw[i].z ^= sign;
+    raw[i].w ^= sign;
+  }
+  if (!bf16) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) qf[i] = __builtin_bit_cast(v8h, raw[i]);
+    return 1.0f;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) m = max(m, max((w[k] & 0x7FFFu) << 16, w[k] & 0x7FFF0000u));
+  }
+#pragma unroll
+  for (int x = FIRST_XOR; x < 64; x *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, x));
+  // exponent of the largest element to 14; a row of zeros and subnormals stays as it is
+  const int e = (int)(m >> 23), up = min(max(127 + 14 + 127 - e, 1), 254);
+  const float mul = e == 0 ? 1.0f : __uint_as_float((uint32_t)up << 23);
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      qf[i][2 * k] = (_Float16)(__uint_as_float(w[k] << 16) * mul);
+      qf[i][2 * k + 1] = (_Float16)(__uint_as_float(w[k] & 0xFFFF0000u) * mul);
+    }
+  }
+  return 1.0f / mul;
+}
 
 // Positions a tile of query rows [r0, r1) of a sequence can see: [lo, hi), lo a
 // multiple of 64.
@@ -101,49 +151,11 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
   const int pos = s.len - s.n + tok;
   const int row_hi = p.q.causal ? min(s.len, pos + 1) : s.len;
   const int row_lo = p.q.window > 0 ? max(0, pos - p.q.window + 1) : 0;
-  v8h qf[DB][2];
-  float qscale = p.q.scale * kLog2e;
-  {
-    const uint16_t* qp = static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head;
-    uint4 raw[DB][2];
-#pragma unroll
-    for (int d = 0; d < DB; ++d)
-#pragma unroll
-      for (int u = 0; u < 2; ++u) raw[d][u] = *reinterpret_cast<const uint4*>(qp + 64 * d + 16 * g + 8 * u);
-    if (!p.q.bf16) {
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) qf[d][u] = __builtin_bit_cast(v8h, raw[d][u]);
-    } else {
-      uint32_t m = 0;
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t w[4] = {raw[d][u].x, raw[d][u].y, raw[d][u].z, raw[d][u].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) m = max(m, max((w[i] & 0x7FFFu) << 16, w[i] & 0x7FFF0000u));
-        }
-      m = max(m, (uint32_t)__shfl_xor((int)m, 16));
-      m = max(m, (uint32_t)__shfl_xor((int)m, 32));
-      // exponent of the largest element to 14; a row of zeros and subnormals stays as it is
-      const int e = (int)(m >> 23), up = min(max(127 + 14 + 127 - e, 1), 254);
-      const float mul = e == 0 ? 1.0f : __uint_as_float((uint32_t)up << 23);
-      qscale = qscale / mul;
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-#pragma unroll
-        for (int u = 0; u < 2; ++u) {
-          const uint32_t w[4] = {raw[d][u].x, raw[d][u].y, raw[d][u].z, raw[d][u].w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            qf[d][u][2 * i] = (_Float16)(__uint_as_float(w[i] << 16) * mul);
-            qf[d][u][2 * i + 1] = (_Float16)(__uint_as_float(w[i] & 0xFFFF0000u) * mul);
-          }
-        }
-    }
-  }
+  v8h qf[2 * DB];
+  const float qscale =
+      fabsf(p.q.scale) * kLog2e *
+      load_query<2 * DB, 16>(static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head,
+                             p.q.bf16, p.q.scale < 0.0f, [&](int i) { return 64 * (i >> 1) + 16 * g + 8 * (i & 1); }, qf);
 
   const int P = p.c.page;
   v4f acc[DT];
@@ -177,8 +189,8 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
       sc[t] = v4f{0, 0, 0, 0};
 #pragma unroll
       for (int d = 0; d < DB; ++d) {
-        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(kr[t][d].x, kr[t][d].y), qf[d][0], sc[t], 0, 0, 0);
-        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(kr[t][d].z, kr[t][d].w), qf[d][1], sc[t], 0, 0, 0);
+        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(kr[t][d].x, kr[t][d].y), qf[2 * d], sc[t], 0, 0, 0);
+        sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(kr[t][d].z, kr[t][d].w), qf[2 * d + 1], sc[t], 0, 0, 0);
       }
     }
     const float f = ks * qscale;
@@ -263,6 +275,275 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
   }
 }
 
+// Many query rows per kv head: a workgroup of NW waves takes 32 NW / DS rows of
+// one kv head and walks over its split of the positions in tiles of 64. The
+// tile's codes are loaded 16 per thread and piece one tile ahead, widened to
+// fp16 once for all waves and kept in two LDS buffers. A wave owns 32 rows; with
+// DS = 2 (wide heads, whose accumulators and queries exceed a wave's 256
+// registers) two waves share them, each with the scores and half of O.
+//
+// S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_f16: row rho of a
+// 32-position tile of the first product is position rho with bits 2 and 3
+// swapped, so registers 8 v .. 8 v + 7 of lane half hi are the scores of
+// positions 16 v + 8 hi .. + 7 of query row lane % 32: the k indices of that
+// lane in the second product. A page (>= 16 positions) is uniform over such
+// a block of 16, so its scales are scalars: p_j vs_j comes out of one exp2 with
+// log2 of the scale in its addend, and the sum of a block's p_j is that of its
+// weights over the scale.
+//
+// LDS rows of K (2 D bytes) and V^T (128 bytes) keep their 16-byte slots
+// XOR-swizzled so that 16 consecutive rows hit distinct bank groups.
+template <int D, int NW, int DS>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4)))
+void k_kv8_prefill(AttnParams p) {
+  constexpr int ST = D / 16, DT = D / 32 / DS;         // k steps of S, the wave's 32-dimension tiles of O
+  constexpr int ROWS = 32 * NW / DS;
+  constexpr int TW = D > 192 ? 32 : 64, NB = TW / 16;  // positions per tile; the widest heads have no registers for 64
+  constexpr int PIECES = TW * D / 16;                  // 16-code pieces of K (or V) per tile
+  constexpr int KB = TW * D * 2;                       // bytes of a K (or V) buffer
+  constexpr int NP = 2 * PIECES / (64 * NW);           // pieces per thread and tile
+  static_assert(NP * 64 * NW == 2 * PIECES && PIECES % 64 == 0, "whole waves load K or V");
+  __shared__ __align__(16) uint8_t lk[2][KB];
+  __shared__ __align__(16) uint8_t lv[2][KB];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int l32 = lane & 31, hi = lane >> 5;
+  const int seq = blockIdx.z;
+  const int ntile = gridDim.x / p.c.heads;
+  // late rows see the most positions: they start first
+  const int h = blockIdx.x % p.c.heads, tile = ntile - 1 - blockIdx.x / p.c.heads;
+  const Seq s = sequence(p.b, seq);
+  const int rows = s.n * p.group;
+  const int r0 = tile * ROWS;
+  if (r0 >= rows) return;
+  const Range rg = tile_range(p, s, r0, min(r0 + ROWS, rows));
+  const int nsplit = max(1, (rg.hi - rg.lo + p.split - 1) / p.split);
+  if ((int)blockIdx.y >= nsplit) return;
+  const int from = rg.lo + blockIdx.y * p.split, to = min(rg.hi, from + p.split);
+
+  // this lane's query row, and the positions its wave's rows see
+  const int wr0 = r0 + 32 * (wave % (NW / DS)), d0 = wave / (NW / DS) * (D / DS);
+  const int r = min(wr0 + l32, rows - 1);
+  const int tok = r / p.group, hq = h * p.group + r % p.group;
+  auto row_hi = [&](int tk) { return p.q.causal ? min(s.len, s.len - s.n + tk + 1) : s.len; };
+  auto row_lo = [&](int tk) { return p.q.window > 0 ? max(0, s.len - s.n + tk - p.q.window + 1) : 0; };
+  const int my_hi = row_hi(tok), my_lo = row_lo(tok);
+  const int tok_a = __builtin_amdgcn_readfirstlane(min(wr0, rows - 1) / p.group);
+  const int tok_b = __builtin_amdgcn_readfirstlane(min(wr0 + 31, rows - 1) / p.group);
+  const int hi_min = row_hi(tok_a), hi_max = row_hi(tok_b), lo_min = row_lo(tok_a), lo_max = row_lo(tok_b);
+  v8h qf[ST];
+  const float qscale =
+      fabsf(p.q.scale) * kLog2e *
+      load_query<ST, 32>(static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head,
+                         p.q.bf16, p.q.scale < 0.0f, [&](int i) { return 16 * i + 8 * hi; }, qf);
+
+  const int P = p.c.page;
+  // piece i of this thread: K codes 16 (x % (D / 16)) .. of position x / (D /
+  // 16), or V codes of positions 16 (x % NB) .. of dimension x / NB
+  auto is_k = [&](int i) { return i * 64 * NW + tid < PIECES; };
+  auto x_of = [&](int i) { return (i * 64 * NW + tid) % PIECES; };
+  auto pos_of = [&](int i, int at) { return at + (is_k(i) ? x_of(i) / (D / 16) : 16 * (x_of(i) % NB)); };
+  int pg[NP], pgs;                                     // pages of the next tile: pieces, blocks of 16
+  auto load_pages = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) pg[i] = pos_of(i, at) < to ? page_of(p.b, p.c, seq, pos_of(i, at)) : -1;
+    pgs = at + 16 * (lane % NB) < to ? page_of(p.b, p.c, seq, at + 16 * (lane % NB)) : -1;
+  };
+  uint4 code[NP];
+  float ksv, vsv;                                      // of block lane % NB
+  int gone;                                            // that block's page is none
+  auto load_codes = [&](int at) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const int64_t base = ((int64_t)max(pg[i], 0) * p.c.heads + h) * P * D;
+      const int in = pos_of(i, at) & (P - 1), x = x_of(i);
+      code[i] = is_k(i) ? *reinterpret_cast<const uint4*>(p.c.k + base + in * D + x % (D / 16) * 16)
+                        : *reinterpret_cast<const uint4*>(p.c.v + base + x / NB * P + in);
+    }
+    gone = pgs < 0;
+    ksv = gone ? 0.0f : p.c.ks[(int64_t)pgs * p.c.heads + h];
+    vsv = gone ? 0.0f : p.c.vs[(int64_t)pgs * p.c.heads + h];
+  };
+  auto k_slot = [&](int row, int slot) {               // byte offset in a K buffer
+    return row * 2 * D + 16 * (slot ^ (D % 128 == 0 ? row & 15 : (row >> 1) & 7));
+  };
+  auto v_slot = [&](int row, int slot) {               // in a V buffer
+    return row * 2 * TW + 16 * (slot ^ (TW == 64 ? (row >> 1) & 7 : (row >> 2) & 3));
+  };
+  auto write_codes = [&](uint8_t* bk, uint8_t* bv) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const v8h a = widen8(code[i].x, code[i].y), b = widen8(code[i].z, code[i].w);
+      const int x = x_of(i);
+      if (is_k(i)) {
+        const int row = x / (D / 16), c = 2 * (x % (D / 16));
+        *reinterpret_cast<v8h*>(bk + k_slot(row, c)) = a;
+        *reinterpret_cast<v8h*>(bk + k_slot(row, c + 1)) = b;
+      } else {
+        const int row = x / NB, c = 2 * (x % NB);
+        *reinterpret_cast<v8h*>(bv + v_slot(row, c)) = a;
+        *reinterpret_cast<v8h*>(bv + v_slot(row, c + 1)) = b;
+      }
+    }
+  };
+
+  v16f acc[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[i][k] = 0.0f;
+  float m = kNone, l = 0.0f, vref = kTinyScale;
+  const int krow = (l32 & 0x13) | (l32 & 4) << 1 | (l32 & 8) >> 1;
+
+  load_pages(from);
+  load_codes(from);
+  load_pages(from + TW);
+  write_codes(lk[0], lv[0]);
+  int buf = 0;
+  for (int at = from; at < to; at += TW, buf ^= 1) {
+    // scalars of this tile's blocks, before the next tile's replace them
+    float ks[NB], vs[NB];
+    int none = 0;
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      ks[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ksv), b));
+      vs[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vsv), b));
+      none |= __builtin_amdgcn_readlane(gone, b) << b;
+    }
+    __syncthreads();                                   // this tile is in LDS; the other buffer is free
+    const bool more = at + TW < to;
+    if (more) {
+      load_codes(at + TW);
+      load_pages(at + 2 * TW);
+    }
+    if (at < hi_max && at + TW > lo_min) {
+      const uint8_t* bk = lk[buf];
+      const uint8_t* bv = lv[buf];
+      v16f sc[TW / 32];
+#pragma unroll
+      for (int t = 0; t < TW / 32; ++t) {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) sc[t][k] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < ST; ++u) {
+          sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              *reinterpret_cast<const v8h*>(bk + k_slot(32 * t + krow, 2 * u + hi)), qf[u], sc[t], 0, 0, 0);
+        }
+      }
+      float vref2 = vref, vmin = vs[0];
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        vref2 = fmaxf(vref2, vs[b]);
+        vmin = fminf(vmin, vs[b]);
+      }
+      v8h pf[TW / 32][2];
+      float m2;
+      // masked positions, and scales too far apart for the sum of weights over scale
+      const bool rare = at + TW > hi_min || at < lo_max || none || !(vmin >= vref2 * 0x1p-40f);
+      if (rare) {
+        float cm = kNone;
+#pragma unroll
+        for (int t = 0; t < TW / 32; ++t)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const int b = 2 * t + (k >> 3), j = at + 16 * b + 8 * hi + (k & 7);
+            sc[t][k] = j >= my_lo && j < my_hi && !(none >> b & 1) ? sc[t][k] * (ks[b] * qscale) : -INFINITY;
+            cm = fmaxf(cm, sc[t][k]);
+          }
+        m2 = fmaxf(m, fmaxf(cm, __shfl_xor(cm, 32)));
+        l *= __builtin_amdgcn_exp2f(m - m2);
+#pragma unroll
+        for (int t = 0; t < TW / 32; ++t)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float e = __builtin_amdgcn_exp2f(sc[t][k] - m2);
+            l += e;
+            pf[t][k >> 3][k & 7] = (_Float16)(e * (vs[2 * t + (k >> 3)] / vref2 * 32768.0f));
+          }
+      } else {
+        float cm = kNone;
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          float x = sc[b >> 1][8 * (b & 1)];
+#pragma unroll
+          for (int k = 1; k < 8; ++k) x = fmaxf(x, sc[b >> 1][8 * (b & 1) + k]);
+          cm = fmaxf(cm, x * (ks[b] * qscale));
+        }
+        m2 = fmaxf(m, fmaxf(cm, __shfl_xor(cm, 32)));
+        l *= __builtin_amdgcn_exp2f(m - m2);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const float f = ks[b] * qscale, c = __builtin_amdgcn_logf(vs[b] / vref2) + 15.0f - m2;
+          float sum = 0.0f;
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float e = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + k], f, c));
+            sum += e;
+            pf[b >> 1][b & 1][k] = (_Float16)e;
+          }
+          l = fmaf(sum, vref2 / vs[b] * 0x1p-15f, l);
+        }
+      }
+      if (__any(m2 != m) || vref2 != vref) {
+        const float ao = __builtin_amdgcn_exp2f(m - m2) * (vref / vref2);
+#pragma unroll
+        for (int i = 0; i < DT; ++i)
+#pragma unroll
+          for (int k = 0; k < 16; ++k) acc[i][k] *= ao;
+      }
+      m = m2;
+      vref = vref2;
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
+              *reinterpret_cast<const v8h*>(bv + v_slot(d0 + 32 * i + l32, 2 * b + hi)), pf[b >> 1][b & 1], acc[i], 0, 0, 0);
+      }
+    }
+    if (more) write_codes(lk[buf ^ 1], lv[buf ^ 1]);
+  }
+
+  // each half of the wave holds half of a row's sum
+  l += __shfl_xor(l, 32);
+  if (wr0 + l32 >= rows) return;
+  const int64_t row = (int64_t)(s.t0 + tok) * p.q.heads + hq;
+  const float back = vref * 0x1p-15f;
+  if (nsplit == 1) {
+    const float out = l == 0.0f ? 0.0f : back / l;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const int64_t o = row * D + d0 + 32 * i + 8 * k + 4 * hi;
+        float f[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) f[e] = l == 0.0f ? 0.0f : acc[i][4 * k + e] * out;
+        if (p.q.ydtype == 0) {
+          *reinterpret_cast<float4*>(static_cast<float*>(p.q.y) + o) = float4{f[0], f[1], f[2], f[3]};
+        } else {
+          const bool bf = p.q.ydtype == 2;
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.q.y) + o) =
+              uint2{u16_of(f[0], bf) | (uint32_t)u16_of(f[1], bf) << 16, u16_of(f[2], bf) | (uint32_t)u16_of(f[3], bf) << 16};
+        }
+      }
+    if (p.q.lse && hi == 0 && d0 == 0) p.q.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) / kLog2e;
+  } else {
+    const int64_t at = blockIdx.y * p.part_rows + row;
+#pragma unroll
+    for (int i = 0; i < DT; ++i)
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        *reinterpret_cast<float4*>(p.part + at * D + d0 + 32 * i + 8 * k + 4 * hi) =
+            float4{acc[i][4 * k] * back, acc[i][4 * k + 1] * back, acc[i][4 * k + 2] * back, acc[i][4 * k + 3] * back};
+    if (hi == 0 && d0 == 0) {
+      float* ml = p.part + (int64_t)gridDim.y * p.part_rows * D + 2 * at;
+      ml[0] = m;
+      ml[1] = l;
+    }
+  }
+}
+
 // Joins the splits of a query row: one wave per row, lanes over the dimensions.
 template <int D>
 __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p, int splits) {
@@ -273,7 +554,8 @@ __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p, int splits) {
   const int x = blockIdx.x * 4 + wave;
   const int h = x % p.c.heads, r = x / p.c.heads;
   if (r >= rows) return;
-  const Range rg = tile_range(p, s, r & ~15, min((r & ~15) + 16, rows));
+  const int r0 = r / p.tile_rows * p.tile_rows;
+  const Range rg = tile_range(p, s, r0, min(r0 + p.tile_rows, rows));
   const int nsplit = (rg.hi - rg.lo + p.split - 1) / p.split;
   if (nsplit <= 1) return;
   const int64_t t = s.t0 + r / p.group;
@@ -298,23 +580,30 @@ __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p, int splits) {
   if (p.q.lse && lane == 0) p.q.lse[row] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
 }
 
-constexpr int kWaves = 4;
+constexpr int kWaves = 4;                  // of k_kv8_decode
 
-// Positions a query row tile can see at most, and how they are split: enough
-// workgroups to fill the chip, splits of at least 64 positions per wave.
+// Which kernel, its query row tiles, and how the positions are split: enough
+// workgroups to fill the chip, splits of at least a few tiles of positions.
 struct Plan {
-  int tiles, split, splits;
+  bool prefill;
+  int tile_rows, tiles, split, splits;
 };
 Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
   Plan pl;
   const int group = q.heads / c.heads;
-  pl.tiles = (int)(((int64_t)b.max_new * group + 15) / 16);
+  const int64_t rows = (int64_t)b.max_new * group;
+  pl.prefill = rows > 64;
+  pl.tile_rows = pl.prefill ? (c.dim <= 128 ? 256 : 128) : 16;
+  pl.tiles = (int)((rows + pl.tile_rows - 1) / pl.tile_rows);
   int64_t span = b.max_len;
-  if (q.window > 0) span = std::min<int64_t>(span, (int64_t)q.window + (q.causal ? 15 / group + 1 : b.max_len) + 64);
+  if (q.window > 0) {
+    const int64_t toks = q.causal ? (pl.tile_rows - 1) / group + 2 : b.max_new;
+    span = std::min<int64_t>(span, (int64_t)q.window + toks + 64);
+  }
   const int64_t work = (int64_t)pl.tiles * c.heads * b.B;
-  const int64_t unit = 64 * kWaves;
-  const int64_t want = std::max<int64_t>(1, 1024 / std::max<int64_t>(work, 1));
-  int64_t units = (span + unit - 1) / unit;
+  const int64_t unit = pl.prefill ? 512 : 64 * kWaves;
+  const int64_t want = std::max<int64_t>(1, (pl.prefill ? 512 : 1024) / std::max<int64_t>(work, 1));
+  const int64_t units = (span + unit - 1) / unit;
   const int64_t per = std::max<int64_t>(1, (units + want - 1) / want);
   pl.split = (int)(per * unit);
   pl.splits = (int)std::max<int64_t>(1, (span + pl.split - 1) / pl.split);
@@ -324,7 +613,11 @@ Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
 template <int D>
 void launch_for(AttnParams p, const Plan& pl, hipStream_t stream) {
   const dim3 grid((unsigned)(pl.tiles * p.c.heads), (unsigned)pl.splits, (unsigned)p.b.B);
-  hipLaunchKernelGGL((k_kv8_decode<D, kWaves>), grid, dim3(64 * kWaves), 0, stream, p);
+  if (pl.prefill) {
+    hipLaunchKernelGGL((k_kv8_prefill<D, 8, (D > 128 ? 2 : 1)>), grid, dim3(512), 0, stream, p);
+  } else {
+    hipLaunchKernelGGL((k_kv8_decode<D, kWaves>), grid, dim3(64 * kWaves), 0, stream, p);
+  }
   if (pl.splits > 1) {
     const int64_t rows = (int64_t)p.b.max_new * p.q.heads;
     hipLaunchKernelGGL((k_kv8_join<D>), dim3((unsigned)((rows + 3) / 4), 1, (unsigned)p.b.B), dim3(256), 0, stream, p,
@@ -346,6 +639,7 @@ void launch_kv8_attention(const KvPool& c, const KvBatch& b, const KvQuery& q, v
   p.b = b;
   p.q = q;
   p.group = q.heads / c.heads;
+  p.tile_rows = pl.tile_rows;
   p.split = pl.split;
   p.part = static_cast<float*>(workspace);
   p.part_rows = (int64_t)b.T * q.heads;
