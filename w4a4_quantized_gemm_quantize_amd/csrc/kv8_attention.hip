@@ -25,6 +25,7 @@
 // weights go from one product's result to the other's operand without
 // leaving their lane, and V^T's rows are read as 16 consecutive bytes.
 #include <algorithm>
+#include <type_traits>
 
 #include "kv8_common.h"
 
@@ -34,7 +35,7 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -3.0e38f;          // running maximum of a row that has seen nothing
-constexpr float kTinyScale = 0x1p-120f;
+constexpr float kTinyScale = 0x1p-120f, kTinyLog = -120.0f;
 
 // Four codes as fp16: 1024 + (code + 128) is the bit pattern 0x6400 | byte.
 __device__ __forceinline__ void widen4(uint32_t w, h2& a, h2& b) {
@@ -108,6 +109,15 @@ __device__ __forceinline__ float load_query(const uint16_t* qp, bool bf16, bool 
     }
   }
   return 1.0f / mul;
+}
+
+// Maximum over a lane and its partner in the other half of the wave.
+__device__ __forceinline__ float max_halves(float x) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float lane_value(float x, int lane) {
+  return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
 }
 
 // Positions a tile of query rows [r0, r1) of a sequence can see: [lo, hi), lo a
@@ -293,7 +303,15 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
 //
 // LDS rows of K (2 D bytes) and V^T (128 bytes) keep their 16-byte slots
 // XOR-swizzled so that 16 consecutive rows hit distinct bank groups.
-template <int D, int NW, int DS>
+//
+// ONE: a page holds whole tiles, so a tile has one page and one pair of scales,
+// fetched through the scalar cache.
+template <typename T>
+__device__ __forceinline__ T scalar_load(const T* p) {
+  return *(const __attribute__((address_space(4))) T*)p;
+}
+
+template <int D, int NW, int DS, bool ONE>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4, NW / 4)))
 void k_kv8_prefill(AttnParams p) {
   constexpr int ST = D / 16, DT = D / 32 / DS;         // k steps of S, the wave's 32-dimension tiles of O
@@ -339,50 +357,84 @@ void k_kv8_prefill(AttnParams p) {
 
   const int P = p.c.page;
   // piece i of this thread: K codes 16 (x % (D / 16)) .. of position x / (D /
-  // 16), or V codes of positions 16 (x % NB) .. of dimension x / NB
-  auto is_k = [&](int i) { return i * 64 * NW + tid < PIECES; };
-  auto x_of = [&](int i) { return (i * 64 * NW + tid) % PIECES; };
-  auto pos_of = [&](int i, int at) { return at + (is_k(i) ? x_of(i) / (D / 16) : 16 * (x_of(i) % NB)); };
-  int pg[NP], pgs;                                     // pages of the next tile: pieces, blocks of 16
-  auto load_pages = [&](int at) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) pg[i] = pos_of(i, at) < to ? page_of(p.b, p.c, seq, pos_of(i, at)) : -1;
-    pgs = at + 16 * (lane % NB) < to ? page_of(p.b, p.c, seq, at + 16 * (lane % NB)) : -1;
+  // 16), or V codes of positions 16 (x % NB) .. of dimension x / NB (a wave's
+  // pieces are all of one kind)
+  auto is_k = [&](int i) {
+    return (i + 1) * 64 * NW <= PIECES ? true : i * 64 * NW >= PIECES ? false : i * 64 * NW + 64 * wave < PIECES;
   };
+  auto x_of = [&](int i) { return i * 64 * NW + tid - (is_k(i) ? 0 : PIECES); };
+  auto pos_of = [&](int i) { return is_k(i) ? x_of(i) / (D / 16) : 16 * (x_of(i) % NB); };
+  // Pages: the table's entries as they are, judged when they are used, so that
+  // nothing waits for them where they are loaded. Positions past the last one
+  // take its page.
+  const int* const table = p.b.table + seq * p.b.table_ld;
+  const uint32_t page_bytes = (uint32_t)p.c.heads * P * D;     // < 2^32
+  const int8_t* const k_head = p.c.k + (int64_t)h * P * D;
+  const int8_t* const v_head = p.c.v + (int64_t)h * P * D;
+  auto page_at = [&](int pos) { return table[min(pos, to - 1) >> p.c.log_page]; };
+  auto page_one = [&](int pos) { return scalar_load(table + (min(pos, to - 1) >> p.c.log_page)); };
+  // A step stages the K codes of tile kt and the V codes of the tile before it.
+  constexpr int NPG = ONE ? 2 : NP;                    // pages: of K and V, or of each piece
+  int pg[NPG];
   uint4 code[NP];
-  float ksv, vsv;                                      // of block lane % NB
-  int gone;                                            // that block's page is none
-  auto load_codes = [&](int at) {
+  auto v_tile = [&](int kt) { return max(kt - TW, from); };
+  auto tile_of = [&](int i, int kt) { return is_k(i) ? kt : v_tile(kt); };
+  auto load_pages = [&](int kt) {
+    if constexpr (ONE) {
+      pg[0] = page_one(kt);
+      pg[1] = page_one(v_tile(kt));
+    } else {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) pg[i] = page_at(tile_of(i, kt) + pos_of(i));
+    }
+  };
+  auto load_codes = [&](int kt) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int64_t base = ((int64_t)max(pg[i], 0) * p.c.heads + h) * P * D;
-      const int in = pos_of(i, at) & (P - 1), x = x_of(i);
-      code[i] = is_k(i) ? *reinterpret_cast<const uint4*>(p.c.k + base + in * D + x % (D / 16) * 16)
-                        : *reinterpret_cast<const uint4*>(p.c.v + base + x / NB * P + in);
+      const int id = pg[ONE ? (is_k(i) ? 0 : 1) : i], x = x_of(i);
+      const uint32_t page = (unsigned)id < (unsigned)p.c.num_pages ? id : 0;
+      const int8_t* src = (is_k(i) ? k_head : v_head) + (uint64_t)page * page_bytes;
+      if constexpr (ONE) {
+        // the tile's offset in its page, then the piece's in the tile
+        const int in = tile_of(i, kt) & (P - 1);
+        src += is_k(i) ? in * D : in;
+        code[i] = *reinterpret_cast<const uint4*>(src + (uint32_t)(is_k(i) ? 16 * x : x / NB * P + 16 * (x % NB)));
+      } else {
+        const int in = (tile_of(i, kt) + pos_of(i)) & (P - 1);
+        code[i] = *reinterpret_cast<const uint4*>(src + (is_k(i) ? in * D + x % (D / 16) * 16 : x / NB * P + in));
+      }
     }
-    gone = pgs < 0;
-    ksv = gone ? 0.0f : p.c.ks[(int64_t)pgs * p.c.heads + h];
-    vsv = gone ? 0.0f : p.c.vs[(int64_t)pgs * p.c.heads + h];
   };
+  // Scales of a tile (of this lane's block lane % NB, or of all), loaded while the
+  // weights of the tile before it are made, from the page loaded one earlier.
+  int pgs, gone, gone_next;
+  float ksv, vsv, ks_next, vs_next;
+  auto load_scales = [&]() {
+    gone_next = (unsigned)pgs >= (unsigned)p.c.num_pages;   // no page of the pool
+    const int64_t e = (int64_t)(gone_next ? 0 : pgs) * p.c.heads + h;
+    ks_next = ONE ? scalar_load(p.c.ks + e) : p.c.ks[e];
+    vs_next = ONE ? scalar_load(p.c.vs + e) : p.c.vs[e];
+  };
+  auto scale_pages = [&](int at) { pgs = ONE ? page_one(at) : page_at(at + 16 * (lane % NB)); };
   auto k_slot = [&](int row, int slot) {               // byte offset in a K buffer
     return row * 2 * D + 16 * (slot ^ (D % 128 == 0 ? row & 15 : (row >> 1) & 7));
   };
   auto v_slot = [&](int row, int slot) {               // in a V buffer
     return row * 2 * TW + 16 * (slot ^ (TW == 64 ? (row >> 1) & 7 : (row >> 2) & 3));
   };
-  auto write_codes = [&](uint8_t* bk, uint8_t* bv) {
+  auto write_codes = [&](int kt) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const v8h a = widen8(code[i].x, code[i].y), b = widen8(code[i].z, code[i].w);
-      const int x = x_of(i);
+      const int x = x_of(i), buf = (tile_of(i, kt) - from) / TW & 1;
       if (is_k(i)) {
         const int row = x / (D / 16), c = 2 * (x % (D / 16));
-        *reinterpret_cast<v8h*>(bk + k_slot(row, c)) = a;
-        *reinterpret_cast<v8h*>(bk + k_slot(row, c + 1)) = b;
+        *reinterpret_cast<v8h*>(lk[buf] + k_slot(row, c)) = a;
+        *reinterpret_cast<v8h*>(lk[buf] + k_slot(row, c + 1)) = b;
       } else {
         const int row = x / NB, c = 2 * (x % NB);
-        *reinterpret_cast<v8h*>(bv + v_slot(row, c)) = a;
-        *reinterpret_cast<v8h*>(bv + v_slot(row, c + 1)) = b;
+        *reinterpret_cast<v8h*>(lv[buf] + v_slot(row, c)) = a;
+        *reinterpret_cast<v8h*>(lv[buf] + v_slot(row, c + 1)) = b;
       }
     }
   };
@@ -392,123 +444,206 @@ void k_kv8_prefill(AttnParams p) {
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int k = 0; k < 16; ++k) acc[i][k] = 0.0f;
-  float m = kNone, l = 0.0f, vref = kTinyScale;
+  // running maximum (log2 domain), sum, and log2 of the largest V scale met
+  float m = kNone, l = 0.0f, lref = kTinyLog;
   const int krow = (l32 & 0x13) | (l32 & 4) << 1 | (l32 & 8) >> 1;
+  v16f sc[TW / 32];
+  v8h pf[TW / 32][2];
+  auto sees = [&](int at) { return at < to && at < hi_max && at + TW > lo_min; };
 
-  load_pages(from);
-  load_codes(from);
-  load_pages(from + TW);
-  write_codes(lk[0], lv[0]);
-  int buf = 0;
-  for (int at = from; at < to; at += TW, buf ^= 1) {
-    // scalars of this tile's blocks, before the next tile's replace them
-    float ks[NB], vs[NB];
-    int none = 0;
+  // The matrix work of a step: values of the last tile (VALUES), scores of this
+  // one (SCORES). Operand reads run RING ahead of the instructions that use
+  // them, in this order; one wave per SIMD does this at a time, so nothing else
+  // hides their latency.
+  auto matrix_step = [&](int at, auto values_c, auto scores_c) {
+    constexpr int NV = decltype(values_c)::value ? DT * NB : 0, NS = decltype(scores_c)::value ? ST * TW / 32 : 0;
+    constexpr int RING = 6;
+    const uint8_t* bk = lk[(at - from) / TW & 1];
+    const uint8_t* bv = lv[(at - TW - from) / TW & 1];
+    auto read = [&](int x) {
+      if (x < NV) return *reinterpret_cast<const v8h*>(bv + v_slot(d0 + 32 * (x % DT) + l32, 2 * (x / DT) + hi));
+      x -= NV;
+      return *reinterpret_cast<const v8h*>(bk + k_slot(32 * (x % (TW / 32)) + krow, 2 * (x / (TW / 32)) + hi));
+    };
+    v8h ring[RING];
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      ks[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(ksv), b));
-      vs[b] = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(vsv), b));
-      none |= __builtin_amdgcn_readlane(gone, b) << b;
-    }
-    __syncthreads();                                   // this tile is in LDS; the other buffer is free
-    const bool more = at + TW < to;
-    if (more) {
-      load_codes(at + TW);
-      load_pages(at + 2 * TW);
-    }
-    if (at < hi_max && at + TW > lo_min) {
-      const uint8_t* bk = lk[buf];
-      const uint8_t* bv = lv[buf];
-      v16f sc[TW / 32];
+    for (int x = 0; x < RING; ++x) ring[x] = read(x);
+    if constexpr (NS > 0) {
 #pragma unroll
-      for (int t = 0; t < TW / 32; ++t) {
+      for (int t = 0; t < TW / 32; ++t)
 #pragma unroll
         for (int k = 0; k < 16; ++k) sc[t][k] = 0.0f;
+    }
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < ST; ++u) {
-          sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              *reinterpret_cast<const v8h*>(bk + k_slot(32 * t + krow, 2 * u + hi)), qf[u], sc[t], 0, 0, 0);
-        }
+    for (int x = 0; x < NV + NS; ++x) {
+      if (x < NV) {
+        const int i = x % DT, b = x / DT;
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[x % RING], pf[b >> 1][b & 1], acc[i], 0, 0, 0);
+      } else {
+        const int t = (x - NV) % (TW / 32), u = (x - NV) / (TW / 32);
+        sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[x % RING], qf[u], sc[t], 0, 0, 0);
       }
-      float vref2 = vref, vmin = vs[0];
+      if (x + RING < NV + NS) ring[x % RING] = read(x + RING);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+  // scores -> weights of the tile at `at`, whose scales this wave holds
+  auto weights = [&](int at) {
+    // factors of the tile's blocks: of the scores, log2 and reciprocal of the V
+    // scale. A block past the last position or of no page is masked; its scales
+    // must not count.
+    constexpr int NF = ONE ? 1 : NB;
+    float f[NF], lvs[NF], ivs[NF];
+    int none = 0;
+    if constexpr (ONE) {
+      f[0] = ksv * qscale;
+      lvs[0] = gone ? kTinyLog : __builtin_amdgcn_logf(vsv);
+      ivs[0] = __builtin_amdgcn_rcpf(vsv);
+      none = gone ? (1 << NB) - 1 : 0;
+    } else {
+      const bool past = at + 16 * (lane % NB) >= to || gone;
+      const float lv_ = past ? kTinyLog : __builtin_amdgcn_logf(vsv), iv_ = __builtin_amdgcn_rcpf(vsv);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
-        vref2 = fmaxf(vref2, vs[b]);
-        vmin = fminf(vmin, vs[b]);
-      }
-      v8h pf[TW / 32][2];
-      float m2;
-      // masked positions, and scales too far apart for the sum of weights over scale
-      const bool rare = at + TW > hi_min || at < lo_max || none || !(vmin >= vref2 * 0x1p-40f);
-      if (rare) {
-        float cm = kNone;
-#pragma unroll
-        for (int t = 0; t < TW / 32; ++t)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const int b = 2 * t + (k >> 3), j = at + 16 * b + 8 * hi + (k & 7);
-            sc[t][k] = j >= my_lo && j < my_hi && !(none >> b & 1) ? sc[t][k] * (ks[b] * qscale) : -INFINITY;
-            cm = fmaxf(cm, sc[t][k]);
-          }
-        m2 = fmaxf(m, fmaxf(cm, __shfl_xor(cm, 32)));
-        l *= __builtin_amdgcn_exp2f(m - m2);
-#pragma unroll
-        for (int t = 0; t < TW / 32; ++t)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float e = __builtin_amdgcn_exp2f(sc[t][k] - m2);
-            l += e;
-            pf[t][k >> 3][k & 7] = (_Float16)(e * (vs[2 * t + (k >> 3)] / vref2 * 32768.0f));
-          }
-      } else {
-        float cm = kNone;
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          float x = sc[b >> 1][8 * (b & 1)];
-#pragma unroll
-          for (int k = 1; k < 8; ++k) x = fmaxf(x, sc[b >> 1][8 * (b & 1) + k]);
-          cm = fmaxf(cm, x * (ks[b] * qscale));
-        }
-        m2 = fmaxf(m, fmaxf(cm, __shfl_xor(cm, 32)));
-        l *= __builtin_amdgcn_exp2f(m - m2);
-#pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const float f = ks[b] * qscale, c = __builtin_amdgcn_logf(vs[b] / vref2) + 15.0f - m2;
-          float sum = 0.0f;
-#pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float e = __builtin_amdgcn_exp2f(fmaf(sc[b >> 1][8 * (b & 1) + k], f, c));
-            sum += e;
-            pf[b >> 1][b & 1][k] = (_Float16)e;
-          }
-          l = fmaf(sum, vref2 / vs[b] * 0x1p-15f, l);
-        }
-      }
-      if (__any(m2 != m) || vref2 != vref) {
-        const float ao = __builtin_amdgcn_exp2f(m - m2) * (vref / vref2);
-#pragma unroll
-        for (int i = 0; i < DT; ++i)
-#pragma unroll
-          for (int k = 0; k < 16; ++k) acc[i][k] *= ao;
-      }
-      m = m2;
-      vref = vref2;
-#pragma unroll
-      for (int i = 0; i < DT; ++i) {
-#pragma unroll
-        for (int b = 0; b < NB; ++b)
-          acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(
-              *reinterpret_cast<const v8h*>(bv + v_slot(d0 + 32 * i + l32, 2 * b + hi)), pf[b >> 1][b & 1], acc[i], 0, 0, 0);
+        f[b] = lane_value(ksv, b) * qscale;
+        lvs[b] = lane_value(lv_, b);
+        ivs[b] = lane_value(iv_, b);
+        none |= __builtin_amdgcn_readlane(gone, b) << b;
       }
     }
-    if (more) write_codes(lk[buf ^ 1], lv[buf ^ 1]);
+    float lref2 = lref, lmin = lvs[0];
+#pragma unroll
+    for (int b = 0; b < NF; ++b) {
+      lref2 = fmaxf(lref2, lvs[b]);
+      lmin = fminf(lmin, lvs[b]);
+    }
+    float m2;
+    // masked positions, and scales too far apart for the sum of weights over scale
+    const bool rare = at + TW > hi_min || at < lo_max || none || !(lmin >= lref2 - 40.0f);
+    float cm = kNone;
+    if (rare) {
+#pragma unroll
+      for (int t = 0; t < TW / 32; ++t)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int b = 2 * t + (k >> 3), j = at + 16 * b + 8 * hi + (k & 7);
+          sc[t][k] = j >= my_lo && j < my_hi && !(none >> b & 1) ? sc[t][k] * f[b % NF] : -INFINITY;
+          cm = fmaxf(cm, sc[t][k]);
+        }
+    } else {
+#pragma unroll
+      for (int g = 0; g < NF; ++g) {                   // scores that share a factor
+        float x = sc[g >> 1][8 * (g & 1)];
+#pragma unroll
+        for (int k = 1; k < 16 * (TW / 32) / NF; ++k) x = fmaxf(x, sc[(8 * g + k) >> 4][(8 * g + k) & 15]);
+        cm = fmaxf(cm, x * f[g]);
+      }
+    }
+    // The maximum only has to keep the weights within fp16: it stays where it is
+    // until some row passes it by a factor of 1.98 (2^15 1.98 < 65504).
+    m2 = fmaxf(m, max_halves(cm));
+    if (__any(m2 > m + 0.985f) || lref2 != lref) {
+      const float al = __builtin_amdgcn_exp2f(m - m2), ao = __builtin_amdgcn_exp2f(m - m2 + (lref - lref2));
+      l *= al;
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[i][k] *= ao;
+      m = m2;
+      lref = lref2;
+    }
+    if (rare) {
+#pragma unroll
+      for (int t = 0; t < TW / 32; ++t)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const int b = 2 * t + (k >> 3);
+          const float e = __builtin_amdgcn_exp2f(sc[t][k] - m);
+          l += e;
+          pf[t][k >> 3][k & 7] = (_Float16)(e * __builtin_amdgcn_exp2f(lvs[b % NF] - lref + 15.0f));
+        }
+    } else {
+      const float base = 15.0f - lref - m, unit = __builtin_amdgcn_exp2f(lref - 15.0f);
+#pragma unroll
+      for (int g = 0; g < NF; ++g) {
+        const float c = lvs[g] + base;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int k = 0; k < 16 * (TW / 32) / NF; ++k) {
+          const int x = 8 * g + k;
+          const float e = __builtin_amdgcn_exp2f(fmaf(sc[x >> 4][x & 15], f[g], c));
+          sum[k & 1] += e;
+          pf[x >> 4][x >> 3 & 1][x & 7] = (_Float16)e;
+        }
+        l = fmaf(sum[0] + sum[1], unit * ivs[g], l);
+      }
+    }
+  };
+
+  // Two groups of waves, one wave of each per SIMD, run the same steps half a
+  // tile apart: while one group's waves do their matrix work (values of the
+  // last tile, scores of this one) the other's turn scores into weights, so the
+  // matrix cores and the vector units work at the same time. K is staged a tile
+  // ahead of V; the late group stages its pieces one tile further ahead, so that
+  // both groups' pieces of a tile are in LDS before the early group reads it.
+#define PHASE_END()                                                                   \
+  {                                                                                   \
+    __builtin_amdgcn_s_waitcnt(0xC07F); /* lgkmcnt(0): own LDS accesses are done */   \
+    asm volatile("" ::: "memory");                                                    \
+    __builtin_amdgcn_sched_barrier(0);                                                \
+    __builtin_amdgcn_s_barrier();                                                     \
+    __builtin_amdgcn_sched_barrier(0);                                                \
+    asm volatile("" ::: "memory");                                                    \
   }
+  const bool late = wave >= NW / 2;
+  const int ahead = late ? 2 * TW : TW;                // K tiles that a wave's weights step stages ahead
+  if (from < to) {
+    load_pages(from);
+    load_codes(from);
+    write_codes(from);
+    if (late) {
+      load_pages(from + TW);
+      load_codes(from + TW);
+      write_codes(from + TW);
+    }
+    load_pages(from + ahead);
+    scale_pages(from);
+    load_scales();
+    scale_pages(from + TW);
+  }
+  PHASE_END()
+  if (late) PHASE_END()
+  for (int at = from; at < to; at += TW) {
+    load_codes(at + ahead);
+    // (a tile that the wave's rows do not see has weights of zero)
+    if (at > from) matrix_step(at, std::true_type{}, std::true_type{});
+    else matrix_step(at, std::false_type{}, std::true_type{});
+    PHASE_END()
+    ksv = ks_next;
+    vsv = vs_next;
+    gone = gone_next;
+    load_scales();
+    scale_pages(at + 2 * TW);
+    load_pages(at + TW + ahead);
+    if (sees(at)) {
+      weights(at);
+    } else {
+#pragma unroll
+      for (int b = 0; b < NB; ++b) pf[b >> 1][b & 1] = v8h{};
+    }
+    write_codes(at + ahead);
+    PHASE_END()
+  }
+  if (from < to) matrix_step(from + (to - from + TW - 1) / TW * TW, std::true_type{}, std::false_type{});
+  if (!late) PHASE_END()
+#undef PHASE_END
 
   // each half of the wave holds half of a row's sum
   l += __shfl_xor(l, 32);
   if (wr0 + l32 >= rows) return;
   const int64_t row = (int64_t)(s.t0 + tok) * p.q.heads + hq;
-  const float back = vref * 0x1p-15f;
+  const float back = __builtin_amdgcn_exp2f(lref - 15.0f);
   if (nsplit == 1) {
     const float out = l == 0.0f ? 0.0f : back / l;
 #pragma unroll
@@ -614,7 +749,9 @@ template <int D>
 void launch_for(AttnParams p, const Plan& pl, hipStream_t stream) {
   const dim3 grid((unsigned)(pl.tiles * p.c.heads), (unsigned)pl.splits, (unsigned)p.b.B);
   if (pl.prefill) {
-    hipLaunchKernelGGL((k_kv8_prefill<D, 8, (D > 128 ? 2 : 1)>), grid, dim3(512), 0, stream, p);
+    constexpr int DS = D > 128 ? 2 : 1;
+    if (p.c.page >= 64) hipLaunchKernelGGL((k_kv8_prefill<D, 8, DS, true>), grid, dim3(512), 0, stream, p);
+    else hipLaunchKernelGGL((k_kv8_prefill<D, 8, DS, false>), grid, dim3(512), 0, stream, p);
   } else {
     hipLaunchKernelGGL((k_kv8_decode<D, kWaves>), grid, dim3(64 * kWaves), 0, stream, p);
   }
