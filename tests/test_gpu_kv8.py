@@ -9,8 +9,9 @@ Codes, scales and read-back values are exact. Attention is compared with a
     by (D + 4) 2^-24 S, in numerator and denominator: 2 (D + 4) 2^-24 S A
   * exp2 (2 ulp), the scale factors and the sums over L positions and the
     joins of splits, numerator and denominator: 2 (L + 32) 2^-24 A
-  * weights under 2^-29 of the largest scale met, to 2^-40 of it: L 127 2^-40
-    times the largest scale
+  * weights in fp16's subnormal range: off by half its step, 2^-25, and scaled
+    by 2^9 at least relative to the largest page scale: 2^-34 of it each, times
+    |code| <= 127, over L positions
   * the output's own rounding: 2^-11 |o| (fp16), 2^-8 (bf16).
 """
 import math
@@ -111,7 +112,7 @@ def attention_ref(B, q, causal, window, scale, hidden=None):
             lse[t0:t0 + n, h] = torch.where(seen, torch.logsumexp(s, dim=1), lse[t0:t0 + n, h])
             a = p @ v[h // grp].abs()
             rel = 2.0 ** -11 + 2 * (B.dim + 4) * 2.0 ** -24 * big + 2 * (length + 32) * 2.0 ** -24
-            bound[t0:t0 + n, h] = rel * a + length * 127 * 2.0 ** -40 * top
+            bound[t0:t0 + n, h] = rel * a + length * 127 * 2.0 ** -34 * top
     return o, lse, bound
 
 

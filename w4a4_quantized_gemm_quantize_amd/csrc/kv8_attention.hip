@@ -12,10 +12,10 @@
 // weight, so no code is ever rounded. bf16 queries are brought to fp16 with a
 // power of two per row (the largest element to [2^14, 2^15): elements down to
 // 2^-29 of it stay exact, smaller ones are off by 2^-40 of it). The weights
-// p_j vs_j enter the second product as fp16(2^15 p_j vs_j / vref), p_j <= 1
-// and vref the largest page scale seen so far: a relative rounding of 2^-12
-// for weights within 2^-29 of the largest one, below that an absolute one of
-// 2^-40 vref.
+// p_j vs_j enter the second product as fp16(2^b p_j vs_j / vref), vref the
+// largest page scale met so far, b = 15 with few query rows and 9 with many: a
+// relative rounding of at most 2^-11 for weights down to 2^(-14 - b) of the
+// largest one, below that an absolute one of 2^(-25 - b) vref.
 //
 // Layout. S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_16x16x32_f16: the rows
 // of the first product are 64 positions in four tiles, row 4 g + i of tile t
@@ -36,6 +36,9 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -3.0e38f;          // running maximum of a row that has seen nothing
 constexpr float kTinyScale = 0x1p-120f, kTinyLog = -120.0f;
+// k_kv8_prefill: weights up to 2^kSlack (the running maximum may lag so far)
+// enter fp16 times 2^kBias: at most 2^15
+constexpr float kBias = 9.0f, kSlack = 6.0f;
 
 // Four codes as fp16: 1024 + (code + 128) is the bit pattern 0x6400 | byte.
 __device__ __forceinline__ void widen4(uint32_t w, h2& a, h2& b) {
@@ -541,9 +544,10 @@ void k_kv8_prefill(AttnParams p) {
       }
     }
     // The maximum only has to keep the weights within fp16: it stays where it is
-    // until some row passes it by a factor of 1.98 (2^15 1.98 < 65504).
+    // until some row passes it by 2^kSlack (rescaling O in most tiles of 8192
+    // positions cost 14 % of the time).
     m2 = fmaxf(m, max_halves(cm));
-    if (__any(m2 > m + 0.985f) || lref2 != lref) {
+    if (__any(m2 > m + kSlack) || lref2 != lref) {
       const float al = __builtin_amdgcn_exp2f(m - m2), ao = __builtin_amdgcn_exp2f(m - m2 + (lref - lref2));
       l *= al;
 #pragma unroll
@@ -561,10 +565,10 @@ void k_kv8_prefill(AttnParams p) {
           const int b = 2 * t + (k >> 3);
           const float e = __builtin_amdgcn_exp2f(sc[t][k] - m);
           l += e;
-          pf[t][k >> 3][k & 7] = (_Float16)(e * __builtin_amdgcn_exp2f(lvs[b % NF] - lref + 15.0f));
+          pf[t][k >> 3][k & 7] = (_Float16)(e * __builtin_amdgcn_exp2f(lvs[b % NF] - lref + kBias));
         }
     } else {
-      const float base = 15.0f - lref - m, unit = __builtin_amdgcn_exp2f(lref - 15.0f);
+      const float base = kBias - lref - m, unit = __builtin_amdgcn_exp2f(lref - kBias);
 #pragma unroll
       for (int g = 0; g < NF; ++g) {
         const float c = lvs[g] + base;
@@ -643,7 +647,7 @@ void k_kv8_prefill(AttnParams p) {
   l += __shfl_xor(l, 32);
   if (wr0 + l32 >= rows) return;
   const int64_t row = (int64_t)(s.t0 + tok) * p.q.heads + hq;
-  const float back = __builtin_amdgcn_exp2f(lref - 15.0f);
+  const float back = __builtin_amdgcn_exp2f(lref - kBias);
   if (nsplit == 1) {
     const float out = l == 0.0f ? 0.0f : back / l;
 #pragma unroll
