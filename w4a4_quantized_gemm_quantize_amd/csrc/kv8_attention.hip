@@ -141,7 +141,8 @@ __device__ __forceinline__ Range tile_range(const AttnParams& p, const Seq& s, i
 // query head of the group) of one kv head and a split of the positions; its
 // waves take chunks of 64 positions in turn, with no sharing until the end.
 template <int D, int NW>
-__global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
+__global__ __launch_bounds__(64 * NW)
+__attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv8_decode(AttnParams p) {
   constexpr int DB = D / 64, DT = D / 16;
   __shared__ float lo_[NW][16][D + 4];
   __shared__ float lm[NW][16], ll[NW][16];
@@ -171,31 +172,59 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
                              p.q.bf16, p.q.scale < 0.0f, [&](int i) { return 64 * (i >> 1) + 16 * g + 8 * (i & 1); }, qf);
 
   const int P = p.c.page;
+  const int* const table = p.b.table + seq * p.b.table_ld;
+  const uint32_t page_bytes = (uint32_t)p.c.heads * P * D;     // < 2^32
+  const int8_t* const k_head = p.c.k + (int64_t)h * P * D;
+  const int8_t* const v_head = p.c.v + (int64_t)h * P * D;
+  // This lane's pages as a reader of K rows (positions 16 (c / 4) .. of a chunk)
+  // and as the owner of scores and V columns (positions 16 g ..): the table's
+  // entries as they are, judged when they are used; positions past the last
+  // one take its page. Everything of a chunk is loaded while the one before it
+  // is worked on: its pages one chunk earlier still, K's codes once the scores
+  // have left their registers, V's once the values have.
+  int gk, gv;
+  auto load_pages = [&](int at) {
+    gk = table[min(at + 16 * (c >> 2), to - 1) >> p.c.log_page];
+    gv = table[min(at + 16 * g, to - 1) >> p.c.log_page];
+  };
+  auto page_ok = [&](int id) { return (unsigned)id < (unsigned)p.c.num_pages; };
+  uint4 kr[4][DB], vr[DT];
+  float ks, vs, ks_next, vs_next;
+  bool ok, ok_next;                                    // the page of this lane's scores is one of the pool
+  const int8_t* vp;
+  auto load_k = [&](int at) {
+    const int8_t* kp = k_head + (uint64_t)(uint32_t)(page_ok(gk) ? gk : 0) * page_bytes +
+                       (((at + 16 * (c >> 2)) & (P - 1)) + (c & 3)) * D + 16 * g;
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int d = 0; d < DB; ++d) kr[t][d] = *reinterpret_cast<const uint4*>(kp + 4 * t * D + 64 * d);
+    ok_next = page_ok(gv);
+    const uint32_t page = ok_next ? gv : 0;
+    ks_next = p.c.ks[(int64_t)page * p.c.heads + h];
+    vs_next = p.c.vs[(int64_t)page * p.c.heads + h];
+    vp = v_head + (uint64_t)page * page_bytes + ((at + 16 * g) & (P - 1)) + c * P;
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int i = 0; i < DT; ++i) vr[i] = *reinterpret_cast<const uint4*>(vp + 16 * i * P);
+  };
+
   v4f acc[DT];
 #pragma unroll
   for (int i = 0; i < DT; ++i) acc[i] = v4f{0, 0, 0, 0};
   float m = kNone, l = 0.0f, vref = kTinyScale;
 
+  if (from + 64 * wave < to) {
+    load_pages(from + 64 * wave);
+    load_k(from + 64 * wave);
+    load_pages(from + 64 * (wave + NW));
+    load_v();
+  }
   for (int at = from + 64 * wave; at < to; at += 64 * NW) {
-    // this lane's page as a reader of K rows (positions 16 (c / 4) ..) and as
-    // the owner of scores and V columns (positions 16 g ..)
-    const int pk = at + 16 * (c >> 2), pv = at + 16 * g;
-    const int gk = pk < to ? page_of(p.b, p.c, seq, pk) : -1;
-    const int gv = pv < to ? page_of(p.b, p.c, seq, pv) : -1;
-    const int8_t* kp = p.c.k + ((int64_t)max(gk, 0) * p.c.heads + h) * P * D + (int64_t)(pk & (P - 1)) * D;
-    const int8_t* vp = p.c.v + ((int64_t)max(gv, 0) * p.c.heads + h) * P * D + (pv & (P - 1));
-    const float ks = gv < 0 ? 0.0f : p.c.ks[(int64_t)gv * p.c.heads + h];
-    const float vs = gv < 0 ? 0.0f : p.c.vs[(int64_t)gv * p.c.heads + h];
-    uint4 kr[4][DB];
-#pragma unroll
-    for (int t = 0; t < 4; ++t)
-#pragma unroll
-      for (int d = 0; d < DB; ++d)
-        kr[t][d] = *reinterpret_cast<const uint4*>(kp + (4 * t + (c & 3)) * D + 64 * d + 16 * g);
-    uint4 vr[DT];
-#pragma unroll
-    for (int i = 0; i < DT; ++i) vr[i] = *reinterpret_cast<const uint4*>(vp + (16 * i + c) * P);
-
+    ks = ks_next;
+    vs = vs_next;
+    ok = ok_next;
     v4f sc[4];
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -206,8 +235,13 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
         sc[t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(kr[t][d].z, kr[t][d].w), qf[2 * d + 1], sc[t], 0, 0, 0);
       }
     }
+    const bool more = at + 64 * NW < to;
+    if (more) {
+      load_k(at + 64 * NW);
+      load_pages(at + 128 * NW);
+    }
     const float f = ks * qscale;
-    const int first = pv, lim = gv < 0 ? 0 : row_hi;
+    const int first = at + 16 * g, lim = ok ? min(row_hi, to) : 0;
     float cm = kNone;
 #pragma unroll
     for (int t = 0; t < 4; ++t)
@@ -218,13 +252,14 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
         cm = fmaxf(cm, sc[t][i]);
       }
     cm = fmaxf(cm, __shfl_xor(cm, 16));
-    cm = fmaxf(cm, __shfl_xor(cm, 32));
-    float vm = fmaxf(vs, __shfl_xor(vs, 16));
-    vm = fmaxf(vm, __shfl_xor(vm, 32));
+    cm = max_halves(cm);
+    // a block past the last position or of no page: its scale must not count
+    const float vs_here = ok && first < to ? vs : 0.0f;
+    const float vm = max_halves(fmaxf(vs_here, __shfl_xor(vs_here, 16)));
     const float m2 = fmaxf(m, cm), vref2 = fmaxf(vref, vm);
     const float al = __builtin_amdgcn_exp2f(m - m2);
     const float ao = al * (vref / vref2);
-    const float w = vs / vref2 * 32768.0f;
+    const float w = vs_here / vref2 * 32768.0f;
     l *= al;
     v8h pf[2];
 #pragma unroll
@@ -244,6 +279,7 @@ __global__ __launch_bounds__(64 * NW) void k_kv8_decode(AttnParams p) {
       acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(vr[i].x, vr[i].y), pf[0], acc[i], 0, 0, 0);
       acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(vr[i].z, vr[i].w), pf[1], acc[i], 0, 0, 0);
     }
+    if (more) load_v();
   }
   // the lanes of a row hold its positions 16 g .. of each chunk
   l += __shfl_xor(l, 16);
@@ -683,46 +719,73 @@ void k_kv8_prefill(AttnParams p) {
   }
 }
 
-// Joins the splits of a query row: one wave per row, lanes over the dimensions.
+// Joins the splits of a query row: a workgroup per row, 4 dimensions per thread,
+// the threads' groups taking the splits in turn and meeting in LDS.
 template <int D>
 __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p, int splits) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int seq = blockIdx.z;
+  constexpr int TPS = D / 4, G = 256 / TPS;            // threads per split, splits at a time
+  __shared__ float so[G][D];
+  __shared__ float sm[G], sl[G];
+  const int seq = blockIdx.y;
   const Seq s = sequence(p.b, seq);
-  const int rows = s.n * p.group;                   // of one kv head
-  const int x = blockIdx.x * 4 + wave;
-  const int h = x % p.c.heads, r = x / p.c.heads;
-  if (r >= rows) return;
+  const int h = blockIdx.x % p.c.heads, r = blockIdx.x / p.c.heads;
+  if (r >= s.n * p.group) return;
   const int r0 = r / p.tile_rows * p.tile_rows;
-  const Range rg = tile_range(p, s, r0, min(r0 + p.tile_rows, rows));
+  const Range rg = tile_range(p, s, r0, min(r0 + p.tile_rows, s.n * p.group));
   const int nsplit = (rg.hi - rg.lo + p.split - 1) / p.split;
   if (nsplit <= 1) return;
   const int64_t t = s.t0 + r / p.group;
   const int head = h * p.group + r % p.group;
   const int64_t row = t * p.q.heads + head;
   const float* ml = p.part + (int64_t)splits * p.part_rows * D;
-  float M = kNone;
-  for (int i = 0; i < nsplit; ++i) M = fmaxf(M, ml[2 * (i * p.part_rows + row)]);
-  float L = 0.0f, o[D / 64];
+  const int g = threadIdx.x / TPS, d = threadIdx.x % TPS * 4;
+  float M = kNone, L = 0.0f;
+  v4f o = {0, 0, 0, 0};
+  if (g < G) {
+#pragma unroll 4
+    for (int i = g; i < nsplit; i += G) {
+      const int64_t at = i * p.part_rows + row;
+      const float2 e = *reinterpret_cast<const float2*>(ml + 2 * at);
+      const v4f x = *reinterpret_cast<const v4f*>(p.part + at * D + d);
+      const float M2 = fmaxf(M, e.x);
+      const float a = __builtin_amdgcn_exp2f(M - M2), b = __builtin_amdgcn_exp2f(e.x - M2);
+      L = L * a + e.y * b;
 #pragma unroll
-  for (int d = 0; d < D / 64; ++d) o[d] = 0.0f;
-  for (int i = 0; i < nsplit; ++i) {
-    const int64_t at = i * p.part_rows + row;
-    const float e = __builtin_amdgcn_exp2f(ml[2 * at] - M);
-    L += ml[2 * at + 1] * e;
-#pragma unroll
-    for (int d = 0; d < D / 64; ++d) o[d] += p.part[at * D + 64 * d + lane] * e;
+      for (int k = 0; k < 4; ++k) o[k] = o[k] * a + x[k] * b;
+      M = M2;
+    }
+    *reinterpret_cast<v4f*>(&so[g][d]) = o;
+    if (d == 0) {
+      sm[g] = M;
+      sl[g] = L;
+    }
   }
+  __syncthreads();
+  if (threadIdx.x >= D) return;
+  const int x = threadIdx.x;
+  M = kNone;
 #pragma unroll
-  for (int d = 0; d < D / 64; ++d)
-    store_as(p.q.y, p.q.ydtype, row * D + 64 * d + lane, L == 0.0f ? 0.0f : o[d] / L);
-  if (p.q.lse && lane == 0) p.q.lse[row] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
+  for (int i = 0; i < G; ++i) M = fmaxf(M, sm[i]);
+  float out = 0.0f;
+  L = 0.0f;
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    const float e = __builtin_amdgcn_exp2f(sm[i] - M);
+    L += sl[i] * e;
+    out += so[i][x] * e;
+  }
+  store_as(p.q.y, p.q.ydtype, row * D + x, L == 0.0f ? 0.0f : out / L);
+  if (p.q.lse && x == 0) p.q.lse[row] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
 }
 
 constexpr int kWaves = 4;                  // of k_kv8_decode
 
-// Which kernel, its query row tiles, and how the positions are split: enough
-// workgroups to fill the chip, splits of at least a few tiles of positions.
+// Which kernel, its query row tiles, and how the positions are split: into as
+// few splits as fill the chip, since each costs a start, an end and a share of
+// the joining launch. One row of 131072 positions, 8 kv heads, in 32 / 64 / 128 /
+// 256 / 512 splits (256 .. 4096 workgroups): 50, 54, 55, 65, 84 us; 64 ragged
+// rows up to 4096 in 1 / 2 / 4: 59, 73, 82 us. Heads of 64 have half the bytes in
+// flight per wave and take twice the workgroups.
 struct Plan {
   bool prefill;
   int tile_rows, tiles, split, splits;
@@ -741,7 +804,8 @@ Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
   }
   const int64_t work = (int64_t)pl.tiles * c.heads * b.B;
   const int64_t unit = pl.prefill ? 512 : 64 * kWaves;
-  const int64_t want = std::max<int64_t>(1, (pl.prefill ? 512 : 1024) / std::max<int64_t>(work, 1));
+  const int64_t fill = c.dim <= 64 || pl.prefill ? 512 : 256;
+  const int64_t want = (fill + work - 1) / work;
   const int64_t units = (span + unit - 1) / unit;
   const int64_t per = std::max<int64_t>(1, (units + want - 1) / want);
   pl.split = (int)(per * unit);
@@ -760,9 +824,8 @@ void launch_for(AttnParams p, const Plan& pl, hipStream_t stream) {
     hipLaunchKernelGGL((k_kv8_decode<D, kWaves>), grid, dim3(64 * kWaves), 0, stream, p);
   }
   if (pl.splits > 1) {
-    const int64_t rows = (int64_t)p.b.max_new * p.q.heads;
-    hipLaunchKernelGGL((k_kv8_join<D>), dim3((unsigned)((rows + 3) / 4), 1, (unsigned)p.b.B), dim3(256), 0, stream, p,
-                       pl.splits);
+    hipLaunchKernelGGL((k_kv8_join<D>), dim3((unsigned)((int64_t)p.b.max_new * p.q.heads), (unsigned)p.b.B), dim3(256), 0,
+                       stream, p, pl.splits);
   }
 }
 
