@@ -445,6 +445,22 @@ w4a4_status_t w8a8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, con
 int64_t w8a8_gemm_workspace(int64_t M, int64_t N, int64_t K);
 
 /*
+ * A W8A8 linear layer: w8a8_quantize_act of X, then w8a8_gemm, with the codes
+ * and scales in the workspace.
+ *
+ *   x, x_dtype, ldx  as for w8a8_quantize_act;  wq, ws, bias, y as for w8a8_gemm
+ *   workspace  device memory of at least w8a8_linear_workspace(M, N, K) bytes,
+ *            16-byte aligned, owned by the caller, overwritten
+ */
+w4a4_status_t w8a8_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                          const int8_t* wq, const float* ws, const float* bias, int64_t N,
+                          void* workspace, int64_t workspace_bytes,
+                          void* y, int32_t y_dtype, int64_t ldy, void* stream);
+
+/* Workspace bytes w8a8_linear needs, or -1 for invalid extents. Host-only. */
+int64_t w8a8_linear_workspace(int64_t M, int64_t N, int64_t K);
+
+/*
  * ---- Storage conversions ------------------------------------------------
  * The pages fix no storage layout ("drop-in replacement in unmodified vLLM",
  * APEX4 abstract, asks only that a linear layer's quantized data can be fed

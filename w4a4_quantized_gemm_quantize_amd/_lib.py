@@ -67,6 +67,7 @@ SIGNATURES = {
     "nvfp4_scales_to_rows": [_p, _i64, _i64, _p, _p],
     "w8a8_quantize_act": [_p, _i32, _i64, _i64, _i64, _p, _p, _p],
     "w8a8_pack_weight": [_p, _i32, _i64, _i64, _p, _p, _p],
+    "w8a8_linear": [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _i64, _p, _i64, _p, _i32, _i64, _p],
     "w8a8_gemm": [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _i32, _i64, _p],
     "kv8_append": [_p, _p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _p, *_KV_BATCH, _p],
     "kv8_gather": [_p, _p, _p, _p, *_KV_BATCH, _p, _p, _i32, _p],
@@ -113,8 +114,9 @@ def load_library() -> ctypes.CDLL:
         lib.w4a4_probe_mfma_ops.restype = ctypes.c_int64
         lib.w4a4_gemm_splitk_noalloc_max_bytes.argtypes = []
         lib.w4a4_gemm_splitk_noalloc_max_bytes.restype = ctypes.c_int64
-        lib.w8a8_gemm_workspace.argtypes = [_i64, _i64, _i64]
-        lib.w8a8_gemm_workspace.restype = ctypes.c_int64
+        for name in ("w8a8_gemm_workspace", "w8a8_linear_workspace"):
+            getattr(lib, name).argtypes = [_i64, _i64, _i64]
+            getattr(lib, name).restype = ctypes.c_int64
         lib.kv8_attention_workspace.argtypes = [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i32, _i64]
         lib.kv8_attention_workspace.restype = ctypes.c_int64
         _lib = lib

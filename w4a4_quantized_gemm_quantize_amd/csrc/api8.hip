@@ -136,6 +136,41 @@ w4a4_status_t w8a8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, con
   return launched();
 }
 
+// Codes, then scales, then the GEMM's partial sums, each on a 256-byte boundary.
+static int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
+
+int64_t w8a8_linear_workspace(int64_t M, int64_t N, int64_t K) {
+  const int64_t gemm = w8a8_gemm_workspace(M, N, K);
+  if (gemm < 0) return -1;
+  if (M == 0 || N == 0) return 0;
+  return align256(M * K) + align256(4 * M) + gemm;
+}
+
+w4a4_status_t w8a8_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                          const int8_t* wq, const float* ws, const float* bias, int64_t N,
+                          void* workspace, int64_t workspace_bytes,
+                          void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+  if (!w8_extents_ok(M, N, K) || ldx < K) return W4A4_E_SHAPE;
+  if (!x_dtype_ok(x_dtype) || !y_dtype_ok(y_dtype)) return W4A4_E_DTYPE;
+  if (ldx % 8) return W4A4_E_ALIGN;
+  if (M == 0 || N == 0) return W4A4_OK;
+  if (ldy < N || workspace_bytes < w8a8_linear_workspace(M, N, K)) return W4A4_E_SHAPE;
+  if (!x || !wq || !ws || !y || !workspace) return W4A4_E_NULL;
+  if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(wq, 16) || !aligned(ws, 4) || !aligned(bias, 4) ||
+      !aligned(y, y_dtype == W4A4_Y_F32 ? 4 : 2))
+    return W4A4_E_ALIGN;
+  int8_t* xq = static_cast<int8_t*>(workspace);
+  float* xs = reinterpret_cast<float*>(xq + align256(M * K));
+  w4a4::launch_w8a8_quant(x, x_dtype == W4A4_Y_BF16, M, K, ldx, xq, xs, as_stream(stream));
+  w4a4::W8GemmArgs g = {};
+  g.a = xq; g.sa = xs; g.w = wq; g.sw = ws; g.bias = bias;
+  g.M = M; g.N = N; g.K = K;
+  g.y = y; g.ydtype = y_dtype; g.ldy = ldy;
+  g.workspace = xq + align256(M * K) + align256(4 * M);
+  w4a4::launch_w8a8_gemm(g, as_stream(stream));
+  return launched();
+}
+
 w4a4_status_t kv8_append(const void* k, const void* v, int32_t x_dtype, int64_t k_tok, int64_t k_head,
                          int64_t v_tok, int64_t v_head,
                          int8_t* k_cache, int8_t* v_cache, float* k_scale, float* v_scale,

@@ -807,7 +807,8 @@ Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
   const int64_t fill = c.dim <= 64 || pl.prefill ? 512 : 256;
   const int64_t want = (fill + work - 1) / work;
   const int64_t units = (span + unit - 1) / unit;
-  const int64_t per = std::max<int64_t>(1, (units + want - 1) / want);
+  // a second launch costs more than two chunks per wave
+  const int64_t per = std::max<int64_t>(span <= 512 ? 2 : 1, (units + want - 1) / want);
   pl.split = (int)(per * unit);
   pl.splits = (int)std::max<int64_t>(1, (span + pl.split - 1) / pl.split);
   return pl;

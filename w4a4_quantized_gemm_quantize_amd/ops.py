@@ -6,7 +6,7 @@ here.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 
 import torch
 
@@ -502,11 +502,21 @@ def _same_device(first, **others) -> None:
             raise ValueError(f"{name} is on {t.device}, expected {first.device}")
 
 
-def _device_of(t):
-    """Makes t's device current for the launches, if it is not."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+def _call8(name: str, device, *args) -> None:
+    """Calls an ABI entry point on ``device``'s current stream (passed last), with
+    that device current for the launches."""
+    index = device.index
+    if index == torch.cuda.current_device():
+        call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+    else:
+        with torch.cuda.device(device):
+            call(name, *args, torch._C._cuda_getCurrentRawStream(index))
+
+
+@functools.lru_cache(maxsize=4096)
+def _workspace_size(name: str, *args) -> int:
+    """A host-only workspace query (a function of its integer arguments alone)."""
+    return workspace_bytes(name, *args)
 
 
 def _rows_stride(x, name: str) -> int:
@@ -532,7 +542,7 @@ def _workspace8(workspace, nbytes: int, device):
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
-def _w8_quantize(fn: str, x, out, names):
+def _w8_quantize(x, out, names):
     dt = _x_dtype8(x, names[0])
     ld = _rows_stride(x, names[0])
     M, K = x.shape
@@ -543,21 +553,49 @@ def _w8_quantize(fn: str, x, out, names):
         q, s = out
         _check_out(q, names[1], (M, K), torch.int8, x.device)
         _check_out(s, names[2], (M,), torch.float32, x.device)
-    with _device_of(x):
-        call("w8a8_quantize_act", x.data_ptr(), dt, M, K, ld, q.data_ptr(), s.data_ptr(), _stream(x))
+    _call8("w8a8_quantize_act", x.device, x.data_ptr(), dt, M, K, ld, q.data_ptr(), s.data_ptr())
     return q, s
 
 
 def w8a8_quantize_act(x: torch.Tensor, out=None):
     """Symmetric INT8 quantization per token of fp16 or bf16 X[M, K] (row stride
     may exceed K): ``(xq int8 [M, K], xs float32 [M])``, ``x ~ xq * xs``."""
-    return _w8_quantize("w8a8_quantize_act", x, out, ("x", "xq", "xs"))
+    return _w8_quantize(x, out, ("x", "xq", "xs"))
 
 
 def w8a8_pack_weight(w: torch.Tensor, out=None):
     """Offline INT8 quantization per output channel of fp16 or bf16 W[N, K]:
     ``(wq int8 [N, K], ws float32 [N])``."""
-    return _w8_quantize("w8a8_pack_weight", w, out, ("w", "wq", "ws"))
+    return _w8_quantize(w, out, ("w", "wq", "ws"))
+
+
+def _w8_weights(wq, ws, bias, device):
+    """Checks the weight side of a W8A8 product; returns (N, K)."""
+    _need(wq, torch.int8, "wq")
+    _need(ws, torch.float32, "ws")
+    if wq.dim() != 2 or not wq.is_contiguous() or not ws.is_contiguous():
+        raise ValueError("wq must be a contiguous 2-D tensor and ws contiguous")
+    N, K = wq.shape
+    if ws.shape != (N,):
+        raise ValueError("ws must hold one scale per output channel: shape (N,)")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        if bias.shape != (N,) or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous [N] tensor")
+        if bias.device != device:
+            raise ValueError(f"bias is on {bias.device}, expected {device}")
+    if wq.device != device or ws.device != device:
+        raise ValueError(f"wq is on {wq.device} and ws on {ws.device}, expected {device}")
+    return N, K
+
+
+def _y_out8(out, shape, out_dtype, device, row_stride_ok=True):
+    """The output of an 8-bit call (new, or the caller's, checked) and its dtype code."""
+    if out is None:
+        return torch.empty(shape, dtype=out_dtype, device=device), _y_dtype8(out_dtype)
+    dt = _y_dtype8(out.dtype) if isinstance(out, torch.Tensor) else 0
+    _check_out(out, "out", shape, getattr(out, "dtype", None), device, row_stride_ok=row_stride_ok)
+    return out, dt
 
 
 def w8a8_gemm(xq, xs, wq, ws, bias=None, out_dtype=torch.float32, out=None, workspace=None):
@@ -565,46 +603,42 @@ def w8a8_gemm(xq, xs, wq, ws, bias=None, out_dtype=torch.float32, out=None, work
     The INT8 products are summed exactly. Y is fp32, fp16 or bf16; the
     workspace (K split across workgroups for small outputs) is allocated here
     with torch unless given."""
-    for t, dt, n in ((xq, torch.int8, "xq"), (wq, torch.int8, "wq"),
-                     (xs, torch.float32, "xs"), (ws, torch.float32, "ws")):
-        _need(t, dt, n)
-        if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    if xq.dim() != 2 or wq.dim() != 2:
-        raise ValueError("xq and wq must be 2-D")
-    M, K = xq.shape
-    N = wq.shape[0]
-    if wq.shape[1] != K:
+    _need(xq, torch.int8, "xq")
+    _need(xs, torch.float32, "xs")
+    if xq.dim() != 2 or not xq.is_contiguous() or not xs.is_contiguous():
+        raise ValueError("xq must be a contiguous 2-D tensor and xs contiguous")
+    M = xq.shape[0]
+    N, K = _w8_weights(wq, ws, bias, xq.device)
+    if xq.shape[1] != K:
         raise ValueError("K of xq and wq differ")
-    if tuple(xs.shape) != (M,) or tuple(ws.shape) != (N,):
-        raise ValueError("xs and ws must hold one scale per row: shapes (M,) and (N,)")
-    if bias is not None:
-        _need(bias, torch.float32, "bias")
-        if tuple(bias.shape) != (N,) or not bias.is_contiguous():
-            raise ValueError("bias must be a contiguous [N] tensor")
-    _same_device(xq, xs=xs, wq=wq, ws=ws, bias=bias)
-    if out is None:
-        _y_dtype8(out_dtype)
-        y = torch.empty((M, N), dtype=out_dtype, device=xq.device)
-    else:
-        y = out
-        if isinstance(y, torch.Tensor):
-            _y_dtype8(y.dtype)
-        _check_out(y, "out", (M, N), getattr(y, "dtype", None), xq.device, row_stride_ok=True)
-    held, wptr, wbytes = _workspace8(workspace, workspace_bytes("w8a8_gemm_workspace", M, N, K), xq.device)
-    with _device_of(xq):
-        call("w8a8_gemm", xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
-             0 if bias is None else bias.data_ptr(), M, N, K, wptr, wbytes, y.data_ptr(), _DTYPE8[y.dtype],
-             y.stride(0) if M > 1 else max(N, 1), _stream(xq))
-    del held
+    if xs.shape != (M,):
+        raise ValueError("xs must hold one scale per row: shape (M,)")
+    _same_device(xq, xs=xs)
+    y, dt = _y_out8(out, (M, N), out_dtype, xq.device)
+    held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_gemm_workspace", M, N, K), xq.device)
+    _call8("w8a8_gemm", xq.device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+           0 if bias is None else bias.data_ptr(), M, N, K, wptr, wbytes, y.data_ptr(), dt,
+           y.stride(0) if M > 1 else max(N, 1))
     return y
 
 
 def w8a8_linear(x: torch.Tensor, wq, ws, bias=None, out_dtype=torch.float32, out=None, workspace=None):
-    """A W8A8 linear layer on fp16 or bf16 activations: X quantized per token
-    here, then :func:`w8a8_gemm`."""
-    xq, xs = w8a8_quantize_act(x)
-    return w8a8_gemm(xq, xs, wq, ws, bias=bias, out_dtype=out_dtype, out=out, workspace=workspace)
+    """A W8A8 linear layer on fp16 or bf16 activations [M, K] (row stride may
+    exceed K): X quantized per token, then the product of :func:`w8a8_gemm`, in one
+    call. The workspace (codes, scales, partial sums) is allocated here with
+    torch unless given."""
+    xdt = _x_dtype8(x, "x")
+    ld = _rows_stride(x, "x")
+    M = x.shape[0]
+    N, K = _w8_weights(wq, ws, bias, x.device)
+    if x.shape[1] != K:
+        raise ValueError("K of x and wq differ")
+    y, dt = _y_out8(out, (M, N), out_dtype, x.device)
+    held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_linear_workspace", M, N, K), x.device)
+    _call8("w8a8_linear", x.device, x.data_ptr(), xdt, M, K, ld, wq.data_ptr(), ws.data_ptr(),
+           0 if bias is None else bias.data_ptr(), N, wptr, wbytes, y.data_ptr(), dt,
+           y.stride(0) if M > 1 else max(N, 1))
+    return y
 
 
 # ------------------------------------------------------ INT8 key/value cache
@@ -622,25 +656,30 @@ def kv8_new_cache(num_pages: int, heads: int, page: int, dim: int, device="cuda"
             torch.zeros((num_pages, heads), dtype=torch.float32, device=device))
 
 
-def _kv_pool(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens):
+_KV_TENSORS = (("k_cache", torch.int8), ("v_cache", torch.int8), ("k_scale", torch.float32),
+               ("v_scale", torch.float32), ("block_table", torch.int32), ("cu_seqlens", torch.int32),
+               ("seq_lens", torch.int32))
+
+
+def _kv_pool(*tensors):
     """Checked pool and batch: (pool pointers, pool extents, batch pointers, B)."""
-    for t, dt, n in ((k_cache, torch.int8, "k_cache"), (v_cache, torch.int8, "v_cache"),
-                     (k_scale, torch.float32, "k_scale"), (v_scale, torch.float32, "v_scale"),
-                     (block_table, torch.int32, "block_table"), (cu_seqlens, torch.int32, "cu_seqlens"),
-                     (seq_lens, torch.int32, "seq_lens")):
-        _need(t, dt, n)
+    first = tensors[0]
+    for t, (name, dtype) in zip(tensors, _KV_TENSORS):
+        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
+            _need(t, dtype, name)
         if not t.is_contiguous():
-            raise ValueError(f"{n} must be contiguous")
-    _same_device(k_cache, v_cache=v_cache, k_scale=k_scale, v_scale=v_scale, block_table=block_table,
-                 cu_seqlens=cu_seqlens, seq_lens=seq_lens)
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != first.device:
+            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
+    k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens = tensors
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, heads, page, dim]")
     pages, heads, page, dim = k_cache.shape
-    if tuple(v_cache.shape) != (pages, heads, dim, page):
+    if v_cache.shape != (pages, heads, dim, page):
         raise ValueError("v_cache must be [num_pages, heads, dim, page]")
-    if tuple(k_scale.shape) != (pages, heads) or tuple(v_scale.shape) != (pages, heads):
+    if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
         raise ValueError("k_scale and v_scale must be [num_pages, heads]")
-    if seq_lens.dim() != 1 or tuple(cu_seqlens.shape) != (seq_lens.shape[0] + 1,):
+    if seq_lens.dim() != 1 or cu_seqlens.shape != (seq_lens.shape[0] + 1,):
         raise ValueError("cu_seqlens must be [B + 1] for seq_lens [B]")
     B = seq_lens.shape[0]
     if block_table.dim() != 2 or block_table.shape[0] != B:
@@ -683,9 +722,8 @@ def kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens
     vt, vh = _heads_strides(v, "v", heads, dim)
     if v.shape[0] != k.shape[0]:
         raise ValueError("k and v hold different numbers of tokens")
-    with _device_of(k_cache):
-        call("kv8_append", k.data_ptr(), v.data_ptr(), dt, kt, kh, vt, vh, *ptrs, pages, heads, page, dim, *batch,
-             B, k.shape[0], _need_max(max_new, "max_new"), batch[1] * page, _stream(k_cache))
+    _call8("kv8_append", k_cache.device, k.data_ptr(), v.data_ptr(), dt, kt, kh, vt, vh, *ptrs, pages, heads, page,
+           dim, *batch, B, k.shape[0], _need_max(max_new, "max_new"), batch[1] * page)
 
 
 def kv8_gather(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens, total: int, max_new: int,
@@ -706,9 +744,8 @@ def kv8_gather(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_
             _y_dtype8(k.dtype)
         _check_out(k, "k", shape, getattr(k, "dtype", None), k_cache.device)
         _check_out(v, "v", shape, k.dtype, k_cache.device)
-    with _device_of(k_cache):
-        call("kv8_gather", *ptrs, pages, heads, page, dim, *batch, B, total, _need_max(max_new, "max_new"),
-             batch[1] * page, k.data_ptr(), v.data_ptr(), _DTYPE8[k.dtype], _stream(k_cache))
+    _call8("kv8_gather", k_cache.device, *ptrs, pages, heads, page, dim, *batch, B, total,
+           _need_max(max_new, "max_new"), batch[1] * page, k.data_ptr(), v.data_ptr(), _DTYPE8[k.dtype])
     return k, v
 
 
@@ -740,21 +777,13 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens
     _need_max(max_new, "max_new")
     if _need_max(max_len, "max_len") > batch[1] * page:
         raise ValueError(f"max_len {max_len} is past the block table's {batch[1]} pages of {page}")
-    if out is None:
-        _y_dtype8(out_dtype or q.dtype)
-        y = torch.empty((T, hq, dim), dtype=out_dtype or q.dtype, device=q.device)
-    else:
-        y = out
-        if isinstance(y, torch.Tensor):
-            _y_dtype8(y.dtype)
-        _check_out(y, "out", (T, hq, dim), getattr(y, "dtype", None), q.device)
-    lse = torch.empty((T, hq), dtype=torch.float32, device=q.device) if return_lse else None
-    nbytes = workspace_bytes("kv8_attention_workspace", hq, heads, page, dim, B, T, max_new, max_len, int(causal),
-                             window)
-    held, wptr, wbytes = _workspace8(workspace, nbytes, q.device)
-    with _device_of(q):
-        call("kv8_attention", q.data_ptr(), dt, qt, qh, hq, *ptrs, pages, heads, page, dim, *batch, B, T, max_new,
-             max_len, dim ** -0.5 if scale is None else scale, int(causal), window, wptr, wbytes, y.data_ptr(),
-             _DTYPE8[y.dtype], 0 if lse is None else lse.data_ptr(), _stream(q))
-    del held
+    device = q.device
+    y, ydt = _y_out8(out, (T, hq, dim), out_dtype or q.dtype, device, row_stride_ok=False)
+    lse = torch.empty((T, hq), dtype=torch.float32, device=device) if return_lse else None
+    causal = int(causal)
+    held, wptr, wbytes = _workspace8(workspace, _workspace_size(
+        "kv8_attention_workspace", hq, heads, page, dim, B, T, max_new, max_len, causal, window), device)
+    _call8("kv8_attention", device, q.data_ptr(), dt, qt, qh, hq, *ptrs, pages, heads, page, dim, *batch, B, T,
+           max_new, max_len, dim ** -0.5 if scale is None else scale, causal, window, wptr, wbytes, y.data_ptr(),
+           ydt, 0 if lse is None else lse.data_ptr())
     return (y, lse) if return_lse else y
