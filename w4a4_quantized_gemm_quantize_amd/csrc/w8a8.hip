@@ -12,7 +12,7 @@
 
 #include "device.h"
 #include "launch.h"
-#include "quant_common.h"
+#include "quant8.h"
 
 namespace w4a4 {
 
@@ -22,55 +22,6 @@ typedef int v16i __attribute__((ext_vector_type(16)));
 
 constexpr int kThreads = 256;
 constexpr int kCUs = 256;      // of an MI355X: launch shapes are planned for it
-
-// The fp32 value of the low / high 16-bit half of w.
-template <bool BF>
-__device__ __forceinline__ float lo_f32(uint32_t w) {
-  if constexpr (BF) return __uint_as_float(w << 16);
-  return (float)__builtin_bit_cast(h2, w).x;
-}
-template <bool BF>
-__device__ __forceinline__ float hi_f32(uint32_t w) {
-  if constexpr (BF) return __uint_as_float(w & 0xFFFF0000u);
-  return (float)__builtin_bit_cast(h2, w).y;
-}
-
-// max |x| over the 16 values of two 16-byte words. The magnitude bits of both
-// formats order as integers.
-__device__ __forceinline__ uint32_t absmax16(const uint4 r[2], uint32_t m) {
-  typedef unsigned short us2 __attribute__((ext_vector_type(2)));
-  const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const us2 v = __builtin_bit_cast(us2, w[i] & 0x7FFF7FFFu);
-    m = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(us2, m), v));
-  }
-  return m;
-}
-
-// The codes of 16 values. x / s is q0 = x r, e = fma(-q0, s, x),
-// fma(e, r, q0) with r = RN(1/s): RN(x/s) (the correction of quant_common.h).
-// k scales x (1, or a power of two that keeps a subnormal s out of the
-// divisions; s and r are scaled alike). Adding 1.5 2^23 rounds to nearest even
-// and leaves the two's-complement code in the low byte.
-template <bool BF>
-__device__ __forceinline__ uint4 codes16(const uint4 r[2], float k, float s, float rs) {
-  const uint32_t w[8] = {r[0].x, r[0].y, r[0].z, r[0].w, r[1].x, r[1].y, r[1].z, r[1].w};
-  uint32_t o[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t b[4];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      b[2 * i] = __float_as_uint(div_rn(lo_f32<BF>(w[2 * j + i]) * k, s, rs) + 12582912.0f);
-      b[2 * i + 1] = __float_as_uint(div_rn(hi_f32<BF>(w[2 * j + i]) * k, s, rs) + 12582912.0f);
-    }
-    const uint32_t p01 = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);
-    const uint32_t p23 = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
-    o[j] = p01 | p23;
-  }
-  return uint4{o[0], o[1], o[2], o[3]};
-}
 
 // One row per WPR waves (256 / (64 WPR) rows a workgroup); NC > 0: the row's
 // 16-element chunks stay in registers (NC per lane), so X is read once. NC = 0:
@@ -106,8 +57,7 @@ __global__ __launch_bounds__(kThreads) void k_w8a8_quant(const uint16_t* __restr
       m = absmax16(r, m);
     }
   }
-  const uint32_t mm = max(m & 0xFFFFu, m >> 16);
-  float a = group_max<64>(BF ? __uint_as_float(mm << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)mm));
+  float a = group_max<64>(absmax_value<BF>(m));
   if constexpr (WPR > 1) {
     if (lane == 0) wave_max[wave] = __float_as_uint(a);
     __syncthreads();
@@ -116,7 +66,7 @@ __global__ __launch_bounds__(kThreads) void k_w8a8_quant(const uint16_t* __restr
   }
   if (!live) return;
   const float sc = a / 127.0f;                     // correctly rounded
-  const float k = BF && sc < 0x1p-60f ? 0x1p80f : 1.0f;
+  const float k = BF ? scale_guard(sc) : 1.0f;     // fp16 scales are 0 or >= 2^-31
   const float sk = sc * k;
   const float rs = sc == 0.0f ? 0.0f : 1.0f / sk;
   uint4* dst = reinterpret_cast<uint4*>(q + row * K);
