@@ -11,7 +11,7 @@
  *   k_scale, v_scale  f32 [num_pages][heads]
  * A key is k_scale * code, a value v_scale * code.
  *   page: 16, 32, 64, 128 or 256; dim: 64, 128, 192 or 256; caches 16-byte
- *   aligned, scales 4-byte aligned.
+ *   aligned, scales 4-byte aligned; heads <= 16384.
  *
  * The batch. B sequences packed along T tokens:
  *   block_table  int32 [B][table_ld]: the page of positions page * j ..
@@ -23,6 +23,7 @@
  *                its n new tokens are positions seq_lens[b] - n .. seq_lens[b] - 1
  *   max_new      at least every sequence's number of new tokens
  *   max_len      at least every seq_lens[b], at most table_ld * page
+ *   B <= 65535; T and max_len < 2^28
  * These four are read on the device: nothing synchronizes, and a captured call
  * follows the values at replay. A longer sequence than max_new or max_len says is
  * cut short; tokens at negative positions (n > seq_lens[b]) are not stored, read

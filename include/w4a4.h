@@ -412,7 +412,7 @@ w4a4_status_t nvfp4_gemm_debug_partials(const uint8_t* xq, const uint8_t* xs,
  *
  *   x       [M][ldx] row-major, 16-byte aligned, ldx >= K, ldx % 8 == 0, of
  *           x_dtype W4A4_Y_F16 or W4A4_Y_BF16
- *   M, K    K > 0, K % 16 == 0, K <= 2^30, M < 2^31
+ *   M, K    K > 0, K % 16 == 0, K <= 2^30, M < 2^24
  *   xq      out: int8 [M][K], 16-byte aligned;  xs  out: f32 [M]
  */
 w4a4_status_t w8a8_quantize_act(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
@@ -429,7 +429,7 @@ w4a4_status_t w8a8_pack_weight(const void* w, int32_t w_dtype, int64_t N, int64_
  *
  *   xq, wq   int8 [M][K], [N][K] (any code, -128 included), 16-byte aligned
  *   xs, ws   f32 [M], [N];  bias  f32 [N] or NULL
- *   M, N, K  M, N >= 0, < 2^31; K > 0, K % 16 == 0, K <= 131056
+ *   M, N, K  M, N >= 0, < 2^24; K > 0, K % 16 == 0, K <= 131056
  *   y        out: [M][ldy] fp32, fp16 or bf16, ldy >= N, aligned to its element
  *   workspace  device memory of at least w8a8_gemm_workspace(M, N, K) bytes,
  *            16-byte aligned, owned by the caller, overwritten; may be NULL

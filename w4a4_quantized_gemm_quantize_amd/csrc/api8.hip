@@ -30,18 +30,25 @@ bool x_dtype_ok(int32_t t) { return t == W4A4_Y_F16 || t == W4A4_Y_BF16; }
 // Longest K of the W8A8 GEMM: 128^2 K < 2^31, a multiple of 16.
 constexpr int64_t kMaxW8K = 131056;
 
+// Most rows: one workgroup of 256 threads per row stays within a launch's 2^32.
+constexpr int64_t kMaxW8Rows = int64_t{1} << 24;
+
 bool w8_extents_ok(int64_t M, int64_t N, int64_t K) {
-  return M >= 0 && N >= 0 && M <= kMaxI32 && N <= kMaxI32 && K > 0 && K % 16 == 0 && K <= kMaxW8K;
+  return M >= 0 && N >= 0 && M < kMaxW8Rows && N < kMaxW8Rows && K > 0 && K % 16 == 0 && K <= kMaxW8K;
 }
+
+// Tokens of a batch, positions of a sequence: 16-position pages times 256
+// threads stay within a launch's 2^32 threads.
+constexpr int64_t kMaxTokens = int64_t{1} << 28;
 
 // The pool's and the batch's extents.
 bool kv_extents_ok(int64_t num_pages, int32_t heads, int32_t page, int32_t dim, int64_t table_ld, int64_t B, int64_t T,
                    int64_t max_new, int64_t max_len) {
-  if (num_pages < 0 || num_pages > kMaxI32 || heads <= 0 || heads > 65535) return false;
+  if (num_pages < 0 || num_pages > kMaxI32 || heads <= 0 || heads > 16384) return false;
   if (page < 16 || page > 256 || (page & (page - 1))) return false;
   if (dim < 64 || dim > 256 || dim % 64) return false;
-  if (B < 0 || B > 65535 || T < 0 || T > kMaxI32) return false;
-  if (max_new < 0 || max_new > kMaxI32 || max_len < 0 || max_len > kMaxI32 - 512) return false;
+  if (B < 0 || B > 65535 || T < 0 || T >= kMaxTokens) return false;
+  if (max_new < 0 || max_new > kMaxI32 || max_len < 0 || max_len >= kMaxTokens) return false;
   return table_ld >= 0 && table_ld <= kMaxI32 && max_len <= table_ld * page;
 }
 
@@ -93,7 +100,7 @@ extern "C" {
 w4a4_status_t w8a8_quantize_act(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
                                 int8_t* xq, float* xs, void* stream) {
   if (!x_dtype_ok(x_dtype)) return W4A4_E_DTYPE;
-  if (M < 0 || M > kMaxI32 || K <= 0 || K % 16 || K > (int64_t{1} << 30) || ldx < K) return W4A4_E_SHAPE;
+  if (M < 0 || M >= kMaxW8Rows || K <= 0 || K % 16 || K > (int64_t{1} << 30) || ldx < K) return W4A4_E_SHAPE;
   if (ldx % 8) return W4A4_E_ALIGN;
   if (M == 0) return W4A4_OK;
   if (!x || !xq || !xs) return W4A4_E_NULL;
@@ -262,7 +269,7 @@ w4a4_status_t kv8_attention(const void* q, int32_t x_dtype, int64_t q_tok, int64
   a.window = window < max_len ? (int)window : 0;   // a window of every position is none
   a.y = y; a.ydtype = y_dtype; a.lse = lse;
   const int64_t need = w4a4::kv8_attention_workspace(c, b, a);
-  if (workspace_bytes < need) return W4A4_E_SHAPE;
+  if (need < 0 || workspace_bytes < need) return W4A4_E_SHAPE;
   if (need > 0 && !workspace) return W4A4_E_NULL;
   if (need > 0 && !aligned(workspace, 16)) return W4A4_E_ALIGN;
   if (num_pages == 0) b.max_len = 0;               // no page to read: every query sees nothing

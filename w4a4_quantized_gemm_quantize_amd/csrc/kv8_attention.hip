@@ -59,7 +59,8 @@ struct AttnParams {
   KvBatch b;
   KvQuery q;
   int group;             // query heads per kv head
-  int tile_rows;         // query rows per workgroup
+  int tile_rows, tiles;  // query rows per workgroup, row tiles of the longest sequence
+  int splits;
   int split;             // positions per split (a multiple of 64 times the waves)
   float* part;           // splits' results: [splits][T heads][dim] then [splits][T heads][2]
   int64_t part_rows;     // T heads
@@ -67,16 +68,18 @@ struct AttnParams {
 
 typedef float v16f __attribute__((ext_vector_type(16)));
 
-// One query row of D elements over LANES-strided owners: qf[i] holds elements
-// dim(i) .. dim(i) + 7. bf16 rows are scaled by a power of two, returned as the
-// factor that undoes it. XOR: the lane distances over which the row's other
-// elements lie (16 and 32, or 32 alone). A negative softmax scale is moved into
-// the queries (flip), so that every factor of a score is >= 0.
-template <int N, int FIRST_XOR, typename Dim>
-__device__ __forceinline__ float load_query(const uint16_t* qp, bool bf16, bool flip, Dim dim, v8h (&qf)[N]) {
-  uint4 raw[N];
+// One query row of D elements, a lane holding N pieces of 8: loads, and later the
+// fp16 operands. bf16 rows are scaled by a power of two, returned as the factor
+// that undoes it; the row's other elements lie FIRST_XOR .. 32 lanes away. A
+// negative softmax scale is moved into the queries (flip), so that every factor
+// of a score is >= 0.
+template <int N, typename Dim>
+__device__ __forceinline__ void load_query(const uint16_t* qp, Dim dim, uint4 (&raw)[N]) {
 #pragma unroll
   for (int i = 0; i < N; ++i) raw[i] = *reinterpret_cast<const uint4*>(qp + dim(i));
+}
+template <int N, int FIRST_XOR>
+__device__ __forceinline__ float query_operands(uint4 (&raw)[N], bool bf16, bool flip, v8h (&qf)[N]) {
   const uint32_t sign = flip ? 0x80008000u : 0u;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -137,6 +140,24 @@ __device__ __forceinline__ Range tile_range(const AttnParams& p, const Seq& s, i
   return r;
 }
 
+// A workgroup's work: row tile `tile` of (sequence, kv head, split), the heads
+// innermost: where they are a multiple of 8, the tiles of one head run on one
+// XCD (workgroup index mod 8), whose L2 fetches its codes once.
+struct Work {
+  int seq, h, split, tile;
+};
+__device__ __forceinline__ Work work_of(const AttnParams& p) {
+  unsigned x = blockIdx.x;
+  Work w;
+  w.h = x % p.c.heads;
+  x /= p.c.heads;
+  w.tile = x % p.tiles;
+  x /= p.tiles;
+  w.split = x % p.splits;
+  w.seq = x / p.splits;
+  return w;
+}
+
 // Few query rows per kv head: a workgroup of NW waves takes 16 rows (token,
 // query head of the group) of one kv head and a split of the positions; its
 // waves take chunks of 64 positions in turn, with no sharing until the end.
@@ -148,29 +169,27 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
   __shared__ float lm[NW][16], ll[NW][16];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int c = lane & 15, g = lane >> 4;
-  const int seq = blockIdx.z;
-  const int h = blockIdx.x % p.c.heads, tile = blockIdx.x / p.c.heads;
+  const Work w = work_of(p);
+  const int seq = w.seq, h = w.h, tile = w.tile;
   const Seq s = sequence(p.b, seq);
   const int rows = s.n * p.group;
   const int r0 = tile * 16;
   if (r0 >= rows) return;
   const Range rg = tile_range(p, s, r0, min(r0 + 16, rows));
   const int nsplit = max(1, (rg.hi - rg.lo + p.split - 1) / p.split);
-  if ((int)blockIdx.y >= nsplit) return;
-  const int from = rg.lo + blockIdx.y * p.split, to = min(rg.hi, from + p.split);
+  if (w.split >= nsplit) return;
+  const int from = rg.lo + w.split * p.split, to = min(rg.hi, from + p.split);
 
   // query row of this lane's column
   const int r = min(r0 + c, rows - 1);
   const int tok = r / p.group, hq = h * p.group + r % p.group;
   const int pos = s.len - s.n + tok;
-  const int row_hi = p.q.causal ? min(s.len, pos + 1) : s.len;
-  const int row_lo = p.q.window > 0 ? max(0, pos - p.q.window + 1) : 0;
-  v8h qf[2 * DB];
-  const float qscale =
-      fabsf(p.q.scale) * kLog2e *
-      load_query<2 * DB, 16>(static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head,
-                             p.q.bf16, p.q.scale < 0.0f, [&](int i) { return 64 * (i >> 1) + 16 * g + 8 * (i & 1); }, qf);
-
+  auto hi_of = [&](int x) { return p.q.causal ? min(s.len, x + 1) : s.len; };
+  auto lo_of = [&](int x) { return p.q.window > 0 ? max(0, x - p.q.window + 1) : 0; };
+  const int row_hi = hi_of(pos), row_lo = lo_of(pos);
+  // positions that every row of the tile sees
+  const int all_hi = min(hi_of(s.len - s.n + r0 / p.group), to);
+  const int all_lo = lo_of(s.len - s.n + min(r0 + 15, rows - 1) / p.group);
   const int P = p.c.page;
   const int* const table = p.b.table + seq * p.b.table_ld;
   const uint32_t page_bytes = (uint32_t)p.c.heads * P * D;     // < 2^32
@@ -215,12 +234,18 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
   for (int i = 0; i < DT; ++i) acc[i] = v4f{0, 0, 0, 0};
   float m = kNone, l = 0.0f, vref = kTinyScale;
 
-  if (from + 64 * wave < to) {
-    load_pages(from + 64 * wave);
+  uint4 raw[2 * DB];
+  const bool work = from + 64 * wave < to;
+  if (work) load_pages(from + 64 * wave);
+  load_query<2 * DB>(static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head,
+                     [&](int i) { return 64 * (i >> 1) + 16 * g + 8 * (i & 1); }, raw);
+  if (work) {
     load_k(from + 64 * wave);
     load_pages(from + 64 * (wave + NW));
     load_v();
   }
+  v8h qf[2 * DB];
+  const float qscale = fabsf(p.q.scale) * kLog2e * query_operands<2 * DB, 16>(raw, p.q.bf16, p.q.scale < 0.0f, qf);
   for (int at = from + 64 * wave; at < to; at += 64 * NW) {
     ks = ks_next;
     vs = vs_next;
@@ -241,16 +266,27 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
       load_pages(at + 128 * NW);
     }
     const float f = ks * qscale;
-    const int first = at + 16 * g, lim = ok ? min(row_hi, to) : 0;
+    const int first = at + 16 * g;
     float cm = kNone;
+    if (at >= all_lo && at + 64 <= all_hi && __all(ok)) {
 #pragma unroll
-    for (int t = 0; t < 4; ++t)
+      for (int t = 0; t < 4; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int j = first + 4 * t + i;
-        sc[t][i] = j >= row_lo && j < lim ? sc[t][i] * f : -INFINITY;
-        cm = fmaxf(cm, sc[t][i]);
-      }
+        for (int i = 0; i < 4; ++i) {
+          sc[t][i] *= f;
+          cm = fmaxf(cm, sc[t][i]);
+        }
+    } else {
+      const int lim = ok ? min(row_hi, to) : 0;
+#pragma unroll
+      for (int t = 0; t < 4; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int j = first + 4 * t + i;
+          sc[t][i] = j >= row_lo && j < lim ? sc[t][i] * f : -INFINITY;
+          cm = fmaxf(cm, sc[t][i]);
+        }
+    }
     cm = fmaxf(cm, __shfl_xor(cm, 16));
     cm = max_halves(cm);
     // a block past the last position or of no page: its scale must not count
@@ -270,12 +306,16 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
         l += e;
         pf[t >> 1][4 * (t & 1) + i] = (_Float16)(e * w);
       }
+    if (__any(m2 != m) || vref2 != vref) {
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) acc[i][k] *= ao;
+    }
     m = m2;
     vref = vref2;
 #pragma unroll
     for (int i = 0; i < DT; ++i) {
-#pragma unroll
-      for (int k = 0; k < 4; ++k) acc[i][k] *= ao;
       acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(vr[i].x, vr[i].y), pf[0], acc[i], 0, 0, 0);
       acc[i] = __builtin_amdgcn_mfma_f32_16x16x32_f16(widen8(vr[i].z, vr[i].w), pf[1], acc[i], 0, 0, 0);
     }
@@ -313,10 +353,10 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
       store_as(p.q.y, p.q.ydtype, (t * p.q.heads + head) * D + d, L == 0.0f ? 0.0f : o / L);
       if (p.q.lse && d == 0) p.q.lse[t * p.q.heads + head] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
     } else {
-      const int64_t row = blockIdx.y * p.part_rows + t * p.q.heads + head;
+      const int64_t row = w.split * p.part_rows + t * p.q.heads + head;
       p.part[row * D + d] = o;
       if (d == 0) {
-        float* ml = p.part + (int64_t)gridDim.y * p.part_rows * D + 2 * row;
+        float* ml = p.part + (int64_t)p.splits * p.part_rows * D + 2 * row;
         ml[0] = M;
         ml[1] = L;
       }
@@ -365,18 +405,17 @@ void k_kv8_prefill(AttnParams p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int l32 = lane & 31, hi = lane >> 5;
-  const int seq = blockIdx.z;
-  const int ntile = gridDim.x / p.c.heads;
+  const Work w = work_of(p);
   // late rows see the most positions: they start first
-  const int h = blockIdx.x % p.c.heads, tile = ntile - 1 - blockIdx.x / p.c.heads;
+  const int seq = w.seq, h = w.h, tile = p.tiles - 1 - w.tile;
   const Seq s = sequence(p.b, seq);
   const int rows = s.n * p.group;
   const int r0 = tile * ROWS;
   if (r0 >= rows) return;
   const Range rg = tile_range(p, s, r0, min(r0 + ROWS, rows));
   const int nsplit = max(1, (rg.hi - rg.lo + p.split - 1) / p.split);
-  if ((int)blockIdx.y >= nsplit) return;
-  const int from = rg.lo + blockIdx.y * p.split, to = min(rg.hi, from + p.split);
+  if (w.split >= nsplit) return;
+  const int from = rg.lo + w.split * p.split, to = min(rg.hi, from + p.split);
 
   // this lane's query row, and the positions its wave's rows see
   const int wr0 = r0 + 32 * (wave % (NW / DS)), d0 = wave / (NW / DS) * (D / DS);
@@ -389,10 +428,13 @@ void k_kv8_prefill(AttnParams p) {
   const int tok_b = __builtin_amdgcn_readfirstlane(min(wr0 + 31, rows - 1) / p.group);
   const int hi_min = row_hi(tok_a), hi_max = row_hi(tok_b), lo_min = row_lo(tok_a), lo_max = row_lo(tok_b);
   v8h qf[ST];
-  const float qscale =
-      fabsf(p.q.scale) * kLog2e *
-      load_query<ST, 32>(static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head,
-                         p.q.bf16, p.q.scale < 0.0f, [&](int i) { return 16 * i + 8 * hi; }, qf);
+  float qscale = fabsf(p.q.scale) * kLog2e;
+  {
+    uint4 raw[ST];
+    load_query<ST>(static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head,
+                   [&](int i) { return 16 * i + 8 * hi; }, raw);
+    qscale *= query_operands<ST, 32>(raw, p.q.bf16, p.q.scale < 0.0f, qf);
+  }
 
   const int P = p.c.page;
   // piece i of this thread: K codes 16 (x % (D / 16)) .. of position x / (D /
@@ -704,7 +746,7 @@ void k_kv8_prefill(AttnParams p) {
       }
     if (p.q.lse && hi == 0 && d0 == 0) p.q.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) / kLog2e;
   } else {
-    const int64_t at = blockIdx.y * p.part_rows + row;
+    const int64_t at = w.split * p.part_rows + row;
 #pragma unroll
     for (int i = 0; i < DT; ++i)
 #pragma unroll
@@ -712,7 +754,7 @@ void k_kv8_prefill(AttnParams p) {
         *reinterpret_cast<float4*>(p.part + at * D + d0 + 32 * i + 8 * k + 4 * hi) =
             float4{acc[i][4 * k] * back, acc[i][4 * k + 1] * back, acc[i][4 * k + 2] * back, acc[i][4 * k + 3] * back};
     if (hi == 0 && d0 == 0) {
-      float* ml = p.part + (int64_t)gridDim.y * p.part_rows * D + 2 * at;
+      float* ml = p.part + (int64_t)p.splits * p.part_rows * D + 2 * at;
       ml[0] = m;
       ml[1] = l;
     }
@@ -722,7 +764,7 @@ void k_kv8_prefill(AttnParams p) {
 // Joins the splits of a query row: a workgroup per row, 4 dimensions per thread,
 // the threads' groups taking the splits in turn and meeting in LDS.
 template <int D>
-__global__ __launch_bounds__(256) void k_kv8_join(AttnParams p, int splits) {
+__global__ __launch_bounds__(256) void k_kv8_join(AttnParams p) {
   constexpr int TPS = D / 4, G = 256 / TPS;            // threads per split, splits at a time
   __shared__ float so[G][D];
   __shared__ float sm[G], sl[G];
@@ -737,7 +779,7 @@ __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p, int splits) {
   const int64_t t = s.t0 + r / p.group;
   const int head = h * p.group + r % p.group;
   const int64_t row = t * p.q.heads + head;
-  const float* ml = p.part + (int64_t)splits * p.part_rows * D;
+  const float* ml = p.part + (int64_t)p.splits * p.part_rows * D;
   const int g = threadIdx.x / TPS, d = threadIdx.x % TPS * 4;
   float M = kNone, L = 0.0f;
   v4f o = {0, 0, 0, 0};
@@ -789,6 +831,7 @@ constexpr int kWaves = 4;                  // of k_kv8_decode
 struct Plan {
   bool prefill;
   int tile_rows, tiles, split, splits;
+  int64_t blocks;
 };
 Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
   Plan pl;
@@ -811,12 +854,13 @@ Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
   const int64_t per = std::max<int64_t>(span <= 512 ? 2 : 1, (units + want - 1) / want);
   pl.split = (int)(per * unit);
   pl.splits = (int)std::max<int64_t>(1, (span + pl.split - 1) / pl.split);
+  pl.blocks = (int64_t)c.heads * pl.tiles * pl.splits * b.B;
   return pl;
 }
 
 template <int D>
 void launch_for(AttnParams p, const Plan& pl, hipStream_t stream) {
-  const dim3 grid((unsigned)(pl.tiles * p.c.heads), (unsigned)pl.splits, (unsigned)p.b.B);
+  const dim3 grid((unsigned)pl.blocks);
   if (pl.prefill) {
     constexpr int DS = D > 128 ? 2 : 1;
     if (p.c.page >= 64) hipLaunchKernelGGL((k_kv8_prefill<D, 8, DS, true>), grid, dim3(512), 0, stream, p);
@@ -826,7 +870,7 @@ void launch_for(AttnParams p, const Plan& pl, hipStream_t stream) {
   }
   if (pl.splits > 1) {
     hipLaunchKernelGGL((k_kv8_join<D>), dim3((unsigned)((int64_t)p.b.max_new * p.q.heads), (unsigned)p.b.B), dim3(256), 0,
-                       stream, p, pl.splits);
+                       stream, p);
   }
 }
 
@@ -834,6 +878,9 @@ void launch_for(AttnParams p, const Plan& pl, hipStream_t stream) {
 
 int64_t kv8_attention_workspace(const KvPool& c, const KvBatch& b, const KvQuery& q) {
   const Plan pl = plan(c, b, q);
+  // more threads than a launch can have
+  if (pl.blocks >= (int64_t{1} << 32) / 512 || (pl.splits > 1 && (int64_t)b.max_new * q.heads >= (int64_t{1} << 32) / 256))
+    return -1;
   return pl.splits > 1 ? (int64_t)pl.splits * b.T * q.heads * (c.dim + 2) * 4 : 0;
 }
 
@@ -845,6 +892,8 @@ void launch_kv8_attention(const KvPool& c, const KvBatch& b, const KvQuery& q, v
   p.q = q;
   p.group = q.heads / c.heads;
   p.tile_rows = pl.tile_rows;
+  p.tiles = pl.tiles;
+  p.splits = pl.splits;
   p.split = pl.split;
   p.part = static_cast<float*>(workspace);
   p.part_rows = (int64_t)b.T * q.heads;
