@@ -167,7 +167,8 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
   constexpr int DB = D / 64, DT = D / 16;
   __shared__ float lo_[NW][16][D + 4];
   __shared__ float lm[NW][16], ll[NW][16];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const Work w = work_of(p);
   const int seq = w.seq, h = w.h, tile = w.tile;
