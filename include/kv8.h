@@ -25,8 +25,8 @@
  *   max_len      at least every seq_lens[b], at most table_ld * page
  *   B <= 65535; T and max_len < 2^28
  * These four are read on the device: nothing synchronizes, and a captured call
- * follows the values at replay. A longer sequence than max_new or max_len says is
- * cut short; tokens at negative positions (n > seq_lens[b]) are not stored, read
+ * follows the values at replay. More new tokens than max_new are read as max_new,
+ * a length above max_len as max_len, so that no access leaves the tensors; tokens at negative positions (n > seq_lens[b]) are not stored, read
  * as zeros and see nothing; table entries that are no page of the pool are
  * skipped (not stored, read as zeros, masked). Table entries past a sequence's
  * last position are never read. Tokens of the packed tensors that belong to no

@@ -59,7 +59,7 @@ __device__ __forceinline__ Slots slots_of(const KvPool& c, const KvBatch& b, con
   j = (first >> c.log_page) + block;
   Slots r;
   r.lo = max(first - j * c.page, 0);
-  r.hi = min(min(s.len, p0 + min(s.n, b.max_new)) - j * c.page, c.page);   // no more tokens than announced
+  r.hi = min(s.len - j * c.page, c.page);
   r.t = s.t0 + ((int64_t)j * c.page - p0);
   r.any = s.n > 0 && r.hi > r.lo;
   return r;
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(kThreads) void k_kv8_gather(KvPool c, KvBatch b, vo
   void* y = is_v ? vo : ko;
   auto row = [&](int64_t t) { return (t * c.heads + h) * D; };
   if (blockIdx.x == 0) {                            // tokens before position 0 read as zeros
-    const int none = min(max(s.n - s.len, 0), min(s.n, b.max_new));
+    const int none = max(s.n - s.len, 0);
     for (int i = tid; i < none * PPT; i += kThreads)
       store16<YT>(y, row(s.t0 + i / PPT) + i % PPT * 16, uint4{0, 0, 0, 0}, 0.0f);
   }
@@ -271,10 +271,11 @@ __global__ __launch_bounds__(kThreads) void k_kv8_gather(KvPool c, KvBatch b, vo
   }
 }
 
-// Pages that a sequence's max_new new tokens can touch.
+// Pages that a sequence's max_new new tokens can touch; 1 at least, whose
+// workgroups read tokens without a position.
 unsigned page_span(const KvPool& c, const KvBatch& b) {
   const int64_t span = ((int64_t)b.max_new + c.page - 2) / c.page + 1;
-  return (unsigned)std::min<int64_t>(span, ((int64_t)b.max_len + c.page - 1) / c.page);
+  return (unsigned)std::max<int64_t>(1, std::min<int64_t>(span, ((int64_t)b.max_len + c.page - 1) / c.page));
 }
 
 unsigned lds_bytes(const KvPool& c) { return (unsigned)(c.page * (c.dim + 4)); }   // <= 66560

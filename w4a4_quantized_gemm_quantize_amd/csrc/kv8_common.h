@@ -11,14 +11,15 @@ typedef _Float16 v8h __attribute__((ext_vector_type(8)));
 
 // A sequence of the batch: its n new tokens are tokens t0 .. t0 + n - 1 of the
 // packed tensors and the last n of its len cached positions. Device values out
-// of range (a cu_seqlens that runs backwards or past T, a length past the
-// table or max_len) are cut, so no access leaves the caller's tensors.
+// of range (a cu_seqlens that runs backwards or past T, more new tokens than
+// max_new, a length past the table or max_len) are cut, so no access leaves the
+// caller's tensors or the workspace, whose size follows from the same bounds.
 struct Seq {
   int t0, n, len;
 };
 __device__ __forceinline__ Seq sequence(const KvBatch& b, int i) {
   const int a = min(max(b.cu[i], 0), b.T), e = min(max(b.cu[i + 1], 0), b.T);
-  return Seq{a, max(e - a, 0), min(max(b.lens[i], 0), b.max_len)};
+  return Seq{a, min(max(e - a, 0), b.max_new), min(max(b.lens[i], 0), b.max_len)};
 }
 
 // The page of a position, or -1 if the table's entry is no page of the pool.
