@@ -128,43 +128,39 @@ __device__ __forceinline__ void store_y(void* y, int ydt, int64_t i, float v) {
 }
 
 // ---- Up to 16 tokens: W streamed once from HBM straight into the operands -----
-// A workgroup of NW waves owns 16 TN columns and splits K across its waves
+// A workgroup of NW waves owns 16 channels and splits K across its waves
 // (contiguous runs of 64-k steps). v_mfma_i32_16x16x64_i8: lane l supplies 16
 // consecutive k of row l % 16 at k offset 16 (l / 16), so a step is one 16-byte
 // load per operand and lane, with no LDS on the way; RING steps are in flight
-// per wave. The waves' int32 sums meet in LDS (exact in any order). K is a
-// multiple of 16: the last step's lanes beyond K read zeros.
-// Bound by the W stream, and with many tokens by the L2 traffic of their codes,
-// which every workgroup reads again (M / (16 TN) of W's bytes): see launch.
-template <int TN, int NW, int RING>
+// per wave (8 measured as 4). The waves' int32 sums meet in LDS (exact in any
+// order). K is a multiple of 16: the last step's lanes beyond K read zeros.
+// Bound by the W stream: one token 4096 -> 128256 86.9 us, 6.0 TB/s of weights;
+// 8192 x 28672 46 us, 5.1 TB/s; small ones by the launch and the loads' latency
+// (8192 x 1024, 8 MB: 6.8 us). With more tokens by the L2 traffic of their
+// codes, which every workgroup reads again (M / 16 of W's bytes): see the plan.
+template <int NW, int RING>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
-  __shared__ int red[NW - 1][TN * 4][64];
+  __shared__ int red[NW - 1][4][64];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16 * TN;
+  const int n0 = (int)blockIdx.x * 16;
   const int steps = (p.K + 63) >> 6;
   const int h0 = (int)((int64_t)steps * wave / NW), h1 = (int)((int64_t)steps * (wave + 1) / NW);
-  const int w_rows = min(16 * TN, p.N - n0);
+  const int w_rows = min(16, p.N - n0);
   const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, p.M * p.K);
   const __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w + (int64_t)n0 * p.K, w_rows * p.K);
   const int offA = c < p.M ? c * p.K + 16 * g : kDroppedOffset;
-  int offW[TN];
-#pragma unroll
-  for (int j = 0; j < TN; ++j) offW[j] = 16 * j + c < w_rows ? (16 * j + c) * p.K + 16 * g : kDroppedOffset;
+  const int offW = c < w_rows ? c * p.K + 16 * g : kDroppedOffset;
   struct Step {
-    v4i a, w[TN];
+    v4i a, w;
   };
   auto load = [&](Step& st, int h) {
     const int out = 64 * h + 16 * g < p.K ? 0 : kDroppedOffset;
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-      st.w[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, offW[j] | out, 64 * h, 0));
+    st.w = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, offW | out, 64 * h, 0));
     st.a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, offA | out, 64 * h, 0));
   };
-  v4i acc[TN];
-#pragma unroll
-  for (int j = 0; j < TN; ++j) acc[j] = v4i{0, 0, 0, 0};
+  v4i acc = {0, 0, 0, 0};
   Step ring[RING];
 #pragma unroll
   for (int u = 0; u < RING; ++u)
@@ -173,34 +169,27 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
 #pragma unroll
     for (int u = 0; u < RING; ++u) {
       if (h + u < h1) {
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-          acc[j] = __builtin_amdgcn_mfma_i32_16x16x64_i8(ring[u].a, ring[u].w[j], acc[j], 0, 0, 0);
+        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(ring[u].a, ring[u].w, acc, 0, 0, 0);
         if (h + u + RING < h1) load(ring[u], h + u + RING);
       }
     }
   }
   if (wave > 0) {
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int r = 0; r < 4; ++r) red[wave - 1][j * 4 + r][lane] = acc[j][r];
+    for (int r = 0; r < 4; ++r) red[wave - 1][r][lane] = acc[r];
   }
   __syncthreads();
   if (wave != 0) return;
+  const int n = n0 + c;
+  const float sw = n < p.N ? p.sw[n] : 0.0f;
+  const float b = p.bias && n < p.N ? p.bias[n] : 0.0f;
 #pragma unroll
-  for (int j = 0; j < TN; ++j) {
-    const int n = n0 + 16 * j + c;
-    const float sw = n < p.N ? p.sw[n] : 0.0f;
-    const float b = p.bias && n < p.N ? p.bias[n] : 0.0f;
+  for (int r = 0; r < 4; ++r) {
+    int v = acc[r];
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      int v = acc[j][r];
-#pragma unroll
-      for (int w = 0; w < NW - 1; ++w) v += red[w][j * 4 + r][lane];
-      const int m = 4 * g + r;
-      if (m < p.M && n < p.N) store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, p.sa[m], sw, b));
-    }
+    for (int w = 0; w < NW - 1; ++w) v += red[w][r][lane];
+    const int m = 4 * g + r;
+    if (m < p.M && n < p.N) store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, p.sa[m], sw, b));
   }
 }
 
@@ -580,9 +569,14 @@ void launch_tiles(W8Params p, int splits, hipStream_t stream) {
 
 // Which kernel, and into how many K ranges.
 //
-// Up to 16 tokens the W stream decides (k_w8a8_gemm_small). Above, the tile
-// whose estimated time is least: rounds of tiles over the CUs times (stages x
-// the tile's time per 128-k stage + its start and output). The times (us) are
+// Up to 16 tokens the W stream decides (k_w8a8_gemm_small), but that kernel's
+// workgroups each read all tokens' codes: with more than 8 tokens and W above
+// 64 MiB 128-channel tiles take over, which read them 8 times less often (16 x
+// 28672 x 8192: 53.5 us, 60 in the small kernel; 16 x 8192 x 28672: 47 and 54;
+// 16 x 18944 x 3584: 19.5 and 22.4; below, 16 x 8192 x 8192: 21.8 and 20.1; all
+// with W from HBM). Above 16 tokens, the tile
+// whose estimated time is least: rounds of tiles over the CUs times (stages x the
+// tile's time per 128-k stage + its start and output). The times (us) are
 // measured ones: 256 x 256 tiles 1.15 a stage with every CU busy (4096 x 4096
 // x 8192 119 us), 256 x 128 0.8 (2048 x 4096 x 11008: 88 us; 256 x 256 tiles
 // 114, 128 x 128 105), 128 x 128 0.5 (512 x 8192 x 8192: 39 us; 45 and 74 with
@@ -594,7 +588,7 @@ struct W8Plan {
   int tile, splits;
 };
 W8Plan plan_w8a8(int64_t M, int64_t N, int64_t K) {
-  if (M <= 16) return W8Plan{TILE_SMALL, 1};
+  if (M <= 8 || (M <= 16 && N * K <= (int64_t{1} << 26))) return W8Plan{TILE_SMALL, 1};
   const int64_t nk = (K + 127) / 128;
   W8Plan best{TILE_256, 1};
   double best_us = 1e30;
@@ -643,15 +637,13 @@ void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream) {
   const W8Plan pl = plan_w8a8(a.M, a.N, a.K);
   switch (pl.tile) {
     case TILE_SMALL: {
-      // More columns per workgroup cut the tokens' L2 traffic and leave fewer
-      // workgroups. 16 x 8192 x 28672 (us): TN = 1 53.6, 2 41.9, 4 67.3; 16 x
-      // 28672 x 8192: 52.2, 55.8, 44.0; one token 4096 -> 11008: 9.3, 10.9, 12.8.
-#define W8A8_SMALL(TN, NW, RING)                                                                           \
-  hipLaunchKernelGGL((k_w8a8_gemm_small<TN, NW, RING>), dim3((unsigned)((a.N + 16 * TN - 1) / (16 * TN))), \
-                     dim3(64 * NW), 0, stream, p)
-      if (a.M > 4 && a.N >= 16384) W8A8_SMALL(4, 4, 2);
-      else if (a.M > 4 && a.N >= 8192) W8A8_SMALL(2, 8, 4);
-      else W8A8_SMALL(1, 8, 4);
+      // 4 waves a workgroup where its count fills the CUs twice over, else 8 (one
+      // token, W from HBM, us: 8192 x 8192 14.0 with 4 and 15.1 with 8, 4096 x
+      // 11008 13.4 and 11.1, 1024 x 8192 9.2 and 6.8).
+#define W8A8_SMALL(NW) \
+  hipLaunchKernelGGL((k_w8a8_gemm_small<NW, 4>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * NW), 0, stream, p)
+      if (a.N >= 32 * kCUs) W8A8_SMALL(4);
+      else W8A8_SMALL(8);
 #undef W8A8_SMALL
       return;
     }
