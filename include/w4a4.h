@@ -445,12 +445,13 @@ w4a4_status_t w8a8_gemm(const int8_t* xq, const float* xs, const int8_t* wq, con
 int64_t w8a8_gemm_workspace(int64_t M, int64_t N, int64_t K);
 
 /*
- * A W8A8 linear layer: w8a8_quantize_act of X, then w8a8_gemm, with the codes
- * and scales in the workspace.
+ * A W8A8 linear layer: the result of w8a8_quantize_act of X, then w8a8_gemm, with
+ * the codes and scales in the workspace (few tokens: one launch without one).
  *
  *   x, x_dtype, ldx  as for w8a8_quantize_act;  wq, ws, bias, y as for w8a8_gemm
  *   workspace  device memory of at least w8a8_linear_workspace(M, N, K) bytes,
- *            16-byte aligned, owned by the caller, overwritten
+ *            16-byte aligned, owned by the caller, overwritten; may be NULL
+ *            when that size is 0
  */
 w4a4_status_t w8a8_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
                           const int8_t* wq, const float* ws, const float* bias, int64_t N,

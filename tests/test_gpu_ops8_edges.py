@@ -49,6 +49,27 @@ def test_linear_reads_strided_rows_and_broadcast_ones():
             assert torch.equal(o.w8a8_linear(same, wq, ws), o.w8a8_linear(x, wq, ws))
 
 
+@pytest.mark.parametrize("M,N,K", [(1, 1, 16), (1, 16, 1024), (1, 17, 1040), (3, 100, 2064), (2, 8193, 4112),
+                                   (4, 9000, 4096), (16, 40, 2000), (7, 300, 4096), (1, 500, 32768), (16, 8200, 1008)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_few_tokens_quantized_where_they_are_used(M, N, K, dtype):
+    """The linear layer of few tokens (one launch) against its two steps, rows of
+    zeros, of wide range and strided ones included."""
+    import torch
+    o = ops()
+    g = torch.Generator(device="cuda").manual_seed(M + N + K)
+    wide = torch.randn(M, K + 8, generator=g, device="cuda") * 2.0 ** (torch.arange(M, device="cuda") - M // 2)[:, None]
+    x = wide.to(getattr(torch, dtype))[:, :K]
+    x[M // 2] = 0
+    x[0, K - 1] = 30.0
+    wq, ws = o.w8a8_pack_weight(torch.randn(N, K, generator=g, device="cuda").half())
+    b = torch.randn(N, generator=g, device="cuda")
+    y = o.w8a8_linear(x, wq, ws, bias=b, out_dtype=torch.float32)
+    q, s = o.w8a8_quantize_act(x)
+    assert torch.equal(y, o.w8a8_gemm(q, s, wq, ws, bias=b))
+    check_y(y, q, s, wq, ws, b)
+
+
 def test_linear_rows_of_zeros_give_the_bias():
     import torch
     o = ops()

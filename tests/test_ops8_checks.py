@@ -44,15 +44,16 @@ def test_gemm_validation():
 
 
 def test_linear_validation():
-    f = lambda x=P, xdt=F16, M=4, K=64, ldx=64, wq=P, ws=P, bias=None, N=4, wsp=P, wb=1 << 30, y=P, ydt=F16, ldy=4: \
+    f = lambda x=P, xdt=F16, M=32, K=64, ldx=64, wq=P, ws=P, bias=None, N=4, wsp=P, wb=1 << 30, y=P, ydt=F16, ldy=4: \
         _lib.status_of("w8a8_linear", x, xdt, M, K, ldx, wq, ws, bias, N, wsp, wb, y, ydt, ldy, None)
     assert f(K=72) == E_SHAPE and f(M=-1) == E_SHAPE and f(ldx=56) == E_SHAPE and f(ldy=3) == E_SHAPE
     assert f(xdt=F32) == E_DTYPE and f(ydt=9) == E_DTYPE
     assert f(ldx=68) == E_ALIGN and f(x=P + 8) == E_ALIGN and f(wsp=P + 8) == E_ALIGN and f(bias=P + 2) == E_ALIGN
     assert f(x=None) == E_NULL and f(wq=None) == E_NULL and f(wsp=None) == E_NULL and f(y=None) == E_NULL
     assert f(x=None, wsp=None, wb=0, M=0) == OK and f(N=0) == OK
-    need = _lib.load_library().w8a8_linear_workspace(4, 4, 64)
-    assert need >= 4 * 64 + 4 * 4 and f(wb=need - 1) == E_SHAPE
+    need = _lib.load_library().w8a8_linear_workspace(32, 4, 64)
+    assert need >= 32 * 64 + 4 * 32 and f(wb=need - 1) == E_SHAPE
+    assert _lib.load_library().w8a8_linear_workspace(1, 4, 64) == 0      # one launch, which keeps nothing
     assert _lib.load_library().w8a8_linear_workspace(4, 4, 72) == -1
 
 

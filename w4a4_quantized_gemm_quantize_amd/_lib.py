@@ -141,7 +141,7 @@ def workspace_bytes(name: str, *args) -> int:
 
 def call(name: str, *args) -> None:
     """Call an ABI entry point; raise W4A4Error on a non-OK status."""
-    lib = load_library()
+    lib = _lib or load_library()
     st = getattr(lib, name)(*args)
     if st != W4A4_OK:
         raise W4A4Error(name, st, lib.w4a4_status_str(st).decode())

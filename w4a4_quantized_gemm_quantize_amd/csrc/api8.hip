@@ -149,7 +149,7 @@ static int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
 int64_t w8a8_linear_workspace(int64_t M, int64_t N, int64_t K) {
   const int64_t gemm = w8a8_gemm_workspace(M, N, K);
   if (gemm < 0) return -1;
-  if (M == 0 || N == 0) return 0;
+  if (M == 0 || N == 0 || w4a4::w8a8_one_launch(M, N, K)) return 0;
   return align256(M * K) + align256(4 * M) + gemm;
 }
 
@@ -161,18 +161,24 @@ w4a4_status_t w8a8_linear(const void* x, int32_t x_dtype, int64_t M, int64_t K, 
   if (!x_dtype_ok(x_dtype) || !y_dtype_ok(y_dtype)) return W4A4_E_DTYPE;
   if (ldx % 8) return W4A4_E_ALIGN;
   if (M == 0 || N == 0) return W4A4_OK;
-  if (ldy < N || workspace_bytes < w8a8_linear_workspace(M, N, K)) return W4A4_E_SHAPE;
-  if (!x || !wq || !ws || !y || !workspace) return W4A4_E_NULL;
-  if (!aligned(x, 16) || !aligned(workspace, 16) || !aligned(wq, 16) || !aligned(ws, 4) || !aligned(bias, 4) ||
+  const int64_t need = w8a8_linear_workspace(M, N, K);
+  if (ldy < N || workspace_bytes < need) return W4A4_E_SHAPE;
+  if (!x || !wq || !ws || !y || (need > 0 && !workspace)) return W4A4_E_NULL;
+  if (!aligned(x, 16) || (need > 0 && !aligned(workspace, 16)) || !aligned(wq, 16) || !aligned(ws, 4) || !aligned(bias, 4) ||
       !aligned(y, y_dtype == W4A4_Y_F32 ? 4 : 2))
     return W4A4_E_ALIGN;
+  w4a4::W8GemmArgs g = {};
+  g.w = wq; g.sw = ws; g.bias = bias;
+  g.M = M; g.N = N; g.K = K;
+  g.y = y; g.ydtype = y_dtype; g.ldy = ldy;
+  if (need == 0) {
+    w4a4::launch_w8a8_small(g, x, x_dtype == W4A4_Y_BF16, ldx, as_stream(stream));
+    return launched();
+  }
   int8_t* xq = static_cast<int8_t*>(workspace);
   float* xs = reinterpret_cast<float*>(xq + align256(M * K));
   w4a4::launch_w8a8_quant(x, x_dtype == W4A4_Y_BF16, M, K, ldx, xq, xs, as_stream(stream));
-  w4a4::W8GemmArgs g = {};
-  g.a = xq; g.sa = xs; g.w = wq; g.sw = ws; g.bias = bias;
-  g.M = M; g.N = N; g.K = K;
-  g.y = y; g.ydtype = y_dtype; g.ldy = ldy;
+  g.a = xq; g.sa = xs;
   g.workspace = xq + align256(M * K) + align256(4 * M);
   w4a4::launch_w8a8_gemm(g, as_stream(stream));
   return launched();

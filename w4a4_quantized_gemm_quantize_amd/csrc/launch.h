@@ -92,6 +92,10 @@ struct W8GemmArgs {
 };
 int64_t w8a8_workspace(int64_t M, int64_t N, int64_t K);
 void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream);
+// A linear layer of few tokens in one launch that quantizes them itself: where
+// it is taken, and the launch (a.a and a.sa are not used).
+bool w8a8_one_launch(int64_t M, int64_t N, int64_t K);
+void launch_w8a8_small(const W8GemmArgs& a, const void* x, int bf16, int64_t ldx, hipStream_t stream);
 
 // ---- INT8 key/value cache (kv8_cache.hip, kv8_attention.hip)
 struct KvPool {

@@ -100,6 +100,8 @@ void launch_quant(const uint16_t* x, int64_t M, int64_t K, int64_t ldx, int8_t* 
 }
 
 struct W8Params {
+  const uint16_t* x;          // k_w8a8_gemm_small with XT > 0: the tokens themselves
+  int64_t ldx;
   const int8_t* a;
   const float* sa;
   const int8_t* w;
@@ -132,15 +134,27 @@ __device__ __forceinline__ void store_y(void* y, int ydt, int64_t i, float v) {
 // (contiguous runs of 64-k steps). v_mfma_i32_16x16x64_i8: lane l supplies 16
 // consecutive k of row l % 16 at k offset 16 (l / 16), so a step is one 16-byte
 // load per operand and lane, with no LDS on the way; RING steps are in flight
-// per wave (8 measured as 4). The waves' int32 sums meet in LDS (exact in any
-// order). K is a multiple of 16: the last step's lanes beyond K read zeros.
+// per wave. The waves' int32 sums meet in LDS (exact in any order). K is a
+// multiple of 16: the last step's lanes beyond K, and steps beyond a wave's
+// run, read zeros of W.
+//
+// XT 0: the tokens' codes come from memory. XT 1, 2 (fp16, bf16 tokens): every
+// workgroup quantizes all of them itself, in pieces of 1024 elements per wave
+// (PIECES each, kept in registers), into LDS, while its first W loads are on
+// their way; that saves a launch and the wait for it.
+//
 // Bound by the W stream: one token 4096 -> 128256 86.9 us, 6.0 TB/s of weights;
-// 8192 x 28672 46 us, 5.1 TB/s; small ones by the launch and the loads' latency
-// (8192 x 1024, 8 MB: 6.8 us). With more tokens by the L2 traffic of their
-// codes, which every workgroup reads again (M / 16 of W's bytes): see the plan.
-template <int NW, int RING>
+// 8192 -> 28672 43.7 us, 5.4 TB/s; small ones by the launch and the loads'
+// latency (8192 -> 1024, 8 MB: 7.6 us). With more tokens by the L2 traffic of
+// their codes, which every workgroup reads again (M / 16 of W's bytes): see the
+// plan. RING 8 measured as 4.
+template <int XT, int NW, int RING, int PIECES>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
+  constexpr bool BF = XT == 2;
   __shared__ int red[NW - 1][4][64];
+  __shared__ float row_scale[16];
+  __shared__ uint32_t row_max[16];
+  extern __shared__ __align__(16) uint8_t codes[];     // XT > 0: [M][K rounded up to 64]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
@@ -148,30 +162,69 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
   const int steps = (p.K + 63) >> 6;
   const int h0 = (int)((int64_t)steps * wave / NW), h1 = (int)((int64_t)steps * (wave + 1) / NW);
   const int w_rows = min(16, p.N - n0);
-  const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, p.M * p.K);
+  const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, XT ? 0 : p.M * p.K);
   const __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w + (int64_t)n0 * p.K, w_rows * p.K);
   const int offA = c < p.M ? c * p.K + 16 * g : kDroppedOffset;
   const int offW = c < w_rows ? c * p.K + 16 * g : kDroppedOffset;
   struct Step {
     v4i a, w;
   };
-  auto load = [&](Step& st, int h) {
-    const int out = 64 * h + 16 * g < p.K ? 0 : kDroppedOffset;
-    st.w = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, offW | out, 64 * h, 0));
-    st.a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, offA | out, 64 * h, 0));
-  };
-  v4i acc = {0, 0, 0, 0};
   Step ring[RING];
+  auto load = [&](Step& st, int h) {
+    const int out = h < h1 && 64 * h + 16 * g < p.K ? 0 : kDroppedOffset;
+    st.w = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, offW | out, 64 * h, 0));
+    if constexpr (XT == 0)
+      st.a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, offA | out, 64 * h, 0));
+  };
+  const int KP = steps * 64;
+  if constexpr (XT > 0) {
+    if (threadIdx.x < 16) row_max[threadIdx.x] = 0;
+    const int per_row = (p.K + 1023) >> 10, pieces = p.M * per_row;
+    uint4 raw[PIECES][2];
+    int row[PIECES], k[PIECES];                          // this lane's first element
 #pragma unroll
-  for (int u = 0; u < RING; ++u)
-    if (h0 + u < h1) load(ring[u], h0 + u);
+    for (int i = 0; i < PIECES; ++i) {
+      const int at = wave + NW * i;
+      row[i] = at < pieces ? at / per_row : 0;
+      k[i] = at < pieces ? (at - row[i] * per_row) * 1024 + 16 * lane : p.K;
+      const uint4* src = reinterpret_cast<const uint4*>(p.x + row[i] * p.ldx + min(k[i], p.K - 16));
+      raw[i][0] = src[0];
+      raw[i][1] = src[1];
+    }
+#pragma unroll
+    for (int u = 0; u < RING; ++u) load(ring[u], h0 + u);
+    __syncthreads();                                     // row_max is cleared
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const float a = group_max<64>(k[i] < p.K ? absmax_value<BF>(absmax16(raw[i], 0)) : 0.0f);
+      if (lane == 0) atomicMax(&row_max[row[i]], __float_as_uint(a));   // of values >= 0: their bits order alike
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < PIECES; ++i) {
+      const float sc = __uint_as_float(row_max[row[i]]) / 127.0f;
+      const float kk = BF ? scale_guard(sc) : 1.0f;
+      const float sk = sc * kk;
+      const float rs = sc == 0.0f ? 0.0f : 1.0f / sk;
+      if (k[i] < p.K) {
+        *reinterpret_cast<uint4*>(codes + row[i] * KP + k[i]) = codes16<BF>(raw[i], kk, sk, rs);
+        if (k[i] == 0) row_scale[row[i]] = sc;
+      }
+    }
+    __syncthreads();
+  } else {
+#pragma unroll
+    for (int u = 0; u < RING; ++u) load(ring[u], h0 + u);
+  }
+  const uint8_t* const la = codes + (c < p.M ? c : 0) * KP + 16 * g;   // rows past M: their sums are not stored
+  v4i acc = {0, 0, 0, 0};
   for (int h = h0; h < h1; h += RING) {
 #pragma unroll
     for (int u = 0; u < RING; ++u) {
-      if (h + u < h1) {
-        acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(ring[u].a, ring[u].w, acc, 0, 0, 0);
-        if (h + u + RING < h1) load(ring[u], h + u + RING);
-      }
+      v4i a = ring[u].a;
+      if constexpr (XT > 0) a = *reinterpret_cast<const v4i*>(la + 64 * min(h + u, steps - 1));
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, ring[u].w, acc, 0, 0, 0);
+      load(ring[u], h + u + RING);
     }
   }
   if (wave > 0) {
@@ -189,7 +242,7 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
 #pragma unroll
     for (int w = 0; w < NW - 1; ++w) v += red[w][r][lane];
     const int m = 4 * g + r;
-    if (m < p.M && n < p.N) store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, p.sa[m], sw, b));
+    if (m < p.M && n < p.N) store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, XT ? row_scale[m] : p.sa[m], sw, b));
   }
 }
 
@@ -618,8 +671,10 @@ void launch_w8a8_quant(const void* x, int bf16, int64_t M, int64_t K, int64_t ld
   else launch_quant<false>(xp, M, K, ldx, q, s, stream);
 }
 
-void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream) {
-  W8Params p;
+namespace {
+
+W8Params params(const W8GemmArgs& a) {
+  W8Params p = {};
   p.a = a.a;
   p.sa = a.sa;
   p.w = a.w;
@@ -631,22 +686,37 @@ void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream) {
   p.y = a.y;
   p.ydtype = a.ydtype;
   p.ldy = a.ldy;
-  p.part = nullptr;
   p.splits = 1;
-  p.stages = 0;
+  return p;
+}
+
+// 4 waves a workgroup where its count fills the CUs twice over, else 8 (one
+// token, W from HBM, us: 8192 x 8192 14.0 with 4 and 15.1 with 8, 4096 x 11008
+// 13.4 and 11.1, 1024 x 8192 9.2 and 6.8).
+bool four_waves(int64_t N) { return N >= 32 * kCUs; }
+
+template <int XT, int PIECES>
+void launch_small(const W8Params& p, hipStream_t stream) {
+  const dim3 grid((unsigned)((p.N + 15) / 16));
+  const unsigned lds = XT ? (unsigned)(p.M * ((p.K + 63) / 64 * 64)) : 0;
+  if (four_waves(p.N)) hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 4, 4, PIECES>), grid, dim3(256), lds, stream, p);
+  else hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 8, 4, PIECES>), grid, dim3(512), lds, stream, p);
+}
+
+// Pieces of 1024 elements per wave that a workgroup of k_w8a8_gemm_small has to
+// quantize for all tokens.
+int64_t pieces_per_wave(int64_t M, int64_t N, int64_t K) {
+  const int64_t nw = four_waves(N) ? 4 : 8;
+  return (M * ((K + 1023) / 1024) + nw - 1) / nw;
+}
+
+}  // namespace
+
+void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream) {
+  W8Params p = params(a);
   const W8Plan pl = plan_w8a8(a.M, a.N, a.K);
   switch (pl.tile) {
-    case TILE_SMALL: {
-      // 4 waves a workgroup where its count fills the CUs twice over, else 8 (one
-      // token, W from HBM, us: 8192 x 8192 14.0 with 4 and 15.1 with 8, 4096 x
-      // 11008 13.4 and 11.1, 1024 x 8192 9.2 and 6.8).
-#define W8A8_SMALL(NW) \
-  hipLaunchKernelGGL((k_w8a8_gemm_small<NW, 4>), dim3((unsigned)((a.N + 15) / 16)), dim3(64 * NW), 0, stream, p)
-      if (a.N >= 32 * kCUs) W8A8_SMALL(4);
-      else W8A8_SMALL(8);
-#undef W8A8_SMALL
-      return;
-    }
+    case TILE_SMALL: launch_small<0, 0>(p, stream); return;
     case TILE_256: launch_tiles<256, 256, 2, 4, 2, false>(p, 1, stream); return;
     case TILE_256_128: launch_tiles<256, 128, 4, 2, 3, false>(p, 1, stream); return;
     default:
@@ -654,6 +724,27 @@ void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream) {
       launch_tiles<128, 128, 2, 2, 3, true>(p, pl.splits, stream);
       return;
   }
+}
+
+// Every workgroup quantizes all tokens, so it pays up to 4 pieces a wave (W
+// from HBM, us, one launch and two): 1 x 11008 x 4096 10.6 and 14.2, 1 x 28672 x
+// 8192 43.7 and 47.5, 4 x 11008 x 4096 (4 pieces) 13.0 and 16.3, 8 x 4096 x 4096
+// (4) 10.1 and 9.8; with 7 and 8 pieces 1 x 8192 x 28672 47.0 and 46.7, 8 x 8192
+// x 4096 14.9 and 13.6.
+bool w8a8_one_launch(int64_t M, int64_t N, int64_t K) {
+  return plan_w8a8(M, N, K).tile == TILE_SMALL && pieces_per_wave(M, N, K) <= 4;
+}
+
+void launch_w8a8_small(const W8GemmArgs& a, const void* x, int bf16, int64_t ldx, hipStream_t stream) {
+  W8Params p = params(a);
+  p.x = static_cast<const uint16_t*>(x);
+  p.ldx = ldx;
+  const int64_t pieces = pieces_per_wave(a.M, a.N, a.K);
+#define W8A8_SMALL(PIECES) bf16 ? launch_small<2, PIECES>(p, stream) : launch_small<1, PIECES>(p, stream)
+  if (pieces <= 1) W8A8_SMALL(1);
+  else if (pieces <= 2) W8A8_SMALL(2);
+  else W8A8_SMALL(4);
+#undef W8A8_SMALL
 }
 
 int64_t w8a8_workspace(int64_t M, int64_t N, int64_t K) {

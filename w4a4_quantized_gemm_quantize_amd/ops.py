@@ -506,7 +506,7 @@ def _call8(name: str, device, *args) -> None:
     """Calls an ABI entry point on ``device``'s current stream (passed last), with
     that device current for the launches."""
     index = device.index
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         call(name, *args, torch._C._cuda_getCurrentRawStream(index))
     else:
         with torch.cuda.device(device):
@@ -659,19 +659,37 @@ def kv8_new_cache(num_pages: int, heads: int, page: int, dim: int, device="cuda"
 _KV_TENSORS = (("k_cache", torch.int8), ("v_cache", torch.int8), ("k_scale", torch.float32),
                ("v_scale", torch.float32), ("block_table", torch.int32), ("cu_seqlens", torch.int32),
                ("seq_lens", torch.int32))
+_I8, _F32, _I32 = torch.int8, torch.float32, torch.int32
+
+
+def _kv_refuse(tensors):
+    """Raises for the first tensor of a pool or batch that a kernel cannot take."""
+    device = next((t.device for t in tensors if isinstance(t, torch.Tensor)), None)
+    for t, (name, dtype) in zip(tensors, _KV_TENSORS):
+        _need(t, dtype, name)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
 
 
 def _kv_pool(*tensors):
     """Checked pool and batch: (pool pointers, pool extents, batch pointers, B)."""
-    first = tensors[0]
-    for t, (name, dtype) in zip(tensors, _KV_TENSORS):
-        if not isinstance(t, torch.Tensor) or t.dtype is not dtype or not t.is_cuda:
-            _need(t, dtype, name)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if t.device != first.device:
-            raise ValueError(f"{name} is on {t.device}, expected {first.device}")
     k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens = tensors
+    try:                                               # the checks of _kv_refuse, at a third of its time
+        at = k_cache.get_device()
+        fine = (at >= 0 and k_cache.dtype is _I8 and v_cache.dtype is _I8 and k_scale.dtype is _F32 and
+                v_scale.dtype is _F32 and block_table.dtype is _I32 and cu_seqlens.dtype is _I32 and
+                seq_lens.dtype is _I32 and
+                at == v_cache.get_device() == k_scale.get_device() == v_scale.get_device() ==
+                block_table.get_device() == cu_seqlens.get_device() == seq_lens.get_device() and
+                k_cache.is_contiguous() and v_cache.is_contiguous() and k_scale.is_contiguous() and
+                v_scale.is_contiguous() and block_table.is_contiguous() and cu_seqlens.is_contiguous() and
+                seq_lens.is_contiguous())
+    except AttributeError:                             # not a tensor
+        fine = False
+    if not fine:
+        _kv_refuse(tensors)
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, heads, page, dim]")
     pages, heads, page, dim = k_cache.shape
