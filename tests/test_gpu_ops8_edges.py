@@ -129,11 +129,40 @@ def test_quantize_one_long_row_and_the_largest_values():
 # --------------------------------------------------------------------- cache
 
 @pytest.mark.parametrize("scale", [-0.11, 0.0, -30.0])
-@pytest.mark.parametrize("new,lens", [([1, 2], [700, 40]), ([1], [5000]), ([120, 3], [300, 77])])
+@pytest.mark.parametrize("new,lens", [([1, 2], [700, 40]), ([1], [5000]), ([9, 5], [300, 77]), ([120, 3], [300, 77])])
 @pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
 def test_softmax_scales_of_any_sign(scale, new, lens, dtype):
     B = Batch(new, lens, 2, 128, 64, dtype, seed=31)
     check(B, 6, scale=scale, window=0 if lens[0] % 2 == 0 else 50)
+
+
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 1), (True, 50), (False, 40), (True, 700)])
+@pytest.mark.parametrize("new,lens,heads,kv", [([9, 3], [600, 3], 6, 2), ([5, 0, 4], [70, 33, 9], 28, 4), ([17], [17], 1, 1),
+                                               ([8, 6], [5000, 260], 8, 1), ([32, 10], [1500, 900], 8, 2),
+                                               ([100, 128], [2000, 600], 3, 3)])
+@pytest.mark.parametrize("dim,page,dtype", [(64, 16, "float16"), (128, 32, "bfloat16"), (128, 256, "float16")])
+def test_17_to_128_rows_per_kv_head(new, lens, heads, kv, causal, window, dim, page, dtype):
+    B = Batch(new, lens, kv, dim, page, dtype, seed=39 + len(lens))
+    check(B, heads, causal=causal, window=window, scale=-0.1 if window == 50 else None)
+
+
+def test_bad_pages_and_nan_rows_of_drafts():
+    import torch
+    B = Batch([9, 6], [300, 130], 2, 128, 32, seed=40)
+    B.table_host[0, 2], B.table_host[0, 9], B.table_host[1, 0] = 1 << 29, -1, B.kc.shape[0]
+    B.table = B.table_host.cuda()
+    ref = Batch([9, 6], [300, 130], 2, 128, 32, seed=40)
+    q = B.rand(8)
+    y = ops().kv8_attention(q, *B.pool, B.max_new, B.max_len)
+    o, _, bound = attention_ref(ref, q, True, 0, 128 ** -0.5, {0: [(64, 96), (288, 300)], 1: [(0, 32)]})
+    t = B.cu_host[-1]
+    assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -10 * o.abs() + 2.0 ** -24)[:t]).all())
+    q[3, 5] = float("nan")
+    z = ops().kv8_attention(q, *B.pool, B.max_new, B.max_len)
+    keep = torch.ones(B.total, 8, dtype=torch.bool)
+    keep[3, 5] = False
+    keep[t:] = False
+    assert bool(torch.isnan(z[3, 5]).all()) and torch.equal(z[keep.cuda()], y[keep.cuda()])
 
 
 @pytest.mark.parametrize("new", [1, 5, 90])

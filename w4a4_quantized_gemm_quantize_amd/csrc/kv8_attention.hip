@@ -158,6 +158,45 @@ __device__ __forceinline__ Work work_of(const AttnParams& p) {
   return w;
 }
 
+// The end of a workgroup whose NW waves hold partial results of the same R query
+// rows (unnormalized sums, running maximum, sum of weights): the rows' outputs,
+// or the split's part for k_kv8_join.
+template <int D, int NW, int R>
+__device__ __forceinline__ void join_waves(const AttnParams& p, const Seq& s, const Work& wk, int r0, int rows, int nsplit,
+                                           const float (&lo_)[NW][R][D + 4], const float (&lm)[NW][R],
+                                           const float (&ll)[NW][R]) {
+  const int h = wk.h;
+  __syncthreads();
+  for (int i = threadIdx.x; i < R * D; i += 64 * NW) {
+    const int rr = i / D, d = i % D;
+    if (r0 + rr >= rows) continue;
+    float M = kNone;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, lm[w][rr]);
+    float L = 0.0f, o = 0.0f;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const float e = __builtin_amdgcn_exp2f(lm[w][rr] - M);
+      L += ll[w][rr] * e;
+      o += lo_[w][rr][d] * e;
+    }
+    const int64_t t = s.t0 + (r0 + rr) / p.group;
+    const int head = h * p.group + (r0 + rr) % p.group;
+    if (nsplit == 1) {
+      store_as(p.q.y, p.q.ydtype, (t * p.q.heads + head) * D + d, L == 0.0f ? 0.0f : o / L);
+      if (p.q.lse && d == 0) p.q.lse[t * p.q.heads + head] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
+    } else {
+      const int64_t row = wk.split * p.part_rows + t * p.q.heads + head;
+      p.part[row * D + d] = o;
+      if (d == 0) {
+        float* ml = p.part + (int64_t)p.splits * p.part_rows * D + 2 * row;
+        ml[0] = M;
+        ml[1] = L;
+      }
+    }
+  }
+}
+
 // Few query rows per kv head: a workgroup of NW waves takes 16 rows (token,
 // query head of the group) of one kv head and a split of the positions; its
 // waves take chunks of 64 positions in turn, with no sharing until the end.
@@ -334,35 +373,201 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
   for (int i = 0; i < DT; ++i)
 #pragma unroll
     for (int k = 0; k < 4; ++k) lo_[wave][c][16 * i + 4 * g + k] = acc[i][k] * back;
-  __syncthreads();
-  for (int i = threadIdx.x; i < 16 * D; i += 64 * NW) {
-    const int rr = i / D, d = i % D;
-    if (r0 + rr >= rows) continue;
-    float M = kNone;
+  join_waves<D, NW, 16>(p, s, w, r0, rows, nsplit, lo_, lm, ll);
+}
+
+// 17 to 128 rows per kv head (drafts being verified, chunks of a few tokens): as k_kv8_decode with 32 rows a workgroup, so that a code is widened
+// for twice the rows. S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_f16:
+// lane l supplies 8 consecutive k of row l % 32 at k offset 8 (l / 32), result
+// register i of lane half hi is row 8 (i / 4) + 4 hi + i % 4. A chunk's 64
+// positions are two tiles T; that row is position 32 T + 16 hi + i, so a lane
+// ends up with the scores of 16 consecutive positions per tile, the k indices
+// that the second product wants in it. The dimensions are summed in the order of
+// the codes in memory: lane half hi takes dimensions hi D / 2 and up.
+template <int D, int NW>
+__global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_kv8_draft(AttnParams p) {
+  constexpr int KB = D / 32, DT = D / 32;              // 16-byte pieces of a half row of K, 32-dimension tiles of O
+  __shared__ __align__(16) float lo_[NW][32][D + 4];
+  __shared__ float lm[NW][32], ll[NW][32];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int c = lane & 31, hi = lane >> 5;
+  const Work w = work_of(p);
+  const int seq = w.seq, h = w.h;
+  const Seq s = sequence(p.b, seq);
+  const int rows = s.n * p.group;
+  const int r0 = w.tile * 32;
+  if (r0 >= rows) return;
+  const Range rg = tile_range(p, s, r0, min(r0 + 32, rows));
+  const int nsplit = max(1, (rg.hi - rg.lo + p.split - 1) / p.split);
+  if (w.split >= nsplit) return;
+  const int from = rg.lo + w.split * p.split, to = min(rg.hi, from + p.split);
+
+  const int r = min(r0 + c, rows - 1);
+  const int tok = r / p.group, hq = h * p.group + r % p.group;
+  const int pos = s.len - s.n + tok;
+  auto hi_of = [&](int x) { return p.q.causal ? min(s.len, x + 1) : s.len; };
+  auto lo_of = [&](int x) { return p.q.window > 0 ? max(0, x - p.q.window + 1) : 0; };
+  const int row_hi = hi_of(pos), row_lo = lo_of(pos);
+  const int all_hi = min(hi_of(s.len - s.n + r0 / p.group), to);
+  const int all_lo = lo_of(s.len - s.n + min(r0 + 31, rows - 1) / p.group);
+  const int P = p.c.page;
+  const int* const table = p.b.table + seq * p.b.table_ld;
+  const uint32_t page_bytes = (uint32_t)p.c.heads * P * D;     // < 2^32
+  const int8_t* const k_head = p.c.k + (int64_t)h * P * D + hi * (D / 2);
+  const int8_t* const v_head = p.c.v + (int64_t)h * P * D + c * P;
+  const int kpos = 16 * ((c >> 2) & 1) + 4 * (c >> 3) + (c & 3);   // the position of this lane's K row in a tile
+  int gk[2], gv[2];
+  auto load_pages = [&](int at) {
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, lm[w][rr]);
-    float L = 0.0f, o = 0.0f;
-#pragma unroll
-    for (int w = 0; w < NW; ++w) {
-      const float e = __builtin_amdgcn_exp2f(lm[w][rr] - M);
-      L += ll[w][rr] * e;
-      o += lo_[w][rr][d] * e;
+    for (int T = 0; T < 2; ++T) {
+      gk[T] = table[min(at + 32 * T + (kpos & 16), to - 1) >> p.c.log_page];
+      gv[T] = table[min(at + 32 * T + 16 * hi, to - 1) >> p.c.log_page];
     }
-    const int64_t t = s.t0 + (r0 + rr) / p.group;
-    const int head = h * p.group + (r0 + rr) % p.group;
-    if (nsplit == 1) {
-      store_as(p.q.y, p.q.ydtype, (t * p.q.heads + head) * D + d, L == 0.0f ? 0.0f : o / L);
-      if (p.q.lse && d == 0) p.q.lse[t * p.q.heads + head] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
-    } else {
-      const int64_t row = w.split * p.part_rows + t * p.q.heads + head;
-      p.part[row * D + d] = o;
-      if (d == 0) {
-        float* ml = p.part + (int64_t)p.splits * p.part_rows * D + 2 * row;
-        ml[0] = M;
-        ml[1] = L;
+  };
+  auto page_ok = [&](int id) { return (unsigned)id < (unsigned)p.c.num_pages; };
+  uint4 kr[2][KB], vr[2][DT];
+  float ks[2], vs[2], ks_next[2], vs_next[2];
+  bool ok[2], ok_next[2];
+  const int8_t* vp[2];
+  auto load_k = [&](int at) {
+#pragma unroll
+    for (int T = 0; T < 2; ++T) {
+      const int8_t* kp = k_head + (uint64_t)(uint32_t)(page_ok(gk[T]) ? gk[T] : 0) * page_bytes +
+                         ((at + 32 * T + kpos) & (P - 1)) * D;
+#pragma unroll
+      for (int b = 0; b < KB; ++b) kr[T][b] = *reinterpret_cast<const uint4*>(kp + 16 * b);
+      ok_next[T] = page_ok(gv[T]);
+      const uint32_t page = ok_next[T] ? gv[T] : 0;
+      ks_next[T] = p.c.ks[(int64_t)page * p.c.heads + h];
+      vs_next[T] = p.c.vs[(int64_t)page * p.c.heads + h];
+      vp[T] = v_head + (uint64_t)page * page_bytes + ((at + 32 * T + 16 * hi) & (P - 1));
+    }
+  };
+  auto load_v = [&]() {
+#pragma unroll
+    for (int T = 0; T < 2; ++T)
+#pragma unroll
+      for (int i = 0; i < DT; ++i) vr[T][i] = *reinterpret_cast<const uint4*>(vp[T] + 32 * i * P);
+  };
+
+  v16f acc[DT];
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int k = 0; k < 16; ++k) acc[i][k] = 0.0f;
+  float m = kNone, l = 0.0f, vref = kTinyScale;
+
+  uint4 raw[2 * KB];
+  const bool work = from + 64 * wave < to;
+  if (work) load_pages(from + 64 * wave);
+  load_query<2 * KB>(static_cast<const uint16_t*>(p.q.q) + (int64_t)(s.t0 + tok) * p.q.q_tok + hq * p.q.q_head,
+                     [&](int i) { return hi * (D / 2) + 8 * i; }, raw);
+  if (work) {
+    load_k(from + 64 * wave);
+    load_pages(from + 64 * (wave + NW));
+    load_v();
+  }
+  v8h qf[2 * KB];
+  const float qscale = fabsf(p.q.scale) * kLog2e * query_operands<2 * KB, 32>(raw, p.q.bf16, p.q.scale < 0.0f, qf);
+  // The operands stay in LDS, where the wave's result will lie: with them a lane
+  // would need more than its 256 registers.
+  v8h* const ql = reinterpret_cast<v8h*>(&lo_[wave][0][0]) + lane;
+#pragma unroll
+  for (int i = 0; i < 2 * KB; ++i) ql[64 * i] = qf[i];
+  for (int at = from + 64 * wave; at < to; at += 64 * NW) {
+    v16f sc[2];
+    int again = 0;
+    asm volatile("" : "+v"(again));                    // read them here, not before the loop
+    const v8h* const qs = ql + again;
+#pragma unroll
+    for (int T = 0; T < 2; ++T) {
+      ks[T] = ks_next[T];
+      vs[T] = vs_next[T];
+      ok[T] = ok_next[T];
+#pragma unroll
+      for (int i = 0; i < 16; ++i) sc[T][i] = 0.0f;
+#pragma unroll
+      for (int b = 0; b < KB; ++b) {
+        sc[T] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8(kr[T][b].x, kr[T][b].y), qs[128 * b], sc[T], 0, 0, 0);
+        sc[T] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8(kr[T][b].z, kr[T][b].w), qs[128 * b + 64], sc[T], 0, 0, 0);
       }
     }
+    const bool more = at + 64 * NW < to;
+    if (more) {
+      load_k(at + 64 * NW);
+      load_pages(at + 128 * NW);
+    }
+    float cm = kNone;
+    if (at >= all_lo && at + 64 <= all_hi && __all(ok[0] && ok[1])) {
+#pragma unroll
+      for (int T = 0; T < 2; ++T)
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          sc[T][i] *= ks[T] * qscale;
+          cm = fmaxf(cm, sc[T][i]);
+        }
+    } else {
+#pragma unroll
+      for (int T = 0; T < 2; ++T) {
+        const int first = at + 32 * T + 16 * hi, lim = ok[T] ? min(row_hi, to) : 0;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          sc[T][i] = first + i >= row_lo && first + i < lim ? sc[T][i] * (ks[T] * qscale) : -INFINITY;
+          cm = fmaxf(cm, sc[T][i]);
+        }
+      }
+    }
+    cm = max_halves(cm);
+    // a block past the last position or of no page: its scale must not count
+    const float vs0 = ok[0] && at + 16 * hi < to ? vs[0] : 0.0f, vs1 = ok[1] && at + 32 + 16 * hi < to ? vs[1] : 0.0f;
+    const float vm = max_halves(fmaxf(vs0, vs1));
+    const float m2 = fmaxf(m, cm), vref2 = fmaxf(vref, vm);
+    const float al = __builtin_amdgcn_exp2f(m - m2);
+    const float ao = al * (vref / vref2);
+    const float unit = 32768.0f / vref2;
+    l *= al;
+    v8h pf[2][2];
+#pragma unroll
+    for (int T = 0; T < 2; ++T) {
+      const float wt = (T ? vs1 : vs0) * unit;
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const float e = __builtin_amdgcn_exp2f(sc[T][i] - m2);
+        l += e;
+        pf[T][i >> 3][i & 7] = (_Float16)(e * wt);
+      }
+    }
+    if (__any(m2 != m) || vref2 != vref) {
+#pragma unroll
+      for (int i = 0; i < DT; ++i)
+#pragma unroll
+        for (int k = 0; k < 16; ++k) acc[i][k] *= ao;
+    }
+    m = m2;
+    vref = vref2;
+#pragma unroll
+    for (int T = 0; T < 2; ++T)
+#pragma unroll
+      for (int i = 0; i < DT; ++i) {
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8(vr[T][i].x, vr[T][i].y), pf[T][0], acc[i], 0, 0, 0);
+        acc[i] = __builtin_amdgcn_mfma_f32_32x32x16_f16(widen8(vr[T][i].z, vr[T][i].w), pf[T][1], acc[i], 0, 0, 0);
+      }
+    if (more) load_v();
   }
+  l += __shfl_xor(l, 32);
+  if (hi == 0) {
+    lm[wave][c] = m;
+    ll[wave][c] = l;
+  }
+  const float back = vref * 0x1p-15f;
+#pragma unroll
+  for (int i = 0; i < DT; ++i)
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      *reinterpret_cast<v4f*>(&lo_[wave][c][32 * i + 8 * k + 4 * hi]) =
+          v4f{acc[i][4 * k] * back, acc[i][4 * k + 1] * back, acc[i][4 * k + 2] * back, acc[i][4 * k + 3] * back};
+  join_waves<D, NW, 32>(p, s, w, r0, rows, nsplit, lo_, lm, ll);
 }
 
 // Many query rows per kv head: a workgroup of NW waves takes 32 NW / DS rows of
@@ -762,17 +967,23 @@ void k_kv8_prefill(AttnParams p) {
   }
 }
 
-// Joins the splits of a query row: a workgroup per row, 4 dimensions per thread,
-// the threads' groups taking the splits in turn and meeting in LDS.
-template <int D>
+// Joins the splits of the query rows, 4 dimensions per thread. FEW splits: D / 4
+// threads per row, which read its splits one after the other. Many: a workgroup
+// per row, its groups of D / 4 threads taking the splits in turn and meeting in
+// LDS. 8 sequences of 64 rows in 2 splits: the call takes 37 us with the first
+// form, 41 with the second.
+template <int D, bool FEW>
 __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p) {
-  constexpr int TPS = D / 4, G = 256 / TPS;            // threads per split, splits at a time
-  __shared__ float so[G][D];
+  constexpr int TPS = D / 4, G = 256 / TPS;            // threads per split, groups of them
+  constexpr int RPW = FEW ? G : 1, STEP = FEW ? 1 : G;  // rows a workgroup, splits at a time
+  __shared__ float so[FEW ? 1 : G][D];
   __shared__ float sm[G], sl[G];
   const int seq = blockIdx.y;
   const Seq s = sequence(p.b, seq);
-  const int h = blockIdx.x % p.c.heads, r = blockIdx.x / p.c.heads;
-  if (r >= s.n * p.group) return;
+  const int g = threadIdx.x / TPS, d = threadIdx.x % TPS * 4;
+  const int x = blockIdx.x * RPW + (FEW ? g : 0);
+  const int h = x % p.c.heads, r = x / p.c.heads;
+  if (r >= s.n * p.group || (FEW && g >= G)) return;
   const int r0 = r / p.tile_rows * p.tile_rows;
   const Range rg = tile_range(p, s, r0, min(r0 + p.tile_rows, s.n * p.group));
   const int nsplit = (rg.hi - rg.lo + p.split - 1) / p.split;
@@ -781,56 +992,76 @@ __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p) {
   const int head = h * p.group + r % p.group;
   const int64_t row = t * p.q.heads + head;
   const float* ml = p.part + (int64_t)p.splits * p.part_rows * D;
-  const int g = threadIdx.x / TPS, d = threadIdx.x % TPS * 4;
   float M = kNone, L = 0.0f;
   v4f o = {0, 0, 0, 0};
   if (g < G) {
 #pragma unroll 4
-    for (int i = g; i < nsplit; i += G) {
+    for (int i = FEW ? 0 : g; i < nsplit; i += STEP) {
       const int64_t at = i * p.part_rows + row;
       const float2 e = *reinterpret_cast<const float2*>(ml + 2 * at);
-      const v4f x = *reinterpret_cast<const v4f*>(p.part + at * D + d);
+      const v4f v = *reinterpret_cast<const v4f*>(p.part + at * D + d);
       const float M2 = fmaxf(M, e.x);
       const float a = __builtin_amdgcn_exp2f(M - M2), b = __builtin_amdgcn_exp2f(e.x - M2);
       L = L * a + e.y * b;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) o[k] = o[k] * a + x[k] * b;
+      for (int k = 0; k < 4; ++k) o[k] = o[k] * a + v[k] * b;
       M = M2;
     }
-    *reinterpret_cast<v4f*>(&so[g][d]) = o;
-    if (d == 0) {
-      sm[g] = M;
-      sl[g] = L;
+  }
+  if constexpr (FEW) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) store_as(p.q.y, p.q.ydtype, row * D + d + k, L == 0.0f ? 0.0f : o[k] / L);
+  } else {
+    if (g < G) {
+      *reinterpret_cast<v4f*>(&so[g][d]) = o;
+      if (d == 0) {
+        sm[g] = M;
+        sl[g] = L;
+      }
     }
-  }
-  __syncthreads();
-  if (threadIdx.x >= D) return;
-  const int x = threadIdx.x;
-  M = kNone;
+    __syncthreads();
+    if (threadIdx.x >= D) return;
+    M = kNone;
 #pragma unroll
-  for (int i = 0; i < G; ++i) M = fmaxf(M, sm[i]);
-  float out = 0.0f;
-  L = 0.0f;
+    for (int i = 0; i < G; ++i) M = fmaxf(M, sm[i]);
+    float out = 0.0f;
+    L = 0.0f;
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    const float e = __builtin_amdgcn_exp2f(sm[i] - M);
-    L += sl[i] * e;
-    out += so[i][x] * e;
+    for (int i = 0; i < G; ++i) {
+      const float e = __builtin_amdgcn_exp2f(sm[i] - M);
+      L += sl[i] * e;
+      out += so[i][threadIdx.x] * e;
+    }
+    store_as(p.q.y, p.q.ydtype, row * D + threadIdx.x, L == 0.0f ? 0.0f : out / L);
   }
-  store_as(p.q.y, p.q.ydtype, row * D + x, L == 0.0f ? 0.0f : out / L);
-  if (p.q.lse && x == 0) p.q.lse[row] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
+  if (p.q.lse && (FEW ? d : (int)threadIdx.x) == 0)
+    p.q.lse[row] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
 }
 
-constexpr int kWaves = 4;                  // of k_kv8_decode
+constexpr int kWaves = 4;                  // of k_kv8_decode and k_kv8_draft
+constexpr int kFewSplits = 8;              // that k_kv8_join reads one after the other
 
-// Which kernel, its query row tiles, and how the positions are split: into as
-// few splits as fill the chip, since each costs a start, an end and a share of
-// the joining launch. One row of 131072 positions, 8 kv heads, in 32 / 64 / 128 /
-// 256 / 512 splits (256 .. 4096 workgroups): 50, 54, 55, 65, 84 us; 64 ragged
+// Which kernel, its query row tiles, and how the positions are split.
+//
+// Up to 16 rows per kv head: k_kv8_decode. Up to 64, k_kv8_draft (8 sequences,
+// 64 rows, 4096 positions, 8 kv heads: 36 us, 44 in the decode kernel; 16 x 64
+// rows of 2048, 32 kv heads: 93 and 140). Up to 128 rows as well, where the
+// prefill kernel's tiles of 256 rows would leave half of the work empty (8 x 128
+// of 2048, 8 kv heads: 32 us, 38 in the prefill kernel; 32 kv heads: 87 and 106),
+// except where these tiles fill the chip and end after a few chunks (8 x 128 of
+// 512, 32 kv heads: 43 and 33). Above, k_kv8_prefill. Heads of more than 128
+// dimensions do not fit k_kv8_draft's registers.
+//
+// As few splits as fill the chip, since each costs a start, an end and a share
+// of the joining launch. One row of 131072 positions, 8 kv heads, in 32 / 64 /
+// 128 / 256 / 512 splits (256 .. 4096 workgroups): 50, 54, 55, 65, 84 us; 64 ragged
 // rows up to 4096 in 1 / 2 / 4: 59, 73, 82 us. Heads of 64 have half the bytes in
-// flight per wave and take twice the workgroups.
+// flight per wave and take twice the workgroups. k_kv8_draft is not split past
+// one workgroup a CU: 192 workgroups of 1088 positions take 24 us, 384 of half
+// as many 31.
+enum Kernel { DECODE, DRAFT, PREFILL };
 struct Plan {
-  bool prefill;
+  Kernel kernel;
   int tile_rows, tiles, split, splits;
   int64_t blocks;
 };
@@ -838,8 +1069,10 @@ Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
   Plan pl;
   const int group = q.heads / c.heads;
   const int64_t rows = (int64_t)b.max_new * group;
-  pl.prefill = rows > 64;
-  pl.tile_rows = pl.prefill ? (c.dim <= 128 ? 256 : 128) : 16;
+  const bool full = (int64_t)c.heads * b.B >= 256 && b.max_len <= 512;
+  if (c.dim > 128) pl.kernel = rows > 64 ? PREFILL : DECODE;
+  else pl.kernel = rows > (full ? 64 : 128) ? PREFILL : rows > 16 ? DRAFT : DECODE;
+  pl.tile_rows = pl.kernel == DECODE ? 16 : pl.kernel == DRAFT ? 32 : c.dim <= 128 ? 256 : 128;
   pl.tiles = (int)((rows + pl.tile_rows - 1) / pl.tile_rows);
   int64_t span = b.max_len;
   if (q.window > 0) {
@@ -847,9 +1080,9 @@ Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
     span = std::min<int64_t>(span, (int64_t)q.window + toks + 64);
   }
   const int64_t work = (int64_t)pl.tiles * c.heads * b.B;
-  const int64_t unit = pl.prefill ? 512 : 64 * kWaves;
-  const int64_t fill = c.dim <= 64 || pl.prefill ? 512 : 256;
-  const int64_t want = (fill + work - 1) / work;
+  const int64_t unit = pl.kernel == PREFILL ? 512 : 64 * kWaves;
+  const int64_t fill = pl.kernel == PREFILL || (pl.kernel == DECODE && c.dim <= 64) ? 512 : 256;
+  const int64_t want = pl.kernel == DRAFT ? std::max<int64_t>(1, fill / work) : (fill + work - 1) / work;
   const int64_t units = (span + unit - 1) / unit;
   // a second launch costs more than two chunks per wave
   const int64_t per = std::max<int64_t>(span <= 512 ? 2 : 1, (units + want - 1) / want);
@@ -862,16 +1095,20 @@ Plan plan(const KvPool& c, const KvBatch& b, const KvQuery& q) {
 template <int D>
 void launch_for(AttnParams p, const Plan& pl, hipStream_t stream) {
   const dim3 grid((unsigned)pl.blocks);
-  if (pl.prefill) {
+  if (pl.kernel == PREFILL) {
     constexpr int DS = D > 128 ? 2 : 1;
     if (p.c.page >= 64) hipLaunchKernelGGL((k_kv8_prefill<D, 8, DS, true>), grid, dim3(512), 0, stream, p);
     else hipLaunchKernelGGL((k_kv8_prefill<D, 8, DS, false>), grid, dim3(512), 0, stream, p);
-  } else {
+  } else if (pl.kernel == DECODE) {
     hipLaunchKernelGGL((k_kv8_decode<D, kWaves>), grid, dim3(64 * kWaves), 0, stream, p);
+  } else if constexpr (D <= 128) {
+    hipLaunchKernelGGL((k_kv8_draft<D, kWaves>), grid, dim3(64 * kWaves), 0, stream, p);
   }
   if (pl.splits > 1) {
-    hipLaunchKernelGGL((k_kv8_join<D>), dim3((unsigned)((int64_t)p.b.max_new * p.q.heads), (unsigned)p.b.B), dim3(256), 0,
-                       stream, p);
+    const int64_t rows = (int64_t)p.b.max_new * p.q.heads, per = pl.splits <= kFewSplits ? 256 / (D / 4) : 1;
+    const dim3 jgrid((unsigned)((rows + per - 1) / per), (unsigned)p.b.B);
+    if (per > 1) hipLaunchKernelGGL((k_kv8_join<D, true>), jgrid, dim3(256), 0, stream, p);
+    else hipLaunchKernelGGL((k_kv8_join<D, false>), jgrid, dim3(256), 0, stream, p);
   }
 }
 
