@@ -200,6 +200,11 @@ __device__ __forceinline__ void join_waves(const AttnParams& p, const Seq& s, co
 // Few query rows per kv head: a workgroup of NW waves takes 16 rows (token,
 // query head of the group) of one kv head and a split of the positions; its
 // waves take chunks of 64 positions in turn, with no sharing until the end.
+// Bound by HBM: 64 ragged rows up to 4096, 8 query heads per kv head, 55 us, 5.0
+// TB/s of codes; 131072 positions 43 us. Short contexts by the chain of loads
+// (lengths, table, codes) and the launch: 257 positions 8.4 us. Two chunks in
+// flight per wave instead of one were slower (67 and 57 us: a wave's registers
+// are full), and so were three waves per SIMD in place of two (75 and 68).
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW)
 __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv8_decode(AttnParams p) {
@@ -384,6 +389,12 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
 // ends up with the scores of 16 consecutive positions per tile, the k indices
 // that the second product wants in it. The dimensions are summed in the order of
 // the codes in memory: lane half hi takes dimensions hi D / 2 and up.
+//
+// Bound by vector work and latency: a wave's chunk is about 650 vector
+// instructions (320 of them widen codes) and 32 matrix ones, and a CU holds one
+// wave per SIMD of them. 35 rows in a window of 1024, 24 sequences of 4 kv heads:
+// 22.4 us; 64 rows of 4096, 8 sequences of 8 kv heads: 36 us in two splits, 49 in
+// one.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_kv8_draft(AttnParams p) {
   constexpr int KB = D / 32, DT = D / 32;              // 16-byte pieces of a half row of K, 32-dimension tiles of O
@@ -591,6 +602,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 //
 // ONE: a page holds whole tiles, so a tile has one page and one pair of scales,
 // fetched through the scalar cache.
+//
+// Bound by the matrix cores and the vector work beside them (softmax, widening)
+// at the clock that the power limit leaves: four chunks of up to 4096 tokens on
+// as much context, 64 heads over 8 kv heads (1214 GFLOP), 1300 to 1500 us with the
+// machine's clock, 810 to 930 TFLOP/s; a large fp16 matrix product reaches 1170.
 template <typename T>
 __device__ __forceinline__ T scalar_load(const T* p) {
   return *(const __attribute__((address_space(4))) T*)p;

@@ -14,7 +14,10 @@
 // reads or writes it. The new rows are read once, 16 values per piece, and stay
 // in registers between the maximum and the codes; V's codes go through LDS in
 // position order and leave transposed, 16 positions of a dimension per store.
-// Both directions are bound by HBM: 3 bytes per value stored, 3 read back.
+// Both directions are bound by HBM, 3 bytes per value stored, 3 read back: 24
+// ragged prompts of up to 1500 tokens, 8 heads of 128 (91 MB each way) take 24.8
+// and 19.9 us, 3.7 and 4.6 TB/s. A decode step's few tokens are bound by the
+// chain of loads (lengths, table, scale, codes): 64 tokens 9 and 8 us.
 #include <algorithm>
 
 #include "kv8_common.h"

@@ -25,7 +25,9 @@ constexpr int kCUs = 256;      // of an MI355X: launch shapes are planned for it
 
 // One row per WPR waves (256 / (64 WPR) rows a workgroup); NC > 0: the row's
 // 16-element chunks stay in registers (NC per lane), so X is read once. NC = 0:
-// rows of any length, read twice (the second time from cache).
+// rows of any length, read twice (the second time from cache). Bound by HBM, 3
+// bytes per element: 4096 x 8192 17.8 us, 5.7 TB/s; 777 x 18944 11 us; one row of
+// 4096 2.1 us, a launch.
 template <bool BF, int WPR, int NC>
 __global__ __launch_bounds__(kThreads) void k_w8a8_quant(const uint16_t* __restrict__ x, int64_t ldx, int64_t M, int K,
                                                          int8_t* __restrict__ q, float* __restrict__ s) {
@@ -281,7 +283,11 @@ enum { OUT_F32 = 0, OUT_16 = 1, OUT_RAW = 2 };
 //
 // Each workgroup takes logical tiles b, b + G, b + 2 G, ... (G workgroups). The
 // next tile's first S stages are issued before a tile's outputs are stored, so
-// the stores drain under the next tile's matrix work. WIDE: rows of y take
+// the stores drain under the next tile's matrix work.
+//
+// Bound by the matrix cores at the clock that the power limit leaves them: 4096
+// x 28672 x 8192 764 us, 2.5 POP/s; smaller products by what their last round of
+// tiles leaves idle (777 x 3584 x 18944, 196 tiles: 67 us, 1.6 POP/s). WIDE: rows of y take
 // 16-byte stores (N, ldy and y aligned); else element stores, one tile per
 // workgroup.
 template <int BM, int BN, int WM, int WN, int S, int OUT, bool WIDE>
@@ -575,7 +581,8 @@ void k_w8a8_gemm_tiles(W8Params p) {
 #undef OUT_OF
 }
 
-// Adds the K splits' int32 sums and scales them.
+// Adds the K splits' int32 sums and scales them. They come from the caches: 16 x
+// 8192 outputs in four ranges 4.4 us.
 __global__ __launch_bounds__(kThreads) void k_w8a8_join(W8Params p, int splits) {
   const int64_t total = (int64_t)p.M * p.N;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
@@ -627,15 +634,18 @@ void launch_tiles(W8Params p, int splits, hipStream_t stream) {
 // 64 MiB 128-channel tiles take over, which read them 8 times less often (16 x
 // 28672 x 8192: 53.5 us, 60 in the small kernel; 16 x 8192 x 28672: 47 and 54;
 // 16 x 18944 x 3584: 19.5 and 22.4; below, 16 x 8192 x 8192: 21.8 and 20.1; all
-// with W from HBM). Above 16 tokens, the tile
-// whose estimated time is least: rounds of tiles over the CUs times (stages x the
-// tile's time per 128-k stage + its start and output). The times (us) are
-// measured ones: 256 x 256 tiles 1.15 a stage with every CU busy (4096 x 4096
-// x 8192 119 us), 256 x 128 0.8 (2048 x 4096 x 11008: 88 us; 256 x 256 tiles
-// 114, 128 x 128 105), 128 x 128 0.5 (512 x 8192 x 8192: 39 us; 45 and 74 with
-// the larger ones). 128 x 128 tiles may also split K, which costs a launch and
-// 8 bytes per output and range through the caches (64 x 8192 x 8192: 28.6 us
-// whole, 19.6 in four ranges; 256 x 8192 x 8192: 31.0 whole, 32.4 in two).
+// with W from HBM).
+//
+// Above 16 tokens, the tile whose estimated time is least: rounds of tiles over
+// the CUs times (stages x the tile's time per 128-k stage + its start and
+// output). The times (us: 256 x 256 tiles 1.15 a stage, 256 x 128 0.8, 128 x 128
+// 0.5) are fitted so that the choice is within 3 % of the fastest over 20 shapes
+// from 32 x 4096 x 4096 to 4096 x 8192 x 28672, tokens x channels x K; us of the
+// three in turn: 4096 x 4096 x 4096 62.6, 70.7, 80.9; 1024 x 8192 x 28672 229, 224,
+// 290; 512 x 8192 x 8192 74, 55.2, 43.4. 128 x 128 tiles may also split K, which
+// costs a launch and 8 bytes per output and range through the caches (64 x 8192
+// x 8192: 35.6 us whole, 25.5 in two ranges, 21.2 in four; 512 x 4096 x 11008:
+// 53.8, 41.7, 50.1; 256 x 11008 x 4096: 24.1, 41.5, 44.7).
 enum { TILE_SMALL = 0, TILE_256 = 1, TILE_256_128 = 2, TILE_128 = 3 };
 struct W8Plan {
   int tile, splits;
