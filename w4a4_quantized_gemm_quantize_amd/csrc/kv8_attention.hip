@@ -203,8 +203,9 @@ __device__ __forceinline__ void join_waves(const AttnParams& p, const Seq& s, co
 // Bound by HBM: 64 ragged rows up to 4096, 8 query heads per kv head, 55 us, 5.0
 // TB/s of codes; 131072 positions 43 us. Short contexts by the chain of loads
 // (lengths, table, codes) and the launch: 257 positions 8.4 us. Two chunks in
-// flight per wave instead of one were slower (67 and 57 us: a wave's registers
-// are full), and so were three waves per SIMD in place of two (75 and 68).
+// flight per wave instead of one measured the same (61.2 and 62.6 us for the 64
+// rows, 43.5 and 40.0 for 20 of 4096), three waves per SIMD in place of two were
+// slower (75).
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW)
 __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv8_decode(AttnParams p) {
