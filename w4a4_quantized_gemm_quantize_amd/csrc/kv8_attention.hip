@@ -605,9 +605,11 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
 // fetched through the scalar cache.
 //
 // Bound by the matrix cores and the vector work beside them (softmax, widening)
-// at the clock that the power limit leaves: four chunks of up to 4096 tokens on
-// as much context, 64 heads over 8 kv heads (1214 GFLOP), 1300 to 1500 us with the
-// machine's clock, 810 to 930 TFLOP/s; a large fp16 matrix product reaches 1170.
+// at the clock that the power limit leaves: a step's matrix phase takes 1700 to
+// 1950 cycles (1024 of matrix instructions), its vector phase as many, so a tile
+// 4200. Four chunks of up to 4096 tokens on as much context, 64 heads over 8 kv
+// heads (1214 GFLOP): 1260 us from a cool machine (965 TFLOP/s), 1450 in a row; a
+// large fp16 matrix product reaches 1170.
 template <typename T>
 __device__ __forceinline__ T scalar_load(const T* p) {
   return *(const __attribute__((address_space(4))) T*)p;
@@ -695,7 +697,7 @@ void k_kv8_prefill(AttnParams p) {
   auto load_codes = [&](int kt) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
-      const int id = pg[ONE ? (is_k(i) ? 0 : 1) : i], x = x_of(i);
+      const int x = x_of(i), id = ONE ? __builtin_amdgcn_readfirstlane(pg[is_k(i) ? 0 : 1]) : pg[i];
       const uint32_t page = (unsigned)id < (unsigned)p.c.num_pages ? id : 0;
       const int8_t* src = (is_k(i) ? k_head : v_head) + (uint64_t)page * page_bytes;
       if constexpr (ONE) {
@@ -714,8 +716,9 @@ void k_kv8_prefill(AttnParams p) {
   int pgs, gone, gone_next;
   float ksv, vsv, ks_next, vs_next;
   auto load_scales = [&]() {
-    gone_next = (unsigned)pgs >= (unsigned)p.c.num_pages;   // no page of the pool
-    const int64_t e = (int64_t)(gone_next ? 0 : pgs) * p.c.heads + h;
+    const int id = ONE ? __builtin_amdgcn_readfirstlane(pgs) : pgs;
+    gone_next = (unsigned)id >= (unsigned)p.c.num_pages;    // no page of the pool
+    const int64_t e = (int64_t)(gone_next ? 0 : id) * p.c.heads + h;
     ks_next = ONE ? scalar_load(p.c.ks + e) : p.c.ks[e];
     vs_next = ONE ? scalar_load(p.c.vs + e) : p.c.vs[e];
   };
@@ -726,21 +729,12 @@ void k_kv8_prefill(AttnParams p) {
   auto v_slot = [&](int row, int slot) {               // in a V buffer
     return row * 2 * TW + 16 * (slot ^ (TW == 64 ? (row >> 1) & 7 : (row >> 2) & 3));
   };
-  auto write_codes = [&](int kt) {
-#pragma unroll
-    for (int i = 0; i < NP; ++i) {
-      const v8h a = widen8(code[i].x, code[i].y), b = widen8(code[i].z, code[i].w);
-      const int x = x_of(i), buf = (tile_of(i, kt) - from) / TW & 1;
-      if (is_k(i)) {
-        const int row = x / (D / 16), c = 2 * (x % (D / 16));
-        *reinterpret_cast<v8h*>(lk[buf] + k_slot(row, c)) = a;
-        *reinterpret_cast<v8h*>(lk[buf] + k_slot(row, c + 1)) = b;
-      } else {
-        const int row = x / NB, c = 2 * (x % NB);
-        *reinterpret_cast<v8h*>(lv[buf] + v_slot(row, c)) = a;
-        *reinterpret_cast<v8h*>(lv[buf] + v_slot(row, c + 1)) = b;
-      }
-    }
+  // half j % 2 of piece j / 2 into LDS
+  auto write_half = [&](int kt, int j) {
+    const int i = j >> 1, x = x_of(i), buf = (tile_of(i, kt) - from) / TW & 1;
+    const v8h a = j & 1 ? widen8(code[i].z, code[i].w) : widen8(code[i].x, code[i].y);
+    if (is_k(i)) *reinterpret_cast<v8h*>(lk[buf] + k_slot(x / (D / 16), 2 * (x % (D / 16)) + (j & 1))) = a;
+    else *reinterpret_cast<v8h*>(lv[buf] + v_slot(x / NB, 2 * (x % NB) + (j & 1))) = a;
   };
 
   v16f acc[DT];
@@ -756,12 +750,13 @@ void k_kv8_prefill(AttnParams p) {
   auto sees = [&](int at) { return at < to && at < hi_max && at + TW > lo_min; };
 
   // The matrix work of a step: values of the last tile (VALUES), scores of this
-  // one (SCORES). Operand reads run RING ahead of the instructions that use
+  // one (SCORES), and between its later instructions the staging of the next
+  // step's codes. Operand reads run RING ahead of the instructions that use
   // them, in this order; one wave per SIMD does this at a time, so nothing else
   // hides their latency.
   auto matrix_step = [&](int at, auto values_c, auto scores_c) {
     constexpr int NV = decltype(values_c)::value ? DT * NB : 0, NS = decltype(scores_c)::value ? ST * TW / 32 : 0;
-    constexpr int RING = 6;
+    constexpr int RING = D > 128 ? 4 : 6;              // (the wide heads' registers are full)
     const uint8_t* bk = lk[(at - from) / TW & 1];
     const uint8_t* bv = lv[(at - TW - from) / TW & 1];
     auto read = [&](int x) {
@@ -769,6 +764,10 @@ void k_kv8_prefill(AttnParams p) {
       x -= NV;
       return *reinterpret_cast<const v8h*>(bk + k_slot(32 * (x % (TW / 32)) + krow, 2 * (x / (TW / 32)) + hi));
     };
+    // The matrix instructions of the late group, whose waves are the younger
+    // ones, would otherwise wait for the early group's vector instructions
+    // (2260 cycles a step in place of 1960).
+    __builtin_amdgcn_s_setprio(3);
     v8h ring[RING];
 #pragma unroll
     for (int x = 0; x < RING; ++x) ring[x] = read(x);
@@ -789,8 +788,12 @@ void k_kv8_prefill(AttnParams p) {
         sc[t] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ring[x % RING], qf[u], sc[t], 0, 0, 0);
       }
       if (x + RING < NV + NS) ring[x % RING] = read(x + RING);
+      constexpr int FIRST = NV + NS - 8 * NP;
+      static_assert(NS == 0 || FIRST >= 0, "four instructions per half piece");
+      if (NS > 0 && x >= FIRST && (x - FIRST) % 4 == 0) write_half(at + TW, (x - FIRST) / 4);
       __builtin_amdgcn_sched_barrier(0);
     }
+    __builtin_amdgcn_s_setprio(0);
   };
   // scores -> weights of the tile at `at`, whose scales this wave holds
   auto weights = [&](int at) {
@@ -888,10 +891,11 @@ void k_kv8_prefill(AttnParams p) {
 
   // Two groups of waves, one wave of each per SIMD, run the same steps half a
   // tile apart: while one group's waves do their matrix work (values of the
-  // last tile, scores of this one) the other's turn scores into weights, so the
-  // matrix cores and the vector units work at the same time. K is staged a tile
-  // ahead of V; the late group stages its pieces one tile further ahead, so that
-  // both groups' pieces of a tile are in LDS before the early group reads it.
+  // last tile, scores of this one, staging of the next) the other's turn scores
+  // into weights, so the matrix cores and the vector units work at the same
+  // time. K is staged a tile ahead of V. A step of the early group reads what both
+  // groups staged in the step before; the buffer that is staged into was last
+  // read by the late group's step before.
 #define PHASE_END()                                                                   \
   {                                                                                   \
     __builtin_amdgcn_s_waitcnt(0xC07F); /* lgkmcnt(0): own LDS accesses are done */   \
@@ -902,17 +906,14 @@ void k_kv8_prefill(AttnParams p) {
     asm volatile("" ::: "memory");                                                    \
   }
   const bool late = wave >= NW / 2;
-  const int ahead = late ? 2 * TW : TW;                // K tiles that a wave's weights step stages ahead
   if (from < to) {
     load_pages(from);
     load_codes(from);
-    write_codes(from);
-    if (late) {
-      load_pages(from + TW);
-      load_codes(from + TW);
-      write_codes(from + TW);
-    }
-    load_pages(from + ahead);
+#pragma unroll
+    for (int j = 0; j < 2 * NP; ++j) write_half(from, j);
+    load_pages(from + TW);
+    load_codes(from + TW);
+    load_pages(from + 2 * TW);
     scale_pages(from);
     load_scales();
     scale_pages(from + TW);
@@ -920,24 +921,28 @@ void k_kv8_prefill(AttnParams p) {
   PHASE_END()
   if (late) PHASE_END()
   for (int at = from; at < to; at += TW) {
-    load_codes(at + ahead);
     // (a tile that the wave's rows do not see has weights of zero)
     if (at > from) matrix_step(at, std::true_type{}, std::true_type{});
     else matrix_step(at, std::false_type{}, std::true_type{});
     PHASE_END()
+    load_codes(at + 2 * TW);
     ksv = ks_next;
     vsv = vs_next;
     gone = gone_next;
     load_scales();
-    scale_pages(at + 2 * TW);
-    load_pages(at + TW + ahead);
+    if constexpr (ONE) {                               // K's page is that of V and of the scales one tile later
+      pg[1] = pgs = pg[0];
+      pg[0] = page_one(at + 3 * TW);
+    } else {
+      scale_pages(at + 2 * TW);
+      load_pages(at + 3 * TW);
+    }
     if (sees(at)) {
       weights(at);
     } else {
 #pragma unroll
       for (int b = 0; b < NB; ++b) pf[b >> 1][b & 1] = v8h{};
     }
-    write_codes(at + ahead);
     PHASE_END()
   }
   if (from < to) matrix_step(from + (to - from + TW - 1) / TW * TW, std::true_type{}, std::false_type{});
