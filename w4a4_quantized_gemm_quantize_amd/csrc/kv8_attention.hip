@@ -126,6 +126,17 @@ __device__ __forceinline__ float lane_value(float x, int lane) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
 }
 
+// Four outputs at a multiple of 4 elements of the 16-byte aligned y.
+__device__ __forceinline__ void store4_as(void* y, int ydt, int64_t i, v4f v) {
+  if (ydt == 0) {
+    *reinterpret_cast<v4f*>(static_cast<float*>(y) + i) = v;
+  } else {
+    const bool bf = ydt == 2;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(y) + i) =
+        uint2{u16_of(v[0], bf) | (uint32_t)u16_of(v[1], bf) << 16, u16_of(v[2], bf) | (uint32_t)u16_of(v[3], bf) << 16};
+  }
+}
+
 // Positions a tile of query rows [r0, r1) of a sequence can see: [lo, hi), lo a
 // multiple of 64.
 struct Range {
@@ -165,34 +176,30 @@ template <int D, int NW, int R>
 __device__ __forceinline__ void join_waves(const AttnParams& p, const Seq& s, const Work& wk, int r0, int rows, int nsplit,
                                            const float (&lo_)[NW][R][D + 4], const float (&lm)[NW][R],
                                            const float (&ll)[NW][R]) {
-  const int h = wk.h;
   __syncthreads();
-  for (int i = threadIdx.x; i < R * D; i += 64 * NW) {
-    const int rr = i / D, d = i % D;
-    if (r0 + rr >= rows) continue;
+  for (int i = threadIdx.x; i < R * D / 4; i += 64 * NW) {
+    const int r = r0 + i / (D / 4), d = i % (D / 4) * 4;
+    if (r >= rows) break;
     float M = kNone;
 #pragma unroll
-    for (int w = 0; w < NW; ++w) M = fmaxf(M, lm[w][rr]);
-    float L = 0.0f, o = 0.0f;
+    for (int w = 0; w < NW; ++w) M = fmaxf(M, lm[w][r - r0]);
+    float L = 0.0f;
+    v4f o = {0, 0, 0, 0};
 #pragma unroll
     for (int w = 0; w < NW; ++w) {
-      const float e = __builtin_amdgcn_exp2f(lm[w][rr] - M);
-      L += ll[w][rr] * e;
-      o += lo_[w][rr][d] * e;
+      const float e = __builtin_amdgcn_exp2f(lm[w][r - r0] - M);
+      L += ll[w][r - r0] * e;
+      o += *reinterpret_cast<const v4f*>(&lo_[w][r - r0][d]) * e;
     }
-    const int64_t t = s.t0 + (r0 + rr) / p.group;
-    const int head = h * p.group + (r0 + rr) % p.group;
+    const int tok = r / p.group;
+    const int64_t row = (int64_t)(s.t0 + tok) * p.q.heads + wk.h * p.group + r - tok * p.group;
     if (nsplit == 1) {
-      store_as(p.q.y, p.q.ydtype, (t * p.q.heads + head) * D + d, L == 0.0f ? 0.0f : o / L);
-      if (p.q.lse && d == 0) p.q.lse[t * p.q.heads + head] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
+      store4_as(p.q.y, p.q.ydtype, row * D + d, L == 0.0f ? v4f{0, 0, 0, 0} : o * (1.0f / L));
+      if (p.q.lse && d == 0) p.q.lse[row] = L == 0.0f ? -INFINITY : (M + __builtin_amdgcn_logf(L)) / kLog2e;
     } else {
-      const int64_t row = wk.split * p.part_rows + t * p.q.heads + head;
-      p.part[row * D + d] = o;
-      if (d == 0) {
-        float* ml = p.part + (int64_t)p.splits * p.part_rows * D + 2 * row;
-        ml[0] = M;
-        ml[1] = L;
-      }
+      const int64_t at = wk.split * p.part_rows + row;
+      *reinterpret_cast<v4f*>(p.part + at * D + d) = o;
+      if (d == 0) *reinterpret_cast<float2*>(p.part + (int64_t)p.splits * p.part_rows * D + 2 * at) = float2{M, L};
     }
   }
 }
@@ -210,7 +217,7 @@ template <int D, int NW>
 __global__ __launch_bounds__(64 * NW)
 __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv8_decode(AttnParams p) {
   constexpr int DB = D / 64, DT = D / 16;
-  __shared__ float lo_[NW][16][D + 4];
+  __shared__ __align__(16) float lo_[NW][16][D + 4];
   __shared__ float lm[NW][16], ll[NW][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -961,16 +968,10 @@ void k_kv8_prefill(AttnParams p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k) {
         const int64_t o = row * D + d0 + 32 * i + 8 * k + 4 * hi;
-        float f[4];
+        v4f f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) f[e] = l == 0.0f ? 0.0f : acc[i][4 * k + e] * out;
-        if (p.q.ydtype == 0) {
-          *reinterpret_cast<float4*>(static_cast<float*>(p.q.y) + o) = float4{f[0], f[1], f[2], f[3]};
-        } else {
-          const bool bf = p.q.ydtype == 2;
-          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.q.y) + o) =
-              uint2{u16_of(f[0], bf) | (uint32_t)u16_of(f[1], bf) << 16, u16_of(f[2], bf) | (uint32_t)u16_of(f[3], bf) << 16};
-        }
+        store4_as(p.q.y, p.q.ydtype, o, f);
       }
     if (p.q.lse && hi == 0 && d0 == 0) p.q.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) / kLog2e;
   } else {
@@ -1031,8 +1032,7 @@ __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p) {
     }
   }
   if constexpr (FEW) {
-#pragma unroll
-    for (int k = 0; k < 4; ++k) store_as(p.q.y, p.q.ydtype, row * D + d + k, L == 0.0f ? 0.0f : o[k] / L);
+    store4_as(p.q.y, p.q.ydtype, row * D + d, L == 0.0f ? v4f{0, 0, 0, 0} : o * (1.0f / L));
   } else {
     if (g < G) {
       *reinterpret_cast<v4f*>(&so[g][d]) = o;
