@@ -85,8 +85,7 @@ __global__ __launch_bounds__(kThreads) void k_kv8_append(KvPool c, KvBatch b, Kv
   const Slots w = slots_of(c, b, s, blockIdx.x, j);
   if (!w.any) return;
   const int P = c.page;
-  const int pg = page_of(b, c, seq, j * P);
-  if (pg < 0) return;
+  const int pg = page_of(b, c, seq, j * P);             // on its way while the tokens are loaded
   const int tid = threadIdx.x;
   const uint16_t* src = is_v ? static_cast<const uint16_t*>(x.v) + h * x.v_head : static_cast<const uint16_t*>(x.k) + h * x.k_head;
   const int64_t tok = is_v ? x.v_tok : x.k_tok;
@@ -103,6 +102,7 @@ __global__ __launch_bounds__(kThreads) void k_kv8_append(KvPool c, KvBatch b, Kv
       raw[n][1] = p[1];
     }
   }
+  if (pg < 0) return;
 #pragma unroll
   for (int n = 0; n < NPT; ++n) m = absmax16(raw[n], m);
   float* sp = (is_v ? c.vs : c.ks) + (int64_t)pg * c.heads + h;
