@@ -207,8 +207,8 @@ __device__ __forceinline__ void join_waves(const AttnParams& p, const Seq& s, co
 // Few query rows per kv head: a workgroup of NW waves takes 16 rows (token,
 // query head of the group) of one kv head and a split of the positions; its
 // waves take chunks of 64 positions in turn, with no sharing until the end.
-// Bound by HBM: 64 ragged rows up to 4096, 8 query heads per kv head, 55 us, 5.0
-// TB/s of codes; 131072 positions 43 us. Short contexts by the chain of loads
+// Bound by HBM: 64 ragged rows up to 4096, 8 query heads per kv head, 57 us, 4.8
+// TB/s of codes; 131072 positions 43 us and a joining launch. Short contexts by the chain of loads
 // (lengths, table, codes) and the launch: 257 positions 8.4 us. Two chunks in
 // flight per wave instead of one measured the same (61.2 and 62.6 us for the 64
 // rows, 43.5 and 40.0 for 20 of 4096), three waves per SIMD in place of two were
@@ -398,11 +398,12 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
 // that the second product wants in it. The dimensions are summed in the order of
 // the codes in memory: lane half hi takes dimensions hi D / 2 and up.
 //
-// Bound by vector work and latency: a wave's chunk is about 650 vector
-// instructions (320 of them widen codes) and 32 matrix ones, and a CU holds one
-// wave per SIMD of them. 35 rows in a window of 1024, 24 sequences of 4 kv heads:
-// 22.4 us; 64 rows of 4096, 8 sequences of 8 kv heads: 36 us in two splits, 49 in
-// one.
+// Bound by the chain of loads at the start (lengths, table, codes: 4 us of it),
+// then by about 5000 cycles a chunk of a wave: its codes' way from memory beside
+// 650 vector instructions (320 of them widen codes) and 32 matrix ones. 35 rows
+// in a window of 1024, 24 sequences of 4 kv heads: 19 us; 64 rows of 4096, 8
+// sequences of 8 kv heads: 34 us in two splits, 47 in one. Neither fewer vector
+// instructions per score nor eight waves a workgroup made it faster.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_kv8_draft(AttnParams p) {
   constexpr int KB = D / 32, DT = D / 32;              // 16-byte pieces of a half row of K, 32-dimension tiles of O
@@ -993,8 +994,8 @@ void k_kv8_prefill(AttnParams p) {
 // Joins the splits of the query rows, 4 dimensions per thread. FEW splits: D / 4
 // threads per row, which read its splits one after the other. Many: a workgroup
 // per row, its groups of D / 4 threads taking the splits in turn and meeting in
-// LDS. 8 sequences of 64 rows in 2 splits: the call takes 37 us with the first
-// form, 41 with the second.
+// LDS. 8 sequences of 64 rows in 2 splits: the call takes 34 us with the first
+// form, 38 with the second.
 template <int D, bool FEW>
 __global__ __launch_bounds__(256) void k_kv8_join(AttnParams p) {
   constexpr int TPS = D / 4, G = 256 / TPS;            // threads per split, groups of them
@@ -1066,21 +1067,21 @@ constexpr int kFewSplits = 8;              // that k_kv8_join reads one after th
 // Which kernel, its query row tiles, and how the positions are split.
 //
 // Up to 16 rows per kv head: k_kv8_decode. Up to 64, k_kv8_draft (8 sequences,
-// 64 rows, 4096 positions, 8 kv heads: 36 us, 44 in the decode kernel; 16 x 64
-// rows of 2048, 32 kv heads: 93 and 140). Up to 128 rows as well, where the
+// 64 rows, 4096 positions, 8 kv heads: 34 us, 42 in the decode kernel; 16 x 64
+// rows of 2048, 32 kv heads: 88 and 134). Up to 128 rows as well, where the
 // prefill kernel's tiles of 256 rows would leave half of the work empty (8 x 128
-// of 2048, 8 kv heads: 32 us, 38 in the prefill kernel; 32 kv heads: 87 and 106),
+// of 2048, 8 kv heads: 28 us, 36 in the prefill kernel; 32 kv heads: 78 and 97),
 // except where these tiles fill the chip and end after a few chunks (8 x 128 of
-// 512, 32 kv heads: 43 and 33). Above, k_kv8_prefill. Heads of more than 128
+// 512, 32 kv heads: 33 and 30). Above, k_kv8_prefill. Heads of more than 128
 // dimensions do not fit k_kv8_draft's registers.
 //
 // As few splits as fill the chip, since each costs a start, an end and a share
 // of the joining launch. One row of 131072 positions, 8 kv heads, in 32 / 64 /
-// 128 / 256 / 512 splits (256 .. 4096 workgroups): 50, 54, 55, 65, 84 us; 64 ragged
-// rows up to 4096 in 1 / 2 / 4: 59, 73, 82 us. Heads of 64 have half the bytes in
+// 128 / 256 / 512 splits (256 .. 4096 workgroups): 50, 51, 55, 63, 82 us; 64 ragged
+// rows up to 4096 in 1 / 2 / 4: 58, 69, 79 us. Heads of 64 have half the bytes in
 // flight per wave and take twice the workgroups. k_kv8_draft is not split past
-// one workgroup a CU: 192 workgroups of 1088 positions take 24 us, 384 of half
-// as many 31.
+// one workgroup a CU: 192 workgroups of 1088 positions take 21 us, 384 of half
+// as many 27.
 enum Kernel { DECODE, DRAFT, PREFILL };
 struct Plan {
   Kernel kernel;
