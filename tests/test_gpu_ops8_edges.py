@@ -165,7 +165,7 @@ def test_bad_pages_and_nan_rows_of_drafts():
     assert bool(torch.isnan(z[3, 5]).all()) and torch.equal(z[keep.cuda()], y[keep.cuda()])
 
 
-@pytest.mark.parametrize("new", [1, 5, 90])
+@pytest.mark.parametrize("new", [1, 5, 20, 90])
 def test_pool_without_pages_and_sequences_without_positions(new):
     """No page in the pool, or no column in the table: every query sees nothing,
     tokens read back as zeros, nothing is stored."""
