@@ -692,19 +692,18 @@ def _kv_pool(*tensors):
         _kv_refuse(tensors)
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [num_pages, heads, page, dim]")
-    pages, heads, page, dim = k_cache.shape
+    extents = pages, heads, page, dim = k_cache.shape
     if v_cache.shape != (pages, heads, dim, page):
         raise ValueError("v_cache must be [num_pages, heads, dim, page]")
     if k_scale.shape != (pages, heads) or v_scale.shape != (pages, heads):
         raise ValueError("k_scale and v_scale must be [num_pages, heads]")
-    if seq_lens.dim() != 1 or cu_seqlens.shape != (seq_lens.shape[0] + 1,):
+    lens, table = seq_lens.shape, block_table.shape
+    if len(lens) != 1 or cu_seqlens.shape != (lens[0] + 1,):
         raise ValueError("cu_seqlens must be [B + 1] for seq_lens [B]")
-    B = seq_lens.shape[0]
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    if len(table) != 2 or table[0] != lens[0]:
         raise ValueError("block_table must be [B, pages per sequence]")
-    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()), \
-        (pages, heads, page, dim), (block_table.data_ptr(), block_table.shape[1], cu_seqlens.data_ptr(),
-                                    seq_lens.data_ptr()), B
+    return (k_cache.data_ptr(), v_cache.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr()), extents, \
+        (block_table.data_ptr(), table[1], cu_seqlens.data_ptr(), seq_lens.data_ptr()), lens[0]
 
 
 def _need_max(value, name: str) -> int:
@@ -715,11 +714,13 @@ def _need_max(value, name: str) -> int:
 
 def _heads_strides(t, name: str, heads: int, dim: int):
     """(token stride, head stride) of a [T, heads, dim] tensor of contiguous rows."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+    shape = t.shape
+    if len(shape) != 3 or shape[1] != heads or shape[2] != dim:
         raise ValueError(f"{name} must be [T, {heads}, {dim}]")
-    if t.stride(2) != 1 and t.numel():
+    tok, head, one = t.stride()
+    if one != 1 and t.numel():
         raise ValueError(f"{name} must have a unit stride along its last dimension")
-    return (t.stride(0) if t.shape[0] > 1 else heads * dim), (t.stride(1) if heads > 1 else dim)
+    return (tok if shape[0] > 1 else heads * dim), (head if heads > 1 else dim)
 
 
 def kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_lens, max_new: int):
@@ -755,7 +756,8 @@ def kv8_gather(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, seq_
     shape = (_need_max(total, "total"), heads, dim)
     if out is None:
         _y_dtype8(out_dtype)
-        k, v = (torch.empty(shape, dtype=out_dtype, device=k_cache.device) for _ in range(2))
+        k = torch.empty(shape, dtype=out_dtype, device=k_cache.device)
+        v = torch.empty_like(k)
     else:
         k, v = out
         if isinstance(k, torch.Tensor):
