@@ -59,6 +59,7 @@ struct AttnParams {
   KvBatch b;
   KvQuery q;
   int group;             // query heads per kv head
+  unsigned group_magic;  // ceil(2^32 / group), for token_of
   int tile_rows, tiles;  // query rows per workgroup, row tiles of the longest sequence
   int splits;
   int split;             // positions per split (a multiple of 64 times the waves)
@@ -137,29 +138,34 @@ __device__ __forceinline__ void store4_as(void* y, int ydt, int64_t i, v4f v) {
   }
 }
 
-// Positions a tile of query rows [r0, r1) of a sequence can see: [lo, hi), lo a
-// multiple of 64.
+// Positions the tokens [t0, t1] of a sequence can see: [lo, hi), lo a multiple of
+// 64.
 struct Range {
   int lo, hi;
 };
-__device__ __forceinline__ Range tile_range(const AttnParams& p, const Seq& s, int r0, int r1) {
+__device__ __forceinline__ Range token_range(const AttnParams& p, const Seq& s, int t0, int t1) {
   const int p0 = s.len - s.n;
   Range r{0, s.len};
-  if (p.q.causal) r.hi = min(s.len, p0 + (r1 - 1) / p.group + 1);
-  if (p.q.window > 0) r.lo = max(0, p0 + r0 / p.group - p.q.window + 1) & ~63;
+  if (p.q.causal) r.hi = min(s.len, p0 + t1 + 1);
+  if (p.q.window > 0) r.lo = max(0, p0 + t0 - p.q.window + 1) & ~63;
   r.hi = max(r.hi, r.lo);
   return r;
+}
+// The same for a tile of query rows [r0, r1).
+__device__ __forceinline__ Range tile_range(const AttnParams& p, const Seq& s, int r0, int r1) {
+  return token_range(p, s, r0 / p.group, (r1 - 1) / p.group);
 }
 
 // A workgroup's work: row tile `tile` of (sequence, kv head, split), the heads
 // innermost: where they are a multiple of 8, the tiles of one head run on one
-// XCD (workgroup index mod 8), whose L2 fetches its codes once.
+// XCD (workgroup index mod 8), whose L2 fetches its codes once. (As a grid of
+// three dimensions, without the divisions, 131072 positions took 2 % longer.)
 struct Work {
   int seq, h, split, tile;
 };
 __device__ __forceinline__ Work work_of(const AttnParams& p) {
-  unsigned x = blockIdx.x;
   Work w;
+  unsigned x = blockIdx.x;
   w.h = x % p.c.heads;
   x /= p.c.heads;
   w.tile = x % p.tiles;
@@ -167,6 +173,12 @@ __device__ __forceinline__ Work work_of(const AttnParams& p) {
   w.split = x % p.splits;
   w.seq = x / p.splits;
   return w;
+}
+
+// r / group for the rows of k_kv8_decode and k_kv8_draft: r (ceil(2^32 / group)
+// group - 2^32) < 2^32, since r < 2^16 and group < 2^16.
+__device__ __forceinline__ int token_of(const AttnParams& p, int r) {
+  return p.group == 1 ? r : (int)__umulhi((unsigned)r, p.group_magic);
 }
 
 // The end of a workgroup whose NW waves hold partial results of the same R query
@@ -191,7 +203,7 @@ __device__ __forceinline__ void join_waves(const AttnParams& p, const Seq& s, co
       L += ll[w][r - r0] * e;
       o += *reinterpret_cast<const v4f*>(&lo_[w][r - r0][d]) * e;
     }
-    const int tok = r / p.group;
+    const int tok = token_of(p, r);
     const int64_t row = (int64_t)(s.t0 + tok) * p.q.heads + wk.h * p.group + r - tok * p.group;
     if (nsplit == 1) {
       store4_as(p.q.y, p.q.ydtype, row * D + d, L == 0.0f ? v4f{0, 0, 0, 0} : o * (1.0f / L));
@@ -209,7 +221,7 @@ __device__ __forceinline__ void join_waves(const AttnParams& p, const Seq& s, co
 // waves take chunks of 64 positions in turn, with no sharing until the end.
 // Bound by HBM: 64 ragged rows up to 4096, 8 query heads per kv head, 57 us, 4.8
 // TB/s of codes; 131072 positions 43 us and a joining launch. Short contexts by the chain of loads
-// (lengths, table, codes) and the launch: 257 positions 8.4 us. Two chunks in
+// (lengths, table, codes) and the launch: 257 positions 7.4 us. Two chunks in
 // flight per wave instead of one measured the same (61.2 and 62.6 us for the 64
 // rows, 43.5 and 40.0 for 20 of 4096), three waves per SIMD in place of two were
 // slower (75).
@@ -228,21 +240,21 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
   const int rows = s.n * p.group;
   const int r0 = tile * 16;
   if (r0 >= rows) return;
-  const Range rg = tile_range(p, s, r0, min(r0 + 16, rows));
+  const Range rg = token_range(p, s, token_of(p, r0), token_of(p, min(r0 + 16, rows) - 1));
   const int nsplit = max(1, (rg.hi - rg.lo + p.split - 1) / p.split);
   if (w.split >= nsplit) return;
   const int from = rg.lo + w.split * p.split, to = min(rg.hi, from + p.split);
 
   // query row of this lane's column
   const int r = min(r0 + c, rows - 1);
-  const int tok = r / p.group, hq = h * p.group + r % p.group;
+  const int tok = token_of(p, r), hq = h * p.group + r - tok * p.group;
   const int pos = s.len - s.n + tok;
   auto hi_of = [&](int x) { return p.q.causal ? min(s.len, x + 1) : s.len; };
   auto lo_of = [&](int x) { return p.q.window > 0 ? max(0, x - p.q.window + 1) : 0; };
   const int row_hi = hi_of(pos), row_lo = lo_of(pos);
   // positions that every row of the tile sees
-  const int all_hi = min(hi_of(s.len - s.n + r0 / p.group), to);
-  const int all_lo = lo_of(s.len - s.n + min(r0 + 15, rows - 1) / p.group);
+  const int all_hi = min(hi_of(s.len - s.n + token_of(p, r0)), to);
+  const int all_lo = lo_of(s.len - s.n + token_of(p, min(r0 + 15, rows - 1)));
   const int P = p.c.page;
   const int* const table = p.b.table + seq * p.b.table_ld;
   const uint32_t page_bytes = (uint32_t)p.c.heads * P * D;     // < 2^32
@@ -389,8 +401,9 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
   join_waves<D, NW, 16>(p, s, w, r0, rows, nsplit, lo_, lm, ll);
 }
 
-// 17 to 128 rows per kv head (drafts being verified, chunks of a few tokens): as k_kv8_decode with 32 rows a workgroup, so that a code is widened
-// for twice the rows. S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_f16:
+// 17 to 128 rows per kv head (drafts being verified, chunks of a few tokens): as
+// k_kv8_decode with 32 rows a workgroup, so that a code is widened for twice the
+// rows. S^T = K Q^T and O^T = V^T P^T with v_mfma_f32_32x32x16_f16:
 // lane l supplies 8 consecutive k of row l % 32 at k offset 8 (l / 32), result
 // register i of lane half hi is row 8 (i / 4) + 4 hi + i % 4. A chunk's 64
 // positions are two tiles T; that row is position 32 T + 16 hi + i, so a lane
@@ -418,19 +431,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int rows = s.n * p.group;
   const int r0 = w.tile * 32;
   if (r0 >= rows) return;
-  const Range rg = tile_range(p, s, r0, min(r0 + 32, rows));
+  const Range rg = token_range(p, s, token_of(p, r0), token_of(p, min(r0 + 32, rows) - 1));
   const int nsplit = max(1, (rg.hi - rg.lo + p.split - 1) / p.split);
   if (w.split >= nsplit) return;
   const int from = rg.lo + w.split * p.split, to = min(rg.hi, from + p.split);
 
   const int r = min(r0 + c, rows - 1);
-  const int tok = r / p.group, hq = h * p.group + r % p.group;
+  const int tok = token_of(p, r), hq = h * p.group + r - tok * p.group;
   const int pos = s.len - s.n + tok;
   auto hi_of = [&](int x) { return p.q.causal ? min(s.len, x + 1) : s.len; };
   auto lo_of = [&](int x) { return p.q.window > 0 ? max(0, x - p.q.window + 1) : 0; };
   const int row_hi = hi_of(pos), row_lo = lo_of(pos);
-  const int all_hi = min(hi_of(s.len - s.n + r0 / p.group), to);
-  const int all_lo = lo_of(s.len - s.n + min(r0 + 31, rows - 1) / p.group);
+  const int all_hi = min(hi_of(s.len - s.n + token_of(p, r0)), to);
+  const int all_lo = lo_of(s.len - s.n + token_of(p, min(r0 + 31, rows - 1)));
   const int P = p.c.page;
   const int* const table = p.b.table + seq * p.b.table_ld;
   const uint32_t page_bytes = (uint32_t)p.c.heads * P * D;     // < 2^32
@@ -1152,6 +1165,7 @@ void launch_kv8_attention(const KvPool& c, const KvBatch& b, const KvQuery& q, v
   p.b = b;
   p.q = q;
   p.group = q.heads / c.heads;
+  p.group_magic = (unsigned)(((uint64_t{1} << 32) + p.group - 1) / p.group);
   p.tile_rows = pl.tile_rows;
   p.tiles = pl.tiles;
   p.splits = pl.splits;
