@@ -28,6 +28,7 @@
 #include <type_traits>
 
 #include "kv8_common.h"
+#include "quant8.h"
 
 namespace w4a4 {
 
@@ -95,12 +96,10 @@ __device__ __forceinline__ float query_operands(uint4 (&raw)[N], bool bf16, bool
     return 1.0f;
   }
   uint32_t m = 0;
+  static_assert(N % 2 == 0, "16 elements at a time");
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-#pragma unroll
-    for (int k = 0; k < 4; ++k) m = max(m, max((w[k] & 0x7FFFu) << 16, w[k] & 0x7FFF0000u));
-  }
+  for (int i = 0; i < N; i += 2) m = absmax16(raw + i, m);
+  m = max(m & 0xFFFFu, m >> 16) << 16;
 #pragma unroll
   for (int x = FIRST_XOR; x < 64; x *= 2) m = max(m, (uint32_t)__shfl_xor((int)m, x));
   // exponent of the largest element to 14; a row of zeros and subnormals stays as it is
@@ -330,18 +329,17 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
       load_k(at + 64 * NW);
       load_pages(at + 128 * NW);
     }
-    const float f = ks * qscale;
+    float f = ks * qscale;                             // >= 0
     const int first = at + 16 * g;
-    float cm = kNone;
+    float cm = sc[0][0];
     if (at >= all_lo && at + 64 <= all_hi && __all(ok)) {
 #pragma unroll
       for (int t = 0; t < 4; ++t)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          sc[t][i] *= f;
-          cm = fmaxf(cm, sc[t][i]);
-        }
+        for (int i = 0; i < 4; ++i) cm = fmaxf(cm, sc[t][i]);
+      cm *= f;
     } else {
+      cm = kNone;
       const int lim = ok ? min(row_hi, to) : 0;
 #pragma unroll
       for (int t = 0; t < 4; ++t)
@@ -351,6 +349,7 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
           sc[t][i] = j >= row_lo && j < lim ? sc[t][i] * f : -INFINITY;
           cm = fmaxf(cm, sc[t][i]);
         }
+      f = 1.0f;
     }
     cm = fmaxf(cm, __shfl_xor(cm, 16));
     cm = max_halves(cm);
@@ -361,16 +360,17 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
     const float al = __builtin_amdgcn_exp2f(m - m2);
     const float ao = al * (vref / vref2);
     const float w = vs_here / vref2 * 32768.0f;
-    l *= al;
+    float sum[2] = {l * al, 0.0f};
     v8h pf[2];
 #pragma unroll
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const float e = __builtin_amdgcn_exp2f(sc[t][i] - m2);
-        l += e;
+        const float e = __builtin_amdgcn_exp2f(fmaf(sc[t][i], f, -m2));
+        sum[i & 1] += e;
         pf[t >> 1][4 * (t & 1) + i] = (_Float16)(e * w);
       }
+    l = sum[0] + sum[1];
     if (__any(m2 != m) || vref2 != vref) {
 #pragma unroll
       for (int i = 0; i < DT; ++i)
@@ -413,10 +413,10 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
 //
 // Bound by the chain of loads at the start (lengths, table, codes: 4 us of it),
 // then by about 5000 cycles a chunk of a wave: its codes' way from memory beside
-// 650 vector instructions (320 of them widen codes) and 32 matrix ones. 35 rows
+// 600 vector instructions (320 of them widen codes) and 32 matrix ones. 35 rows
 // in a window of 1024, 24 sequences of 4 kv heads: 19 us; 64 rows of 4096, 8
-// sequences of 8 kv heads: 34 us in two splits, 47 in one. Neither fewer vector
-// instructions per score nor eight waves a workgroup made it faster.
+// sequences of 8 kv heads: 34 us in two splits, 47 in one. Eight waves a
+// workgroup were slower.
 template <int D, int NW>
 __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2))) void k_kv8_draft(AttnParams p) {
   constexpr int KB = D / 32, DT = D / 32;              // 16-byte pieces of a half row of K, 32-dimension tiles of O
@@ -531,24 +531,25 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
       load_k(at + 64 * NW);
       load_pages(at + 128 * NW);
     }
-    float cm = kNone;
+    float cm = kNone, f[2] = {ks[0] * qscale, ks[1] * qscale};   // >= 0
     if (at >= all_lo && at + 64 <= all_hi && __all(ok[0] && ok[1])) {
 #pragma unroll
-      for (int T = 0; T < 2; ++T)
+      for (int T = 0; T < 2; ++T) {
+        float x = sc[T][0];
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          sc[T][i] *= ks[T] * qscale;
-          cm = fmaxf(cm, sc[T][i]);
-        }
+        for (int i = 1; i < 16; ++i) x = fmaxf(x, sc[T][i]);
+        cm = fmaxf(cm, x * f[T]);
+      }
     } else {
 #pragma unroll
       for (int T = 0; T < 2; ++T) {
         const int first = at + 32 * T + 16 * hi, lim = ok[T] ? min(row_hi, to) : 0;
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
-          sc[T][i] = first + i >= row_lo && first + i < lim ? sc[T][i] * (ks[T] * qscale) : -INFINITY;
+          sc[T][i] = first + i >= row_lo && first + i < lim ? sc[T][i] * f[T] : -INFINITY;
           cm = fmaxf(cm, sc[T][i]);
         }
+        f[T] = 1.0f;
       }
     }
     cm = max_halves(cm);
@@ -559,18 +560,19 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     const float al = __builtin_amdgcn_exp2f(m - m2);
     const float ao = al * (vref / vref2);
     const float unit = 32768.0f / vref2;
-    l *= al;
+    float sum[2] = {l * al, 0.0f};
     v8h pf[2][2];
 #pragma unroll
     for (int T = 0; T < 2; ++T) {
       const float wt = (T ? vs1 : vs0) * unit;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
-        const float e = __builtin_amdgcn_exp2f(sc[T][i] - m2);
-        l += e;
+        const float e = __builtin_amdgcn_exp2f(fmaf(sc[T][i], f[T], -m2));
+        sum[i & 1] += e;
         pf[T][i >> 3][i & 7] = (_Float16)(e * wt);
       }
     }
+    l = sum[0] + sum[1];
     if (__any(m2 != m) || vref2 != vref) {
 #pragma unroll
       for (int i = 0; i < DT; ++i)
