@@ -559,12 +559,12 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
     const float m2 = fmaxf(m, cm), vref2 = fmaxf(vref, vm);
     const float al = __builtin_amdgcn_exp2f(m - m2);
     const float ao = al * (vref / vref2);
-    const float unit = 32768.0f / vref2;
+    const float unit = 1.0f / vref2;                   // finite: vref2 >= kTinyScale (2^15 over it would not be)
     float sum[2] = {l * al, 0.0f};
     v8h pf[2][2];
 #pragma unroll
     for (int T = 0; T < 2; ++T) {
-      const float wt = (T ? vs1 : vs0) * unit;
+      const float wt = (T ? vs1 : vs0) * unit * 32768.0f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const float e = __builtin_amdgcn_exp2f(fmaf(sc[T][i], f[T], -m2));
