@@ -1,4 +1,5 @@
 """The 8-bit operators at the ends of the range of their inputs."""
+import copy
 import math
 
 import pytest
@@ -60,4 +61,39 @@ def test_whole_pages_that_are_none_of_the_pool(kernel, page):
     y, _ = attend(B, q)
     o, _, bound = attention_ref(ref, q, True, 0, 128 ** -0.5, {0: [(0, page)], 1: [(page, 2 * page)]})
     t = B.cu_host[-1]
+    assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -11 * (o.abs() + bound) + 2.0 ** -25)[:t]).all())
+
+
+# ------------------------------------------------------- negative positions
+
+def seen_ref(B, q, causal, window, max_len=None):
+    """As attention_ref, for sequences with more new tokens than positions (their
+    first tokens see nothing), lengths cut to max_len."""
+    import torch
+    o = torch.zeros(q.shape, dtype=torch.float64, device="cuda")
+    bound, lse = torch.zeros_like(o), torch.full(q.shape[:2], -math.inf, dtype=torch.float64, device="cuda")
+    for b, (n, length) in enumerate(zip(B.new, B.lens)):
+        length = length if max_len is None else min(length, max_len)
+        C = copy.copy(B)
+        C.new, C.lens, C.cu_host, C.table = [min(n, length)], [length], [0, min(n, length)], B.table[b:b + 1]
+        rows = slice(B.cu_host[b + 1] - C.new[0], B.cu_host[b + 1])
+        o[rows], lse[rows], bound[rows] = attention_ref(C, q[rows].contiguous(), causal, window, B.dim ** -0.5)
+    return o, lse, bound
+
+
+@pytest.mark.parametrize("causal,window", [(False, 0), (False, 3), (False, 100), (True, 0), (True, 100)])
+@pytest.mark.parametrize("new,lens,max_len", [([5, 2], [3, 1], None), ([4, 4], [130, 3], 3), ([20, 25], [7, 90], None),
+                                              ([30, 6], [200, 100], 17), ([90, 150], [70, 200], None),
+                                              ([150, 100], [300, 300], 100), ([6, 200], [0, 1], None)])
+@pytest.mark.parametrize("dim", [128, 192])
+def test_tokens_at_negative_positions_see_nothing(new, lens, max_len, causal, window, dim):
+    import torch
+    B = Batch(new, lens, 2, dim, 16, seed=53)
+    q = B.rand(6)
+    y, lse = ops().kv8_attention(q, *B.pool, B.max_new, B.max_len if max_len is None else max_len, causal=causal,
+                                 window=window, return_lse=True)
+    o, want, bound = seen_ref(B, q, causal, window, max_len)
+    t = B.cu_host[-1]
+    assert torch.equal(torch.isinf(lse[:t]), torch.isinf(want[:t])), "which rows see something"
+    assert bool((y[:t][torch.isinf(want[:t])] == 0).all())
     assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -11 * (o.abs() + bound) + 2.0 ** -25)[:t]).all())

@@ -137,6 +137,11 @@ __device__ __forceinline__ void store4_as(void* y, int ydt, int64_t i, v4f v) {
   }
 }
 
+// A query at position x sees positions below this; at a negative one it sees none.
+__device__ __forceinline__ int sees_below(const AttnParams& p, const Seq& s, int x) {
+  return p.q.causal ? min(s.len, x + 1) : x < 0 ? 0 : s.len;
+}
+
 // Positions the tokens [t0, t1] of a sequence can see: [lo, hi), lo a multiple of
 // 64.
 struct Range {
@@ -248,7 +253,7 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
   const int r = min(r0 + c, rows - 1);
   const int tok = token_of(p, r), hq = h * p.group + r - tok * p.group;
   const int pos = s.len - s.n + tok;
-  auto hi_of = [&](int x) { return p.q.causal ? min(s.len, x + 1) : s.len; };
+  auto hi_of = [&](int x) { return sees_below(p, s, x); };
   auto lo_of = [&](int x) { return p.q.window > 0 ? max(0, x - p.q.window + 1) : 0; };
   const int row_hi = hi_of(pos), row_lo = lo_of(pos);
   // positions that every row of the tile sees
@@ -439,7 +444,7 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
   const int r = min(r0 + c, rows - 1);
   const int tok = token_of(p, r), hq = h * p.group + r - tok * p.group;
   const int pos = s.len - s.n + tok;
-  auto hi_of = [&](int x) { return p.q.causal ? min(s.len, x + 1) : s.len; };
+  auto hi_of = [&](int x) { return sees_below(p, s, x); };
   auto lo_of = [&](int x) { return p.q.window > 0 ? max(0, x - p.q.window + 1) : 0; };
   const int row_hi = hi_of(pos), row_lo = lo_of(pos);
   const int all_hi = min(hi_of(s.len - s.n + token_of(p, r0)), to);
@@ -669,7 +674,7 @@ void k_kv8_prefill(AttnParams p) {
   const int wr0 = r0 + 32 * (wave % (NW / DS)), d0 = wave / (NW / DS) * (D / DS);
   const int r = min(wr0 + l32, rows - 1);
   const int tok = r / p.group, hq = h * p.group + r % p.group;
-  auto row_hi = [&](int tk) { return p.q.causal ? min(s.len, s.len - s.n + tk + 1) : s.len; };
+  auto row_hi = [&](int tk) { return sees_below(p, s, s.len - s.n + tk); };
   auto row_lo = [&](int tk) { return p.q.window > 0 ? max(0, s.len - s.n + tk - p.q.window + 1) : 0; };
   const int my_hi = row_hi(tok), my_lo = row_lo(tok);
   const int tok_a = __builtin_amdgcn_readfirstlane(min(wr0, rows - 1) / p.group);
