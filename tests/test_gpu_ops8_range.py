@@ -2,9 +2,10 @@
 import copy
 import math
 
+import numpy as np
 import pytest
 
-from test_gpu_kv8 import Batch, attention_ref
+from test_gpu_kv8 import Batch, attention_ref, check_append
 
 pytestmark = pytest.mark.gpu
 
@@ -97,3 +98,22 @@ def test_tokens_at_negative_positions_see_nothing(new, lens, max_len, causal, wi
     assert torch.equal(torch.isinf(lse[:t]), torch.isinf(want[:t])), "which rows see something"
     assert bool((y[:t][torch.isinf(want[:t])] == 0).all())
     assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -11 * (o.abs() + bound) + 2.0 ** -25)[:t]).all())
+
+
+# ------------------------------------------------- results half way between two
+
+@pytest.mark.parametrize("top", [2.0, 6.0, 10.0, 12.0, 14.0, 96.0])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_rescaled_codes_round_their_product_first(top, dtype):
+    """Every code of a page with maximum 1 when the maximum becomes `top`: rne(fl32(q
+    fl32(s_old / s))), whose product lies within a rounding of a half for many."""
+    import torch
+    B = Batch([1, 3], [33, 18], 2, 64, 64, dtype, seed=54)
+    B.kc[:] = ((torch.arange(B.kc.numel(), device="cuda") % 255) - 127).to(torch.int8).view(B.kc.shape)
+    B.vc[:] = ((torch.arange(B.vc.numel(), device="cuda") % 255) - 127).to(torch.int8).view(B.vc.shape)
+    one = torch.tensor(np.float32(1) / np.float32(127), device="cuda")
+    B.ks[:], B.vs[:] = one, one
+    k, v = B.rand(2, 0.01), B.rand(2, 0.01)
+    k[0, :, 5], k[1, :, 9] = top, -top
+    v[0, :, 63], v[1, :, 0] = -top, top
+    check_append(B, k, v)

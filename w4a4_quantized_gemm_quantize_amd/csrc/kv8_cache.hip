@@ -30,8 +30,11 @@ namespace {
 constexpr int kThreads = 256;
 
 // rne(fl32(q r)) of the four codes of a word (|q r| <= 127): as in codes16, the
-// addition of 1.5 2^23 rounds and leaves the code in the low byte.
+// addition of 1.5 2^23 rounds and leaves the code in the low byte. The product
+// has to round to fp32 before it (fused, 22 of the 255 codes differ by one for
+// s_old / s = 1 / 6).
 __device__ __forceinline__ uint32_t rescale4(uint32_t w, float r) {
+#pragma clang fp contract(off)
   uint32_t b[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
