@@ -425,7 +425,7 @@ w4a4_status_t w8a8_pack_weight(const void* w, int32_t w_dtype, int64_t N, int64_
 /*
  * W8A8 GEMM:
  *   P[m,n] = sum_k xq[m,k] * wq[n,k]    (exact: 128^2 K < 2^31)
- *   Y[m,n] = fl32(fl32(P) * fl32(xs[m] * ws[n])) (+ bias[n]), as y_dtype
+ *   Y[m,n] = fl32(fl32(fl32(P) * fl32(xs[m] * ws[n])) + bias[n]), as y_dtype
  *
  *   xq, wq   int8 [M][K], [N][K] (any code, -128 included), 16-byte aligned
  *   xs, ws   f32 [M], [N];  bias  f32 [N] or NULL

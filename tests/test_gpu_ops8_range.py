@@ -117,3 +117,24 @@ def test_rescaled_codes_round_their_product_first(top, dtype):
     k[0, :, 5], k[1, :, 9] = top, -top
     v[0, :, 63], v[1, :, 0] = -top, top
     check_append(B, k, v)
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 130, 256), (7, 8200, 1024), (12, 300, 4112), (33, 100, 4096), (64, 130, 8192),
+                                   (130, 256, 512), (300, 520, 1024), (2048, 512, 256)])
+def test_bias_is_added_to_the_rounded_product(M, N, K):
+    """fl32(fl32(fl32(P) fl32(xs ws)) + bias), bit for bit: the streaming kernel, the
+    tiles with element and with wide stores, the join of K ranges."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(56)
+    q = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    w = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
+    s, t = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
+    b = torch.randn(N, generator=g, device="cuda") * 100
+    p = (q.double() @ w.double().t()).cpu().numpy()                   # exact: below 2^53
+    sc = s.cpu().numpy()[:, None] * t.cpu().numpy()[None, :]
+    want = p.astype(np.float32) * sc + b.cpu().numpy()[None, :]
+    assert want.dtype == np.float32
+    y = ops().w8a8_gemm(q, s, w, t, bias=b)
+    assert np.array_equal(y.cpu().numpy(), want)
+    zero = torch.zeros_like(b)
+    assert np.array_equal(ops().w8a8_gemm(q, s, w, t, bias=zero).cpu().numpy(), p.astype(np.float32) * sc)

@@ -4,7 +4,7 @@
 //
 //   a = max_k |x|, s = fl32(a / 127), q = rne(fl32(x / s)) in [-127, 127]
 //   P[m,n] = sum_k xq[m,k] wq[n,k]            (int32, exact for K <= 131056)
-//   Y[m,n] = fl32(fl32(P) fl32(xs[m] ws[n])) + bias[n]
+//   Y[m,n] = fl32(fl32(fl32(P) fl32(xs[m] ws[n])) + bias[n])
 //
 // The scales do not vary along K, so the whole reduction stays in the matrix
 // cores' int32 accumulators and any split of K gives the same bits.
@@ -118,8 +118,10 @@ struct W8Params {
   int stages;                 // 128-k stages per range
 };
 
-// Y value of an exact sum, and its store as ydt (0 fp32, 1 fp16, 2 bf16).
+// Y value of an exact sum (the product rounds to fp32 before the bias is added: no
+// fma), and its store as ydt (0 fp32, 1 fp16, 2 bf16).
 __device__ __forceinline__ float scaled(int p, float sa, float sw, float b) {
+#pragma clang fp contract(off)
   return (float)p * (sa * sw) + b;
 }
 __device__ __forceinline__ uint16_t bf16_rne(float v) {
