@@ -138,3 +138,70 @@ def test_bias_is_added_to_the_rounded_product(M, N, K):
     assert np.array_equal(y.cpu().numpy(), want)
     zero = torch.zeros_like(b)
     assert np.array_equal(ops().w8a8_gemm(q, s, w, t, bias=zero).cpu().numpy(), p.astype(np.float32) * sc)
+
+
+# ------------------------------------------------------------- large scores
+
+@pytest.mark.parametrize("dtype,ks,exp", [("float16", 1817 / 127, 0), ("float16", 40.0, 0), ("float16", 1e4, 0),
+                                          ("bfloat16", 40.0, 0), ("bfloat16", 300.0, 40)])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_one_key_far_above_the_others(kernel, dtype, ks, exp):
+    """Scores of 3e7 and more, where a rounding of one moves its weight by whole
+    powers of two: one key of a head is above the others by half its score and
+    takes all the weight. The output is that key's values: its weight is rounded to
+    11 bits, and a page's scale may pass through its log2 (below 16, so steps of
+    2^-20: three of them, and the sums)."""
+    import torch
+    new, lens, heads = KERNELS[kernel]
+    for page in (64, 16):
+        B = Batch(new, lens, 2, 128, page, dtype, seed=57)
+        B.kc[:] = torch.randint(-40, 41, B.kc.shape, generator=B.g, device="cuda", dtype=torch.int8)
+        B.ks[:] = ks
+        best = [[70, 141], [3, 400]]
+        t = B.cu_host[-1]
+        q = (torch.rand(B.total, heads, 128, generator=B.g, device="cuda") * 800 + 1000).to(B.dtype) * 2.0 ** exp
+        want = torch.zeros((t, heads, 128), dtype=torch.float64, device="cuda")
+        top = torch.zeros((t, heads), dtype=torch.float64, device="cuda")
+        for b in range(2):
+            rows = slice(B.cu_host[b], B.cu_host[b + 1])
+            for h in range(2):
+                at = best[b][h]
+                B.kc[int(B.table_host[b, at // page]), h, at % page] = 127
+                v = B.values(b, torch.float64)[1][h, at]
+                want[rows, 4 * h:4 * h + 4] = v
+                top[rows, 4 * h:4 * h + 4] = 127 * float(B.ks[0, 0]) * 128 ** -0.5 * q[rows, 4 * h:4 * h + 4].double().sum(-1)
+        y, lse = attend(B, q, out_dtype=torch.float32)
+        y, lse = y[:t].double(), lse[:t].double()
+        assert bool(torch.isfinite(y).all()) and bool(torch.isfinite(lse).all())
+        assert bool(((y - want).abs() <= (2.0 ** -11 + 2.0 ** -18) * want.abs()).all())
+        # 128 products of one sign summed in fp32, the factors' roundings
+        assert bool(((lse - top).abs() <= (128 + 16) * 2.0 ** -24 * top).all())
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_large_scores_that_rise_by_little(kernel):
+    """Scores of 6e7 (in units of ln 2) that rise by 2 of their roundings from one
+    chunk of positions to the next: whatever the weights are, they are weights:
+    outputs lie between the values."""
+    import torch
+    new, lens, heads = KERNELS[kernel]
+    for q0 in (1024.0, 1023.0, 1020.0, 1001.0):
+        B = Batch(new, lens, 2, 128, 64, seed=58)
+        B.kc[:] = 0
+        B.ks[:] = 1.0
+        for b, length in enumerate(lens):
+            for j in range(-(-length // 64)):
+                page = int(B.table_host[b, j])
+                B.kc[page, :, :, 0] = 127
+                B.kc[page, :, :, 1] = j
+        q = torch.zeros(B.total, heads, 128, dtype=torch.float16, device="cuda")
+        q[..., 0], q[..., 1] = q0, 2.0 ** -6
+        t = B.cu_host[-1]
+        for scale in (512 * math.log(2), -512 * math.log(2)):
+            y, lse = attend(B, q if scale > 0 else -q, scale=scale, out_dtype=torch.float32)
+            assert bool(torch.isfinite(y[:t]).all()) and bool(torch.isfinite(lse[:t]).all())
+            for b in range(len(lens)):
+                rows = slice(B.cu_host[b], B.cu_host[b + 1])
+                big = B.values(b, torch.float64)[1].abs().amax(dim=1).repeat_interleave(heads // 2, 0)
+                # weights rounded to 11 bits, their sum to fp32
+                assert bool((y[rows].double().abs() <= big[None] * (1 + 2.0 ** -10)).all())

@@ -37,6 +37,12 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kNone = -3.0e38f;          // running maximum of a row that has seen nothing
 constexpr float kTinyScale = 0x1p-120f, kTinyLog = -120.0f;
+// Scores (in log2 units) up to this size keep their factor in the weight's exponent,
+// one fma; the maximum that is taken from it there has rounded, so the largest
+// score's exponent is that rounding, not 0. Up to 2^10 it is 2^-14 at most, under
+// the weights' own 2^-11. Past 2^25 it would be 2 and more, and a weight no fp16:
+// larger scores are rounded first.
+constexpr float kFusedScores = 1024.0f;
 // k_kv8_prefill: weights up to 2^kSlack (the running maximum may lag so far)
 // enter fp16 times 2^kBias: at most 2^15
 constexpr float kBias = 9.0f, kSlack = 6.0f;
@@ -343,6 +349,13 @@ __attribute__((amdgpu_waves_per_eu(D > 192 ? 1 : 2, D > 192 ? 1 : 2))) void k_kv
 #pragma unroll
         for (int i = 0; i < 4; ++i) cm = fmaxf(cm, sc[t][i]);
       cm *= f;
+      if (__any(fabsf(cm) > kFusedScores)) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) sc[t][i] *= f;
+        f = 1.0f;
+      }
     } else {
       cm = kNone;
       const int lim = ok ? min(row_hi, to) : 0;
@@ -543,7 +556,15 @@ __global__ __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(2, 2)))
         float x = sc[T][0];
 #pragma unroll
         for (int i = 1; i < 16; ++i) x = fmaxf(x, sc[T][i]);
-        cm = fmaxf(cm, x * f[T]);
+        cm = T == 0 ? x * f[0] : fmaxf(cm, x * f[1]);   // (NaN queries: not kNone, which is no score)
+      }
+      if (__any(fabsf(cm) > kFusedScores)) {
+#pragma unroll
+        for (int T = 0; T < 2; ++T) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) sc[T][i] *= f[T];
+          f[T] = 1.0f;
+        }
       }
     } else {
 #pragma unroll
@@ -854,10 +875,22 @@ void k_kv8_prefill(AttnParams p) {
       lmin = fminf(lmin, lvs[b]);
     }
     float m2;
-    // masked positions, and scales too far apart for the sum of weights over scale
-    const bool rare = at + TW > hi_min || at < lo_max || none || !(lmin >= lref2 - 40.0f);
+    // masked positions, scales too far apart for the sum of weights over scale, large
+    // scores
+    bool rare = at + TW > hi_min || at < lo_max || none || !(lmin >= lref2 - 40.0f);
     float cm = kNone;
+    if (!rare) {
+#pragma unroll
+      for (int g = 0; g < NF; ++g) {                   // scores that share a factor
+        float x = sc[g >> 1][8 * (g & 1)];
+#pragma unroll
+        for (int k = 1; k < 16 * (TW / 32) / NF; ++k) x = fmaxf(x, sc[(8 * g + k) >> 4][(8 * g + k) & 15]);
+        cm = g == 0 ? x * f[0] : fmaxf(cm, x * f[g]);   // (NaN queries: not kNone, which is no score)
+      }
+      rare = __any(fabsf(cm) > kFusedScores);
+    }
     if (rare) {
+      cm = kNone;
 #pragma unroll
       for (int t = 0; t < TW / 32; ++t)
 #pragma unroll
@@ -866,20 +899,12 @@ void k_kv8_prefill(AttnParams p) {
           sc[t][k] = j >= my_lo && j < my_hi && !(none >> b & 1) ? sc[t][k] * f[b % NF] : -INFINITY;
           cm = fmaxf(cm, sc[t][k]);
         }
-    } else {
-#pragma unroll
-      for (int g = 0; g < NF; ++g) {                   // scores that share a factor
-        float x = sc[g >> 1][8 * (g & 1)];
-#pragma unroll
-        for (int k = 1; k < 16 * (TW / 32) / NF; ++k) x = fmaxf(x, sc[(8 * g + k) >> 4][(8 * g + k) & 15]);
-        cm = fmaxf(cm, x * f[g]);
-      }
     }
     // The maximum only has to keep the weights within fp16: it stays where it is
     // until some row passes it by 2^kSlack (rescaling O in most tiles of 8192
     // positions cost 14 % of the time).
     m2 = fmaxf(m, max_halves(cm));
-    if (__any(m2 > m + kSlack) || lref2 != lref) {
+    if (__any(m2 - m > kSlack) || lref2 != lref) {     // (m + kSlack would round where m is large)
       const float al = __builtin_amdgcn_exp2f(m - m2), ao = __builtin_amdgcn_exp2f(m - m2 + (lref - lref2));
       l *= al;
 #pragma unroll
