@@ -91,9 +91,10 @@ w4a4_status_t kv8_gather(const int8_t* k_cache, const int8_t* v_cache, const flo
  * Codes enter the matrix products exactly; softmax statistics and sums are
  * fp32. A weight (softmax numerator times its page's value scale) is rounded to
  * 11 bits, or, where it is under 2^-23 of the largest such, to 2^-34 of the
- * largest page scale; bf16 queries lose elements under 2^-39 of a row's largest.
- * Scales are finite and >= 0; scores may take any size that fp32 holds. Results do not depend on the order in which
- * workgroups run.
+ * largest page scale (2^-120, where all are smaller); bf16 queries lose elements
+ * under 2^-39 of a row's largest. Scales are finite and >= 0; scores may take any
+ * size that fp32 holds. Results do not depend on the order in which workgroups
+ * run.
  */
 w4a4_status_t kv8_attention(const void* q, int32_t x_dtype, int64_t q_tok, int64_t q_head, int32_t q_heads,
                             const int8_t* k_cache, const int8_t* v_cache, const float* k_scale, const float* v_scale,

@@ -205,3 +205,27 @@ def test_large_scores_that_rise_by_little(kernel):
                 big = B.values(b, torch.float64)[1].abs().amax(dim=1).repeat_interleave(heads // 2, 0)
                 # weights rounded to 11 bits, their sum to fp32
                 assert bool((y[rows].double().abs() <= big[None] * (1 + 2.0 ** -10)).all())
+
+
+# ------------------------------------------------------- small value scales
+
+@pytest.mark.parametrize("exp", [-100, -112, -118, -121, -126, -130])
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_values_down_to_subnormal_scales(kernel, exp):
+    """Every value scale in [2^exp, 2^(exp + 1)): the outputs keep their relative
+    precision (the bound of attention_ref, whose absolute term is a share of the
+    largest page scale, 2^-120 at least), the log-sum-exp does not depend on them."""
+    import torch
+    new, lens, heads = KERNELS[kernel]
+    for page in (64, 16):
+        B = Batch(new, lens, 2, 128, page, seed=59)
+        B.vs = torch.ldexp(1 + torch.rand(B.vs.shape, generator=B.g, device="cuda"), torch.tensor(exp, device="cuda"))
+        q = B.rand(heads)
+        t = B.cu_host[-1]
+        o, want, bound = attention_ref(B, q, True, 0, 128 ** -0.5)
+        y, lse = attend(B, q, out_dtype=torch.float32)
+        assert bool(((lse[:t].double() - want[:t]).abs() <= 2.0 ** -10).all())
+        # the output's step, 2^-24 or half a subnormal one, and that of a subnormal factor of the largest scale
+        tiny = max(lens) * 127 * 2.0 ** -34 * 2.0 ** -120 + 2.0 ** -150
+        err = (y.double() - o).abs()[:t]
+        assert bool((err <= (bound + (2.0 ** -24 + 2.0 ** -14) * o.abs())[:t] + tiny).all()), float((err / o.abs()[:t]).max())

@@ -132,6 +132,12 @@ __device__ __forceinline__ float lane_value(float x, int lane) {
   return __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(x), lane));
 }
 
+// log2 of a page scale, subnormal ones too (the instruction takes them as zeros).
+__device__ __forceinline__ float log2_scale(float x) {
+  const bool tiny = x < 0x1p-126f;
+  return __builtin_amdgcn_logf(tiny ? x * 0x1p32f : x) - (tiny ? 32.0f : 0.0f);
+}
+
 // Four outputs at a multiple of 4 elements of the 16-byte aligned y.
 __device__ __forceinline__ void store4_as(void* y, int ydt, int64_t i, v4f v) {
   if (ydt == 0) {
@@ -846,25 +852,22 @@ void k_kv8_prefill(AttnParams p) {
   };
   // scores -> weights of the tile at `at`, whose scales this wave holds
   auto weights = [&](int at) {
-    // factors of the tile's blocks: of the scores, log2 and reciprocal of the V
-    // scale. A block past the last position or of no page is masked; its scales
+    // factors of the tile's blocks: of the scores, and log2 of the V scale. A block past the last position or of no page is masked; its scales
     // must not count.
     constexpr int NF = ONE ? 1 : NB;
-    float f[NF], lvs[NF], ivs[NF];
+    float f[NF], lvs[NF];
     int none = 0;
     if constexpr (ONE) {
       f[0] = ksv * qscale;
-      lvs[0] = gone ? kTinyLog : __builtin_amdgcn_logf(vsv);
-      ivs[0] = __builtin_amdgcn_rcpf(vsv);
+      lvs[0] = gone ? kTinyLog : log2_scale(vsv);
       none = gone ? (1 << NB) - 1 : 0;
     } else {
       const bool past = at + 16 * (lane % NB) >= to || gone;
-      const float lv_ = past ? kTinyLog : __builtin_amdgcn_logf(vsv), iv_ = __builtin_amdgcn_rcpf(vsv);
+      const float lv_ = past ? kTinyLog : log2_scale(vsv);
 #pragma unroll
       for (int b = 0; b < NB; ++b) {
         f[b] = lane_value(ksv, b) * qscale;
         lvs[b] = lane_value(lv_, b);
-        ivs[b] = lane_value(iv_, b);
         none |= __builtin_amdgcn_readlane(gone, b) << b;
       }
     }
@@ -925,7 +928,7 @@ void k_kv8_prefill(AttnParams p) {
           pf[t][k >> 3][k & 7] = (_Float16)(e * __builtin_amdgcn_exp2f(lvs[b % NF] - lref + kBias));
         }
     } else {
-      const float base = kBias - lref - m, unit = __builtin_amdgcn_exp2f(lref - kBias);
+      const float base = kBias - lref - m;
 #pragma unroll
       for (int g = 0; g < NF; ++g) {
         const float c = lvs[g] + base;
@@ -937,7 +940,7 @@ void k_kv8_prefill(AttnParams p) {
           sum[k & 1] += e;
           pf[x >> 4][x >> 3 & 1][x & 7] = (_Float16)e;
         }
-        l = fmaf(sum[0] + sum[1], unit * ivs[g], l);
+        l = fmaf(sum[0] + sum[1], __builtin_amdgcn_exp2f(lref - kBias - lvs[g]), l);
       }
     }
   };
@@ -1006,7 +1009,10 @@ void k_kv8_prefill(AttnParams p) {
   l += __shfl_xor(l, 32);
   if (wr0 + l32 >= rows) return;
   const int64_t row = (int64_t)(s.t0 + tok) * p.q.heads + hq;
-  const float back = __builtin_amdgcn_exp2f(lref - kBias);
+  // (exp2 gives no subnormal numbers: where the factor is one, a power of two of it
+  // is left for the end)
+  const bool tiny = lref < -60.0f;
+  const float back = __builtin_amdgcn_exp2f(lref - kBias + (tiny ? 64.0f : 0.0f)), rest = tiny ? 0x1p-64f : 1.0f;
   if (nsplit == 1) {
     const float out = l == 0.0f ? 0.0f : back / l;
 #pragma unroll
@@ -1016,7 +1022,7 @@ void k_kv8_prefill(AttnParams p) {
         const int64_t o = row * D + d0 + 32 * i + 8 * k + 4 * hi;
         v4f f;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) f[e] = l == 0.0f ? 0.0f : acc[i][4 * k + e] * out;
+        for (int e = 0; e < 4; ++e) f[e] = l == 0.0f ? 0.0f : acc[i][4 * k + e] * out * rest;
         store4_as(p.q.y, p.q.ydtype, o, f);
       }
     if (p.q.lse && hi == 0 && d0 == 0) p.q.lse[row] = l == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) / kLog2e;
@@ -1027,7 +1033,8 @@ void k_kv8_prefill(AttnParams p) {
 #pragma unroll
       for (int k = 0; k < 4; ++k)
         *reinterpret_cast<float4*>(p.part + at * D + d0 + 32 * i + 8 * k + 4 * hi) =
-            float4{acc[i][4 * k] * back, acc[i][4 * k + 1] * back, acc[i][4 * k + 2] * back, acc[i][4 * k + 3] * back};
+            float4{acc[i][4 * k] * back * rest, acc[i][4 * k + 1] * back * rest, acc[i][4 * k + 2] * back * rest,
+                   acc[i][4 * k + 3] * back * rest};
     if (hi == 0 && d0 == 0) {
       float* ml = p.part + (int64_t)p.splits * p.part_rows * D + 2 * at;
       ml[0] = m;
