@@ -48,10 +48,12 @@ extern "C" {
  *   s = max(s_old, fl32(max|new| / 127))
  *   earlier codes, if s > s_old:  q <- rne(fl32(q * fl32(s_old / s)))
  *   new codes:                    rne(fl32(x / s))  (s = 0: 0)
- * Other slots keep their bytes. The pages written must not be shared.
+ * Other slots keep their bytes. The pages written must not be shared. A NaN or an
+ * infinity among the new values makes s NaN (the codes of the new tokens are then
+ * any), until the page is used afresh.
  *
  *   k, v    new keys and values, token t of head h at k + t * k_tok + h * k_head
- *           (elements), dim contiguous; x_dtype W4A4_Y_F16 or W4A4_Y_BF16, finite;
+ *           (elements), dim contiguous; x_dtype W4A4_Y_F16 or W4A4_Y_BF16;
  *           16-byte aligned, strides multiples of 8
  */
 w4a4_status_t kv8_append(const void* k, const void* v, int32_t x_dtype, int64_t k_tok, int64_t k_head,
@@ -93,8 +95,9 @@ w4a4_status_t kv8_gather(const int8_t* k_cache, const int8_t* v_cache, const flo
  * 11 bits, or, where it is under 2^-23 of the largest such, to 2^-34 of the
  * largest page scale (2^-120, where all are smaller); bf16 queries lose elements
  * under 2^-39 of a row's largest. Scales are finite and >= 0; scores may take any
- * size that fp32 holds. Results do not depend on the order in which workgroups
- * run.
+ * size that fp32 holds. A page whose key or value scale is NaN gives NaN to every
+ * query that sees one of its positions, and may to others of its sequence.
+ * Results do not depend on the order in which workgroups run.
  */
 w4a4_status_t kv8_attention(const void* q, int32_t x_dtype, int64_t q_tok, int64_t q_head, int32_t q_heads,
                             const int8_t* k_cache, const int8_t* v_cache, const float* k_scale, const float* v_scale,

@@ -408,7 +408,8 @@ w4a4_status_t nvfp4_gemm_debug_partials(const uint8_t* xq, const uint8_t* xs,
 /*
  * Symmetric INT8 quantization of activations, per row: a = max|x|;
  * s = fl32(a / 127); q = rne(fl32(x / s)) with correctly rounded binary32
- * divisions, in [-127, 127]; an all-zero row gives s = 0 and codes 0. x finite.
+ * divisions, in [-127, 127]; an all-zero row gives s = 0 and codes 0. A row with a
+ * NaN or an infinity gives s = NaN and any codes, so its products are NaN.
  *
  *   x       [M][ldx] row-major, 16-byte aligned, ldx >= K, ldx % 8 == 0, of
  *           x_dtype W4A4_Y_F16 or W4A4_Y_BF16

@@ -229,3 +229,75 @@ def test_values_down_to_subnormal_scales(kernel, exp):
         tiny = max(lens) * 127 * 2.0 ** -34 * 2.0 ** -120 + 2.0 ** -150
         err = (y.double() - o).abs()[:t]
         assert bool((err <= (bound + (2.0 ** -24 + 2.0 ** -14) * o.abs())[:t] + tiny).all()), float((err / o.abs()[:t]).max())
+
+
+# -------------------------------------------------- inputs that are not finite
+
+BAD = [float("nan"), -float("nan"), float("inf"), -float("inf")]
+
+
+@pytest.mark.parametrize("M,N,K", [(3, 40, 512), (5, 40, 4096), (9, 8200, 1024), (4, 40, 40000), (40, 40, 8192), (2, 20, 20000)])
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_a_token_that_is_not_finite_gives_nan(M, N, K, dtype):
+    """A NaN or an infinity in a token, beside its largest finite values: the token's
+    outputs are NaN, the other tokens' are as without it."""
+    import torch
+    o = ops()
+    g = torch.Generator(device="cuda").manual_seed(60)
+    x = torch.randn(M, K, generator=g, device="cuda").to(getattr(torch, dtype))
+    wq, ws = o.w8a8_pack_weight(torch.randn(N, K, generator=g, device="cuda").half())
+    clean, s0 = o.w8a8_linear(x, wq, ws), o.w8a8_quantize_act(x)[1]
+    for i, bad in enumerate(BAD):
+        for at in (0, 5, K // 2 + 3, K - 1):
+            z = x.clone()
+            row = (at + i) % M
+            z[row, at // 16 * 16:at // 16 * 16 + 16] = 1000.0
+            z[row, at] = bad
+            keep = torch.arange(M, device="cuda") != row
+            q, s = o.w8a8_quantize_act(z)
+            assert bool(torch.isnan(s[row])) and torch.equal(s[keep], s0[keep])
+            for y in (o.w8a8_linear(z, wq, ws), o.w8a8_gemm(q, s, wq, ws)):
+                assert bool(torch.isnan(y[row]).all()) and torch.equal(y[keep], clean[keep])
+
+
+@pytest.mark.parametrize("bad", BAD)
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_a_page_that_is_not_finite_says_so(bad, dtype):
+    """The scale of the page and head that a NaN or an infinity is stored in becomes
+    NaN, and stays so while the page is filled; the others are as without it; the
+    page starts afresh when it is used again. Queries that see it get NaN."""
+    import torch
+    o = ops()
+    B = Batch([20, 3], [37, 40], 2, 64, 16, dtype, seed=61)
+    k, v = B.rand(2), B.rand(2)
+    kc, vc, ks, vs = (x.clone() for x in B.pool[:4])
+    o.kv8_append(k, v, kc, vc, ks, vs, *B.pool[4:], B.max_new)
+    bk, bv = k.clone(), v.clone()
+    bk[4, 1, 7], bv[15, 0, 60] = bad, bad                # positions 21 and 32 of sequence 0: pages 1 and 2
+    pk, pv = int(B.table_host[0, 1]), int(B.table_host[0, 2])
+    o.kv8_append(bk, bv, *B.pool, B.max_new)
+    assert bool(torch.isnan(B.ks[pk, 1])) and bool(torch.isnan(B.vs[pv, 0]))
+    for a, b, at in ((B.ks, ks, (pk, 1)), (B.vs, vs, (pv, 0)), (B.kc, kc, (pk, 1)), (B.vc, vc, (pv, 0))):
+        a, b = a.clone(), b.clone()
+        a[at], b[at] = 0, 0
+        assert torch.equal(torch.nan_to_num(a.float()), torch.nan_to_num(b.float()))
+    last = torch.tensor([0, 1, 2], dtype=torch.int32, device="cuda")
+    for heads, cu, n in ((4, B.cu, 20), (16, B.cu, 20), (4, last, 1)):    # 40, 160 and 2 query rows per kv head
+        q, g = B.rand(heads), heads // 2
+        y, lse = o.kv8_attention(q, *B.pool[:5], cu, B.sl, n, B.max_len, causal=False, return_lse=True)
+        clean, clean_lse = o.kv8_attention(q, kc, vc, ks, vs, B.table, cu, B.sl, n, B.max_len, causal=False, return_lse=True)
+        assert bool(torch.isnan(y[:n]).all()), "values of its first kv head, keys of its second"
+        assert torch.equal(lse[:n, :g], clean_lse[:n, :g]) and bool(torch.isnan(lse[:n, g:]).all())
+        rest = slice(n, int(cu[2]))
+        assert torch.equal(y[rest], clean[rest]) and torch.equal(lse[rest], clean_lse[rest])
+    # 3 more tokens on the page: its scale still says so
+    B.sl = torch.tensor([40, 40], dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 3, 3], dtype=torch.int32, device="cuda")
+    o.kv8_append(k, v, *B.pool[:5], cu, B.sl, 3)
+    assert bool(torch.isnan(B.vs[pv, 0]))
+    # used again from its first position
+    sl = torch.tensor([2, 0], dtype=torch.int32, device="cuda")
+    table = B.table.clone()
+    table[0, 0] = pv
+    o.kv8_append(k, v, *B.pool[:4], table, torch.tensor([0, 2, 2], dtype=torch.int32, device="cuda"), sl, 2)
+    assert bool(torch.isfinite(B.vs[pv]).all()) and bool(torch.isfinite(B.ks[pv]).all())

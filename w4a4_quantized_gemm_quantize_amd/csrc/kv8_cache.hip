@@ -110,12 +110,12 @@ __global__ __launch_bounds__(kThreads) void k_kv8_append(KvPool c, KvBatch b, Kv
   for (int n = 0; n < NPT; ++n) m = absmax16(raw[n], m);
   float* sp = (is_v ? c.vs : c.ks) + (int64_t)pg * c.heads + h;
   const float s_old = w.lo > 0 ? *sp : 0.0f;
-  float a = group_max<64>(absmax_value<BF>(m));
+  float a = wave_absmax<BF>(m);
   if ((tid & 63) == 0) wave_max[tid >> 6] = a;
   __syncthreads();                                  // also: every thread has read *sp
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) a = fmaxf(a, wave_max[i]);
-  const float sc = fmaxf(s_old, a / 127.0f);
+  for (int i = 0; i < kThreads / 64; ++i) a = max_or_nan(a, wave_max[i]);
+  const float sc = max_or_nan(s_old, a / 127.0f);
   const bool grown = w.lo > 0 && sc > s_old;
   const float r = grown ? s_old / sc : 1.0f;
   const float k = scale_guard(sc), sk = sc * k, rs = sc == 0.0f ? 0.0f : 1.0f / sk;

@@ -1,5 +1,6 @@
 // Device helpers of the INT8 quantizers (w8a8_quantize_act, kv8_append): the rule
-// is a = max|x|, s = fl32(a / 127), q = rne(fl32(x / s)).
+// is a = max|x|, s = fl32(a / 127), q = rne(fl32(x / s)); s is NaN where a value
+// of the row is a NaN or an infinity.
 #pragma once
 
 #include "quant_common.h"
@@ -55,12 +56,30 @@ __device__ __forceinline__ uint4 codes16(const uint4 r[2], float k, float s, flo
   return uint4{o[0], o[1], o[2], o[3]};
 }
 
-// The value of an absmax16 result, and the factor k that codes16 needs for s.
-template <bool BF>
-__device__ __forceinline__ float absmax_value(uint32_t m) {
-  const uint32_t mm = max(m & 0xFFFFu, m >> 16);
-  return BF ? __uint_as_float(mm << 16) : (float)__builtin_bit_cast(_Float16, (uint16_t)mm);
+// The largest of the wave's absmax16 results, NaN if it is not finite. All of it on
+// the bits, which order NaN above infinity above the numbers (a maximum of floats
+// drops a NaN and what its lane had found beside it). Every lane must be active.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_max(uint32_t m) {
+  return max(m, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)m, CTRL, 0xF, 0xF, false));
 }
+template <bool BF>
+__device__ __forceinline__ float wave_absmax(uint32_t m) {
+  m = max(m & 0xFFFFu, m >> 16);
+  m = dpp_max<DPP_HALF_MIRROR>(m);
+  m = dpp_max<DPP_QUAD_1032>(m);
+  m = dpp_max<DPP_QUAD_2301>(m);
+  m = dpp_max<DPP_ROW_MIRROR>(m);
+  m = max(m, (uint32_t)__shfl_xor((int)m, 16));
+  m = max(m, (uint32_t)__shfl_xor((int)m, 32));
+  if constexpr (BF) return __uint_as_float((m >= 0x7F80u ? 0x7FC0u : m) << 16);
+  return (float)__builtin_bit_cast(_Float16, (uint16_t)(m >= 0x7C00u ? 0x7E00u : m));
+}
+// Maximum of two such values, and of scales: none below 0, NaN stays.
+__device__ __forceinline__ float max_or_nan(float a, float b) {
+  return __uint_as_float(max(__float_as_uint(a), __float_as_uint(b)));
+}
+// The factor k that codes16 needs for s.
 __device__ __forceinline__ float scale_guard(float s) { return s < 0x1p-60f ? 0x1p80f : 1.0f; }
 
 }  // namespace w4a4

@@ -3,6 +3,7 @@
 // cores.
 //
 //   a = max_k |x|, s = fl32(a / 127), q = rne(fl32(x / s)) in [-127, 127]
+//   (s = NaN, and with it the row of Y, if an x is a NaN or an infinity)
 //   P[m,n] = sum_k xq[m,k] wq[n,k]            (int32, exact for K <= 131056)
 //   Y[m,n] = fl32(fl32(fl32(P) fl32(xs[m] ws[n])) + bias[n])
 //
@@ -32,7 +33,7 @@ template <bool BF, int WPR, int NC>
 __global__ __launch_bounds__(kThreads) void k_w8a8_quant(const uint16_t* __restrict__ x, int64_t ldx, int64_t M, int K,
                                                          int8_t* __restrict__ q, float* __restrict__ s) {
   constexpr int RPB = kThreads / 64 / WPR;
-  __shared__ uint32_t wave_max[kThreads / 64];
+  __shared__ float wave_max[kThreads / 64];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int64_t row = (int64_t)blockIdx.x * RPB + wave / WPR;
   const bool live = row < M;                       // WPR > 1 has one row per block: uniform
@@ -59,12 +60,12 @@ __global__ __launch_bounds__(kThreads) void k_w8a8_quant(const uint16_t* __restr
       m = absmax16(r, m);
     }
   }
-  float a = group_max<64>(absmax_value<BF>(m));
+  float a = wave_absmax<BF>(m);
   if constexpr (WPR > 1) {
-    if (lane == 0) wave_max[wave] = __float_as_uint(a);
+    if (lane == 0) wave_max[wave] = a;
     __syncthreads();
 #pragma unroll
-    for (int w = 0; w < WPR; ++w) a = fmaxf(a, __uint_as_float(wave_max[w]));
+    for (int w = 0; w < WPR; ++w) a = max_or_nan(a, wave_max[w]);
   }
   if (!live) return;
   const float sc = a / 127.0f;                     // correctly rounded
@@ -200,8 +201,8 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
     __syncthreads();                                     // row_max is cleared
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
-      const float a = group_max<64>(k[i] < p.K ? absmax_value<BF>(absmax16(raw[i], 0)) : 0.0f);
-      if (lane == 0) atomicMax(&row_max[row[i]], __float_as_uint(a));   // of values >= 0: their bits order alike
+      const float a = wave_absmax<BF>(k[i] < p.K ? absmax16(raw[i], 0) : 0);
+      if (lane == 0) atomicMax(&row_max[row[i]], __float_as_uint(a));   // as max_or_nan
     }
     __syncthreads();
 #pragma unroll
