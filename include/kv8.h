@@ -48,6 +48,10 @@ extern "C" {
  *   s = max(s_old, fl32(max|new| / 127))
  *   earlier codes, if s > s_old:  q <- rne(fl32(q * fl32(s_old / s)))
  *   new codes:                    rne(fl32(x / s))  (s = 0: 0)
+ * Each growth of a page's scale rounds its older codes again, by half a step at
+ * most: after g growths a value is within (g + 1) / 2 steps s of what was stored (its
+ * steps never shrink), so a page whose maximum rises with every token may be off by
+ * page / 2 steps at its first tokens; one whose largest values come first, by 1/2.
  * Other slots keep their bytes. The pages written must not be shared. A NaN or an
  * infinity among the new values makes s NaN (the codes of the new tokens are then
  * any), until the page is used afresh.
@@ -92,8 +96,10 @@ w4a4_status_t kv8_gather(const int8_t* k_cache, const int8_t* v_cache, const flo
  *           16-byte aligned, overwritten; may be NULL when that size is 0
  * Codes enter the matrix products exactly; softmax statistics and sums are
  * fp32. A weight (softmax numerator times its page's value scale) is rounded to
- * 11 bits, or, where it is under 2^-23 of the largest such, to 2^-34 of the
- * largest page scale (2^-120, where all are smaller); bf16 queries lose elements
+ * 11 bits, or, where it is under 2^-29 of the largest such, to 2^-40 of the
+ * largest page scale (2^-120, where all are smaller); with more than 128 query
+ * rows per kv head (64, where the short contexts of 256 and more pairs of sequence
+ * and kv head fill the GPU, or dim > 128) 2^-23 and 2^-34; bf16 queries lose elements
  * under 2^-39 of a row's largest. Scales are finite and >= 0; scores may take any
  * size that fp32 holds. A page whose key or value scale is NaN gives NaN to every
  * query that sees one of its positions, and may to others of its sequence.

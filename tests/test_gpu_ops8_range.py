@@ -119,6 +119,31 @@ def test_rescaled_codes_round_their_product_first(top, dtype):
     check_append(B, k, v)
 
 
+def test_a_page_filled_token_by_token_stays_within_its_bound():
+    """A value stored and then rescaled g times is off by at most half a step of the
+    scale at each of the g + 1 roundings (steps never shrink): (g + 1) / 2 steps
+    of the last one. The quotients and products round to fp32 before: up to 127
+    units times 2 roundings of 2^-24 each."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(55)
+    page, dim = 32, 64
+    pool = ops().kv8_new_cache(1, 1, page, dim)
+    table = torch.zeros((1, 1), dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 1], dtype=torch.int32, device="cuda")
+    x = torch.randn(2, page, 1, dim, generator=g, device="cuda").clamp(-3, 3)
+    x[:, :, 0, 7] = 3.0 + 0.02 * torch.arange(page, device="cuda")     # the maximum rises with every token
+    x = x.half()
+    for i in range(page):
+        sl = torch.tensor([i + 1], dtype=torch.int32, device="cuda")
+        ops().kv8_append(x[0, i:i + 1], x[1, i:i + 1], *pool, table, cu, sl, 1)
+    every = torch.tensor([0, page], dtype=torch.int32, device="cuda")
+    got = ops().kv8_gather(*pool, table, every, sl, page, page, out_dtype=torch.float32)
+    roundings = page - torch.arange(page, device="cuda").double()
+    for side, back, scale in zip(x, got, pool[2:]):
+        off = (side.double() - back.double()).abs().amax(dim=(1, 2)) / scale[0, 0].double()
+        assert bool((off <= roundings * (0.5 + 127 * 2 * 2.0 ** -24)).all())
+
+
 @pytest.mark.parametrize("M,N,K", [(1, 130, 256), (7, 8200, 1024), (12, 300, 4112), (33, 100, 4096), (64, 130, 8192),
                                    (130, 256, 512), (300, 520, 1024), (2048, 512, 256)])
 def test_bias_is_added_to_the_rounded_product(M, N, K):
@@ -301,3 +326,26 @@ def test_a_page_that_is_not_finite_says_so(bad, dtype):
     table[0, 0] = pv
     o.kv8_append(k, v, *B.pool[:4], table, torch.tensor([0, 2, 2], dtype=torch.int32, device="cuda"), sl, 2)
     assert bool(torch.isfinite(B.vs[pv]).all()) and bool(torch.isfinite(B.ks[pv]).all())
+
+
+# --------------------------------------------------------- small weights
+
+@pytest.mark.parametrize("new,lens,heads", [([1, 3], [300, 900], 8), ([9, 5], [300, 517], 8), ([30, 8], [400, 100], 8),
+                                            ([1], [5000], 16), ([7, 2], [900, 90], 4)])
+@pytest.mark.parametrize("dim,page", [(64, 16), (128, 64)])
+def test_small_weights_of_few_rows(new, lens, heads, dim, page):
+    """Up to 128 rows per kv head a weight in fp16's subnormal range is off by half
+    its step, 2^-25, relative to 2^15 for the largest page scale: 2^-40 of it
+    (many rows: 2^-34)."""
+    import torch
+    B = Batch(new, lens, 2, dim, page, seed=62)
+    B.vs[::2] *= 2.0 ** -16                               # pages whose values are small beside the largest
+    q = B.rand(heads, 6.0)
+    o, _, bound = attention_ref(B, q, True, 0, dim ** -0.5)
+    t = B.cu_host[-1]
+    for b in range(len(lens)):
+        pages = B.table[b, :-(-lens[b] // page)].long()
+        top = max(float(torch.nan_to_num(B.vs[pages]).max()), 0.0)
+        bound[B.cu_host[b]:B.cu_host[b + 1]] -= lens[b] * 127 * (2.0 ** -34 - 2.0 ** -40) * top
+    y, _ = attend(B, q, out_dtype=torch.float32)
+    assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -24 * o.abs())[:t]).all())
