@@ -87,6 +87,12 @@ w4a4_status_t kv8_gather(const int8_t* k_cache, const int8_t* v_cache, const flo
  * and o = 0, lse = -inf where it sees none. Query head h reads kv head
  * h / (q_heads / heads).
  *
+ * One kernel, chosen by max_new, serves all sequences of a call. Sequences with a
+ * single new token run several times faster in a call of their own than beside long
+ * chunks: put them first or last, and give each call its part of block_table,
+ * cu_seqlens (which need not start at 0) and seq_lens. Rows of y that belong to no
+ * sequence are left alone, so both may fill one y.
+ *
  *   q       [T][q_heads] rows of dim elements at strides q_tok, q_head
  *           (elements, multiples of 8), 16-byte aligned, x_dtype W4A4_Y_F16 or
  *           W4A4_Y_BF16; q_heads a multiple of heads

@@ -349,3 +349,21 @@ def test_small_weights_of_few_rows(new, lens, heads, dim, page):
         bound[B.cu_host[b]:B.cu_host[b + 1]] -= lens[b] * 127 * (2.0 ** -34 - 2.0 ** -40) * top
     y, _ = attend(B, q, out_dtype=torch.float32)
     assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -24 * o.abs())[:t]).all())
+
+
+@pytest.mark.parametrize("single", [5, 1])
+def test_single_tokens_and_chunks_in_two_calls(single):
+    """A mixed batch in one call, and its single tokens and chunks each in a call of
+    their own that fills its rows of one output."""
+    import torch
+    B = Batch([1] * single + [90, 40], [300 + 7 * i for i in range(single)] + [200, 40], 2, 128, 64, seed=63)
+    q = B.rand(8)
+    o, _, bound = attention_ref(B, q, True, 0, 128 ** -0.5)
+    t = B.cu_host[-1]
+    out = torch.full_like(q, 7.0)
+    for part, new in ((slice(0, single), 1), (slice(single, None), 90)):
+        cu = B.cu[:single + 1] if new == 1 else B.cu[single:]
+        ops().kv8_attention(q, *B.pool[:4], B.table[part], cu, B.sl[part], new, B.max_len, out=out)
+    for y in (out, ops().kv8_attention(q, *B.pool, B.max_new, B.max_len)):
+        assert bool(((y.double() - o).abs()[:t] <= (bound + 2.0 ** -11 * (o.abs() + bound) + 2.0 ** -25)[:t]).all())
+    assert bool((out[t:] == 7).all())

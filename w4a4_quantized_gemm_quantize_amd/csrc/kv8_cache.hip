@@ -15,8 +15,8 @@
 // in registers between the maximum and the codes; V's codes go through LDS in
 // position order and leave transposed, 16 positions of a dimension per store.
 // Both directions are bound by HBM, 3 bytes per value stored, 3 read back: 24
-// ragged prompts of up to 1500 tokens, 8 heads of 128 (91 MB each way) take 24.8
-// and 19.9 us, 3.7 and 4.6 TB/s. A decode step's few tokens are bound by the
+// ragged prompts of up to 1500 tokens, 8 heads of 128 (91 MB each way) take 24.2
+// and 20.1 us, 3.8 and 4.5 TB/s. A decode step's few tokens are bound by the
 // chain of loads (lengths, table, scale, codes): 64 tokens 9 and 8 us.
 #include <algorithm>
 

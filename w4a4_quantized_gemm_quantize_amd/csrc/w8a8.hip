@@ -642,9 +642,8 @@ void launch_tiles(W8Params p, int splits, hipStream_t stream) {
 // Above 16 tokens, the tile whose estimated time is least: rounds of tiles over
 // the CUs times (stages x the tile's time per 128-k stage + its start and
 // output). The times (us: 256 x 256 tiles 1.15 a stage, 256 x 128 0.8, 128 x 128
-// 0.5) are fitted so that the choice is within 3 % of the fastest over 20 shapes
-// from 32 x 4096 x 4096 to 4096 x 8192 x 28672, tokens x channels x K; us of the
-// three in turn: 4096 x 4096 x 4096 62.6, 70.7, 80.9; 1024 x 8192 x 28672 229, 224,
+// 0.5) are fitted to measured shapes, tokens x channels x K, among them those named
+// here, where the choice is the fastest; us of the three in turn: 4096 x 4096 x 4096 62.6, 70.7, 80.9; 1024 x 8192 x 28672 229, 224,
 // 290; 512 x 8192 x 8192 74, 55.2, 43.4. 128 x 128 tiles may also split K, which
 // costs a launch and 8 bytes per output and range through the caches (64 x 8192
 // x 8192: 35.6 us whole, 25.5 in two ranges, 21.2 in four; 512 x 4096 x 11008:

@@ -559,7 +559,8 @@ def _w8_quantize(x, out, names):
 
 def w8a8_quantize_act(x: torch.Tensor, out=None):
     """Symmetric INT8 quantization per token of fp16 or bf16 X[M, K] (row stride
-    may exceed K): ``(xq int8 [M, K], xs float32 [M])``, ``x ~ xq * xs``."""
+    may exceed K): ``(xq int8 [M, K], xs float32 [M])``, ``x ~ xq * xs``; NaN scales
+    for rows that are not finite."""
     return _w8_quantize(x, out, ("x", "xq", "xs"))
 
 
@@ -730,7 +731,8 @@ def kv8_append(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens
     Sequence b's new tokens are rows ``cu_seqlens[b] .. cu_seqlens[b+1] - 1``, and
     the last positions of its ``seq_lens[b]`` (new tokens included). A page keeps
     one scale per head: it grows when a new token needs it, and the codes
-    already there are rescaled. Everything but ``max_new`` (at least the largest
+    already there are rescaled (each time off by half a step more, at most). NaN or
+    infinite values make it NaN. Everything but ``max_new`` (at least the largest
     number of new tokens of a sequence) is read on the device."""
     ptrs, (pages, heads, page, dim), batch, B = _kv_pool(k_cache, v_cache, k_scale, v_scale, block_table,
                                                          cu_seqlens, seq_lens)
@@ -782,7 +784,9 @@ def kv8_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens
     device). ``scale`` defaults to dim ** -0.5; ``window`` w > 0 hides the keys w
     and more positions back. Returns [T, q_heads, dim] of ``out_dtype`` (default:
     q's), with ``return_lse`` also float32 [T, q_heads] (natural log). A query that
-    sees no key gives zeros and -inf; rows of no sequence are left alone. The
+    sees no key gives zeros and -inf; rows of no sequence are left alone. One
+    kernel, chosen by ``max_new``, serves the call: many single tokens beside a long
+    chunk are faster in a call of their own with the same ``out``. The
     workspace is allocated here with torch unless given."""
     ptrs, (pages, heads, page, dim), batch, B = _kv_pool(k_cache, v_cache, k_scale, v_scale, block_table,
                                                          cu_seqlens, seq_lens)
