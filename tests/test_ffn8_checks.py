@@ -1,0 +1,135 @@
+"""Argument validation of what surrounds the W8A8 products (CPU only): statuses of the
+C ABI, which returns before any HIP call, and the tensor wrappers' refusals."""
+import pytest
+import torch
+
+from w4a4_quantized_gemm_quantize_amd import _lib, ops
+
+OK, E_NULL, E_SHAPE, E_ALIGN, E_DTYPE = 0, 1, 2, 4, 5
+F32, F16, BF16 = 0, 1, 2
+P = 0x10000          # a fake, aligned "device pointer"
+
+
+def test_rmsnorm_validation():
+    def f(x=P, dt=F16, ldx=64, r=None, ldr=0, w=P, wdt=F32, eps=1e-6, M=4, K=64, q=P, s=P, h=None, ldh=0, y=None, ldy=0):
+        return _lib.status_of("w8a8_rmsnorm_quantize", x, dt, ldx, r, ldr, w, wdt, eps, M, K, q, s, h, ldh, y, ldy, None)
+    assert f(dt=F32) == E_DTYPE and f(wdt=BF16) == E_DTYPE and f(dt=BF16, wdt=F16) == E_DTYPE
+    assert f(M=-1) == E_SHAPE and f(M=1 << 24) == E_SHAPE and f(K=0) == E_SHAPE and f(K=72, ldx=72) == E_SHAPE
+    assert f(ldx=56) == E_SHAPE and f(ldx=68) == E_ALIGN
+    for eps in (0.0, -1.0, float("nan"), float("inf")):
+        assert f(eps=eps) == E_SHAPE
+    res = dict(r=P, ldr=64, h=P, ldh=64)
+    assert f(**dict(res, ldr=56)) == E_SHAPE and f(**dict(res, ldh=56)) == E_SHAPE
+    assert f(**dict(res, ldr=68)) == E_ALIGN and f(**dict(res, ldh=68)) == E_ALIGN
+    assert f(**dict(res, h=None)) == E_NULL and f(**dict(res, h=P + 8)) == E_ALIGN and f(**dict(res, r=P + 2)) == E_ALIGN
+    assert f(y=P, ldy=56) == E_SHAPE and f(y=P, ldy=68) == E_ALIGN and f(y=P + 2, ldy=64) == E_ALIGN
+    assert f(x=None) == E_NULL and f(w=None) == E_NULL and f(q=None) == E_NULL and f(s=None) == E_NULL
+    assert f(x=P + 8) == E_ALIGN and f(w=P + 4) == E_ALIGN and f(q=P + 8) == E_ALIGN and f(s=P + 2) == E_ALIGN
+    assert f(x=None, w=None, q=None, s=None, M=0) == OK
+
+
+def gemm_act(xq=P, xs=P, wq=P, ws=P, bias=None, act=0, gated=0, res=None, ldr=0, M=32, N=8, K=64, wsp=P, wb=1 << 30, y=P,
+             dt=F16, ldy=8):
+    return _lib.status_of("w8a8_gemm_act", xq, xs, wq, ws, bias, act, gated, res, ldr, M, N, K, wsp, wb, y, dt, ldy, None)
+
+
+def linear_act(x=P, xdt=F16, M=32, K=64, ldx=64, wq=P, ws=P, bias=None, act=0, gated=0, res=None, ldr=0, N=8, wsp=P,
+               wb=1 << 30, y=P, dt=F16, ldy=8):
+    return _lib.status_of("w8a8_linear_act", x, xdt, M, K, ldx, wq, ws, bias, act, gated, res, ldr, N, wsp, wb, y, dt, ldy,
+                          None)
+
+
+def test_act_validation():
+    for f in (gemm_act, linear_act):
+        assert f(K=72) == E_SHAPE and f(K=131072) == E_SHAPE and f(M=-1) == E_SHAPE and f(N=-1) == E_SHAPE
+        assert f(M=1 << 24) == E_SHAPE and f(N=1 << 24, ldy=1 << 24) == E_SHAPE
+        assert f(N=1 << 23, ldy=1 << 23, gated=1) == E_SHAPE             # 2^24 channels
+        assert f(act=5) == E_SHAPE and f(act=-1) == E_SHAPE
+        assert f(dt=F32) == E_DTYPE and f(dt=9) == E_DTYPE
+        assert f(ldy=7) == E_SHAPE and f(res=P, ldr=7) == E_SHAPE
+        assert f(wq=None) == E_NULL and f(ws=None) == E_NULL and f(y=None) == E_NULL
+        assert f(wq=P + 8) == E_ALIGN and f(bias=P + 2) == E_ALIGN and f(y=P + 1) == E_ALIGN
+        assert f(res=P + 1, ldr=8) == E_ALIGN and f(wsp=P + 8) == E_ALIGN
+        assert f(M=0) == OK and f(N=0) == OK
+    assert gemm_act(xq=None) == E_NULL and gemm_act(xs=None) == E_NULL and gemm_act(xq=P + 8) == E_ALIGN
+    assert linear_act(x=None) == E_NULL and linear_act(xdt=F32) == E_DTYPE and linear_act(ldx=68) == E_ALIGN
+    assert linear_act(ldx=56) == E_SHAPE and linear_act(x=P + 8) == E_ALIGN
+
+
+def test_act_workspace():
+    gemm, lin = _lib.load_library().w8a8_gemm_act_workspace, _lib.load_library().w8a8_linear_act_workspace
+    assert gemm(4, 8, 72, 0, 1) == -1 and lin(4, 8, 72, 0, 1) == -1 and gemm(0, 8, 64, 0, 1) == 0
+    assert gemm(300, 1000, 336, 0, 1) == 0                               # tiles write the outputs
+    assert gemm(300, 1000, 336, 0, 0) == 300 * 1000 * 4                  # other rows: int32 sums first
+    assert gemm(300, 1001, 336, 0, 1) == 300 * 1001 * 4
+    assert gemm(300, 1001, 336, 1, 1) == 300 * 2002 * 4
+    for M, N, K in [(64, 8192, 8192), (4096, 4096, 4096), (17, 100, 1040), (512, 4096, 11008)]:
+        for gated in (0, 1):
+            assert gemm(M, N, K, gated, 0) >= gemm(M, N, K, gated, 1)
+            assert lin(M, N, K, gated, 1) >= M * K + 4 * M + gemm(M, N, K, gated, 1)
+    assert lin(1, 4096, 4096, 1, 1) == 0                                 # one launch
+    need = gemm(64, 8192, 8192, 0, 1)
+    assert need > 0
+    big = dict(M=64, N=8192, K=8192, ldy=8192)
+    assert gemm_act(**big, wb=need - 1) == E_SHAPE and gemm_act(**big, wsp=None, wb=need) == E_NULL
+    assert linear_act(**big, ldx=8192, wb=need) == E_SHAPE
+
+
+def test_route_validation():
+    def f(x=P, dt=F32, T=4, E=64, ld=64, k=8, ids=P, w=P):
+        return _lib.status_of("moe_route", x, dt, T, E, ld, k, 1, ids, w, None)
+    assert f(dt=3) == E_DTYPE and f(T=-1) == E_SHAPE and f(T=1 << 28) == E_SHAPE
+    assert f(E=0) == E_SHAPE and f(E=513, ld=513) == E_SHAPE and f(ld=63) == E_SHAPE
+    assert f(k=0) == E_SHAPE and f(k=65) == E_SHAPE
+    assert f(x=None) == E_NULL and f(ids=None) == E_NULL and f(w=None) == E_NULL
+    assert f(x=P + 2) == E_ALIGN and f(x=P + 1, dt=F16) == E_ALIGN and f(ids=P + 2) == E_ALIGN and f(w=P + 1) == E_ALIGN
+    assert f(x=None, ids=None, w=None, T=0) == OK
+
+
+def test_moe_validation():
+    def f(xq=P, xs=P, ids=P, w=P, T=4, k=2, w13=P, s13=P, w2=P, s2=P, E=8, H=64, I=32, act=2, wsp=P, wb=1 << 30, y=P,
+          dt=F16, ldy=64):
+        return _lib.status_of("w8a8_moe", xq, xs, ids, w, T, k, w13, s13, w2, s2, E, H, I, act, wsp, wb, y, dt, ldy, None)
+    assert f(T=-1) == E_SHAPE and f(T=257) == E_SHAPE and f(k=0) == E_SHAPE and f(T=1, k=513) == E_SHAPE
+    assert f(T=1 << 62, k=8) == E_SHAPE                                  # no overflow on the way
+    assert f(E=0) == E_SHAPE and f(E=513) == E_SHAPE
+    assert f(H=72, ldy=72) == E_SHAPE and f(I=24) == E_SHAPE and f(H=131072, ldy=131072) == E_SHAPE and f(I=0) == E_SHAPE
+    assert f(act=7) == E_SHAPE and f(dt=F32) == E_DTYPE and f(ldy=63) == E_SHAPE
+    need = _lib.load_library().w8a8_moe_workspace(4, 2, 8, 64, 32)
+    assert need >= 8 * 32 * 5 and f(wb=need - 1) == E_SHAPE
+    assert _lib.load_library().w8a8_moe_workspace(4, 2, 8, 64, 24) == -1
+    assert _lib.load_library().w8a8_moe_workspace(0, 2, 8, 64, 32) == 0
+    for name in ("xq", "xs", "ids", "w", "w13", "s13", "w2", "s2", "y", "wsp"):
+        assert f(**{name: None}) == E_NULL, name
+    for name in ("xq", "w13", "w2", "wsp"):
+        assert f(**{name: P + 8}) == E_ALIGN, name
+    for name in ("xs", "ids", "w", "s13", "s2"):
+        assert f(**{name: P + 2}) == E_ALIGN, name
+    assert f(y=P + 1) == E_ALIGN
+    assert f(xq=None, T=0) == OK
+
+
+def test_wrappers_refuse_host_tensors_and_bad_names():
+    x = torch.zeros((4, 64), dtype=torch.float16)
+    q, s = x.to(torch.int8), torch.ones(4)
+    with pytest.raises(TypeError):
+        ops.w8a8_rmsnorm_quantize(x, torch.ones(64))
+    with pytest.raises(TypeError):
+        ops.w8a8_gemm_act(q, s, q, s)
+    with pytest.raises(TypeError):
+        ops.w8a8_linear_act(x, q, s)
+    with pytest.raises(TypeError):
+        ops.moe_route(x, 2)
+    with pytest.raises(TypeError):
+        ops.w8a8_moe(q, s, q.int(), x.float(), q[None], s[None], q[None], s[None])
+    for bad in ("swish", 1, True, ""):
+        with pytest.raises(ValueError):
+            ops._activation(bad)
+    with pytest.raises(ValueError):
+        ops.w8a8_pack_gated(x, x[:2])
+
+
+def test_public_names():
+    import w4a4_quantized_gemm_quantize_amd as pkg
+    for name in ("w8a8_rmsnorm_quantize", "w8a8_gemm_act", "w8a8_linear_act", "w8a8_pack_gated", "moe_route", "w8a8_moe"):
+        assert getattr(pkg, name) is getattr(ops, name)

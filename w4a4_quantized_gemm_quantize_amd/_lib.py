@@ -30,7 +30,10 @@ _f32 = ctypes.c_float
 # the pool and batch arguments that the kv8 calls share
 _KV_BATCH = [_i64, _i32, _i32, _i32, _p, _i64, _p, _p, _i64, _i64, _i64, _i64]
 
-# name -> argtypes, mirroring include/w4a4.h and include/kv8.h
+# the weight side and the epilogue that the products with one share
+_ACT = [_p, _p, _p, _i32, _i32, _p, _i64]
+
+# name -> argtypes, mirroring include/w4a4.h, include/ffn8.h and include/kv8.h
 SIGNATURES = {
     "w4a4_quantize_act": [_p, _i64, _i64, _i64, _i32, _p, _p, _p],
     "w4a4_pack_weight": [_p, _i64, _i64, _i32, _p, _p, _p],
@@ -69,6 +72,11 @@ SIGNATURES = {
     "w8a8_pack_weight": [_p, _i32, _i64, _i64, _p, _p, _p],
     "w8a8_linear": [_p, _i32, _i64, _i64, _i64, _p, _p, _p, _i64, _p, _i64, _p, _i32, _i64, _p],
     "w8a8_gemm": [_p, _p, _p, _p, _p, _i64, _i64, _i64, _p, _i64, _p, _i32, _i64, _p],
+    "w8a8_rmsnorm_quantize": [_p, _i32, _i64, _p, _i64, _p, _i32, _f32, _i64, _i64, _p, _p, _p, _i64, _p, _i64, _p],
+    "w8a8_gemm_act": [_p, _p, *_ACT, _i64, _i64, _i64, _p, _i64, _p, _i32, _i64, _p],
+    "w8a8_linear_act": [_p, _i32, _i64, _i64, _i64, *_ACT, _i64, _p, _i64, _p, _i32, _i64, _p],
+    "moe_route": [_p, _i32, _i64, _i64, _i64, _i64, _i32, _p, _p, _p],
+    "w8a8_moe": [_p, _p, _p, _p, _i64, _i64, _p, _p, _p, _p, _i64, _i64, _i64, _i32, _p, _i64, _p, _i32, _i64, _p],
     "kv8_append": [_p, _p, _i32, _i64, _i64, _i64, _i64, _p, _p, _p, _p, *_KV_BATCH, _p],
     "kv8_gather": [_p, _p, _p, _p, *_KV_BATCH, _p, _p, _i32, _p],
     "kv8_attention": [_p, _i32, _i64, _i64, _i32, _p, _p, _p, _p, *_KV_BATCH, _f32, _i32, _i64, _p, _i64,
@@ -117,6 +125,11 @@ def load_library() -> ctypes.CDLL:
         for name in ("w8a8_gemm_workspace", "w8a8_linear_workspace"):
             getattr(lib, name).argtypes = [_i64, _i64, _i64]
             getattr(lib, name).restype = ctypes.c_int64
+        for name in ("w8a8_gemm_act_workspace", "w8a8_linear_act_workspace"):
+            getattr(lib, name).argtypes = [_i64, _i64, _i64, _i32, _i32]
+            getattr(lib, name).restype = ctypes.c_int64
+        lib.w8a8_moe_workspace.argtypes = [_i64, _i64, _i64, _i64, _i64]
+        lib.w8a8_moe_workspace.restype = ctypes.c_int64
         lib.kv8_attention_workspace.argtypes = [_i32, _i32, _i32, _i32, _i64, _i64, _i64, _i64, _i32, _i64]
         lib.kv8_attention_workspace.restype = ctypes.c_int64
         _lib = lib

@@ -1,8 +1,11 @@
-// C ABI of the 8-bit operators (w8a8_*, include/w4a4.h; kv8_*, include/kv8.h):
+// C ABI of the 8-bit operators (w8a8_*, include/w4a4.h; the rest of a feed-forward
+// block, include/ffn8.h; kv8_*, include/kv8.h):
 // argument validation, then the launches of one call.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "act8.h"
+#include "ffn8.h"
 #include "kv8.h"
 #include "launch.h"
 #include "w4a4.h"
@@ -280,6 +283,176 @@ w4a4_status_t kv8_attention(const void* q, int32_t x_dtype, int64_t q_tok, int64
   if (need > 0 && !aligned(workspace, 16)) return W4A4_E_ALIGN;
   if (num_pages == 0) b.max_len = 0;               // no page to read: every query sees nothing
   w4a4::launch_kv8_attention(c, b, a, workspace, as_stream(stream));
+  return launched();
+}
+
+// ---- The rest of a feed-forward block (ffn8.h)
+
+static_assert(W8A8_ACT_NONE == w4a4::ACT_NONE && W8A8_ACT_RELU == w4a4::ACT_RELU && W8A8_ACT_SILU == w4a4::ACT_SILU &&
+              W8A8_ACT_GELU == w4a4::ACT_GELU && W8A8_ACT_GELU_TANH == w4a4::ACT_GELU_TANH, "activation codes");
+static bool act_ok(int32_t act) { return act >= W8A8_ACT_NONE && act <= W8A8_ACT_GELU_TANH; }
+
+w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx, const void* residual, int64_t ldr,
+                                    const void* weight, int32_t w_dtype, float eps, int64_t M, int64_t K,
+                                    int8_t* xq, float* xs, void* h, int64_t ldh, void* y, int64_t ldy, void* stream) {
+  if (!x_dtype_ok(x_dtype) || (w_dtype != W4A4_Y_F32 && w_dtype != x_dtype)) return W4A4_E_DTYPE;
+  if (M < 0 || M >= kMaxW8Rows || K <= 0 || K % 16 || K > (int64_t{1} << 30) || ldx < K) return W4A4_E_SHAPE;
+  if ((residual && (ldr < K || ldh < K)) || (y && ldy < K)) return W4A4_E_SHAPE;
+  if (!(eps > 0.0f) || !(eps < __builtin_inff())) return W4A4_E_SHAPE;
+  if (ldx % 8 || (residual && (ldr % 8 || ldh % 8)) || (y && ldy % 8)) return W4A4_E_ALIGN;
+  if (M == 0) return W4A4_OK;
+  if (!x || !weight || !xq || !xs || (residual && !h)) return W4A4_E_NULL;
+  if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(xq, 16) || !aligned(xs, 4) ||
+      (residual && !aligned(h, 16)) || !aligned(y, 16))
+    return W4A4_E_ALIGN;
+  w4a4::W8NormArgs a = {};
+  a.x = x; a.residual = residual; a.weight = weight; a.h = h; a.y = y; a.q = xq; a.s = xs;
+  a.ldx = ldx; a.ldr = ldr; a.ldh = ldh; a.ldy = ldy; a.M = M; a.K = K;
+  a.eps = eps;
+  a.bf16 = x_dtype == W4A4_Y_BF16;
+  a.weight_f32 = w_dtype == W4A4_Y_F32;
+  w4a4::launch_w8a8_rmsnorm(a, as_stream(stream));
+  return launched();
+}
+
+// Channels of W for N outputs, and the extents of such a product.
+static int64_t act_channels(int64_t N, int32_t gated) { return gated ? 2 * N : N; }
+static bool act_extents_ok(int64_t M, int64_t N, int64_t K, int32_t gated) {
+  return N >= 0 && N < kMaxW8Rows && w8_extents_ok(M, act_channels(N, gated), K);
+}
+
+int64_t w8a8_gemm_act_workspace(int64_t M, int64_t N, int64_t K, int32_t gated, int32_t wide) {
+  if (!act_extents_ok(M, N, K, gated)) return -1;
+  if (M == 0 || N == 0) return 0;
+  return w4a4::w8a8_act_workspace(M, act_channels(N, gated), K, wide && N % 8 == 0);
+}
+
+int64_t w8a8_linear_act_workspace(int64_t M, int64_t N, int64_t K, int32_t gated, int32_t wide) {
+  const int64_t gemm = w8a8_gemm_act_workspace(M, N, K, gated, wide);
+  if (gemm < 0) return -1;
+  if (M == 0 || N == 0 || w4a4::w8a8_one_launch(M, act_channels(N, gated), K)) return 0;
+  return align256(M * K) + align256(4 * M) + gemm;
+}
+
+// The checks and the descriptions that the two calls share.
+static w4a4_status_t act_call(const int8_t* wq, const float* ws, const float* bias, int32_t act, int32_t gated,
+                              const void* residual, int64_t ldr, int64_t M, int64_t N, int64_t K, const void* workspace,
+                              void* y, int32_t y_dtype, int64_t ldy, w4a4::W8GemmArgs& g, w4a4::W8Epilogue& e) {
+  if (!wq || !ws || !y) return W4A4_E_NULL;
+  if (!aligned(wq, 16) || !aligned(ws, 4) || !aligned(bias, 4) || !aligned(y, 2) || !aligned(residual, 2) ||
+      !aligned(workspace, 16))
+    return W4A4_E_ALIGN;
+  g = w4a4::W8GemmArgs{};
+  g.w = wq; g.sw = ws; g.bias = bias;
+  g.M = M; g.N = act_channels(N, gated); g.K = K;
+  g.y = y; g.ydtype = y_dtype; g.ldy = ldy;
+  e.act = act;
+  e.gated = gated != 0;
+  e.residual = residual;
+  e.ldr = ldr;
+  e.wide = w4a4::w8a8_wide_rows(N, y, ldy, residual, ldr);
+  return W4A4_OK;
+}
+
+w4a4_status_t w8a8_gemm_act(const int8_t* xq, const float* xs, const int8_t* wq, const float* ws, const float* bias,
+                            int32_t act, int32_t gated, const void* residual, int64_t ldr,
+                            int64_t M, int64_t N, int64_t K, void* workspace, int64_t workspace_bytes,
+                            void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+  if (!act_extents_ok(M, N, K, gated) || !act_ok(act)) return W4A4_E_SHAPE;
+  if (!x_dtype_ok(y_dtype)) return W4A4_E_DTYPE;
+  if (M == 0 || N == 0) return W4A4_OK;
+  if (ldy < N || (residual && ldr < N)) return W4A4_E_SHAPE;
+  if (!xq || !xs) return W4A4_E_NULL;
+  if (!aligned(xq, 16) || !aligned(xs, 4)) return W4A4_E_ALIGN;
+  w4a4::W8GemmArgs g;
+  w4a4::W8Epilogue e;
+  const w4a4_status_t st = act_call(wq, ws, bias, act, gated, residual, ldr, M, N, K, workspace, y, y_dtype, ldy, g, e);
+  if (st != W4A4_OK) return st;
+  const int64_t need = w8a8_gemm_act_workspace(M, N, K, gated, e.wide);
+  if (workspace_bytes < need) return W4A4_E_SHAPE;
+  if (need > 0 && !workspace) return W4A4_E_NULL;
+  g.a = xq; g.sa = xs;
+  g.workspace = workspace;
+  w4a4::launch_w8a8_gemm_act(g, e, as_stream(stream));
+  return launched();
+}
+
+w4a4_status_t w8a8_linear_act(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
+                              const int8_t* wq, const float* ws, const float* bias, int32_t act, int32_t gated,
+                              const void* residual, int64_t ldr, int64_t N, void* workspace, int64_t workspace_bytes,
+                              void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+  if (!act_extents_ok(M, N, K, gated) || ldx < K || !act_ok(act)) return W4A4_E_SHAPE;
+  if (!x_dtype_ok(x_dtype) || !x_dtype_ok(y_dtype)) return W4A4_E_DTYPE;
+  if (ldx % 8) return W4A4_E_ALIGN;
+  if (M == 0 || N == 0) return W4A4_OK;
+  if (ldy < N || (residual && ldr < N)) return W4A4_E_SHAPE;
+  if (!x) return W4A4_E_NULL;
+  if (!aligned(x, 16)) return W4A4_E_ALIGN;
+  w4a4::W8GemmArgs g;
+  w4a4::W8Epilogue e;
+  const w4a4_status_t st = act_call(wq, ws, bias, act, gated, residual, ldr, M, N, K, workspace, y, y_dtype, ldy, g, e);
+  if (st != W4A4_OK) return st;
+  const int64_t need = w8a8_linear_act_workspace(M, N, K, gated, e.wide);
+  if (workspace_bytes < need) return W4A4_E_SHAPE;
+  if (need > 0 && !workspace) return W4A4_E_NULL;
+  const int bf16 = x_dtype == W4A4_Y_BF16;
+  if (w4a4::w8a8_one_launch(M, g.N, K)) {
+    w4a4::launch_w8a8_small_act(g, e, x, bf16, ldx, as_stream(stream));
+    return launched();
+  }
+  int8_t* xq = static_cast<int8_t*>(workspace);
+  float* xs = reinterpret_cast<float*>(xq + align256(M * K));
+  w4a4::launch_w8a8_quant(x, bf16, M, K, ldx, xq, xs, as_stream(stream));
+  g.a = xq; g.sa = xs;
+  g.workspace = xq + align256(M * K) + align256(4 * M);
+  w4a4::launch_w8a8_gemm_act(g, e, as_stream(stream));
+  return launched();
+}
+
+w4a4_status_t moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ldl, int64_t k,
+                        int32_t renormalize, int32_t* ids, float* weights, void* stream) {
+  if (!y_dtype_ok(dtype)) return W4A4_E_DTYPE;
+  if (T < 0 || T >= kMaxTokens || E <= 0 || E > w4a4::kMoeMaxExperts || ldl < E || k <= 0 || k > w4a4::kRouteMaxK)
+    return W4A4_E_SHAPE;
+  if (T == 0) return W4A4_OK;
+  if (!logits || !ids || !weights) return W4A4_E_NULL;
+  if (!aligned(logits, dtype == W4A4_Y_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4)) return W4A4_E_ALIGN;
+  w4a4::launch_moe_route(logits, dtype, T, E, ldl, (int)k, renormalize != 0, ids, weights, as_stream(stream));
+  return launched();
+}
+
+static bool moe_extents_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  return T >= 0 && k > 0 && T <= w4a4::kMoeMaxPairs && k <= w4a4::kMoeMaxPairs && T * k <= w4a4::kMoeMaxPairs &&
+         E > 0 && E <= w4a4::kMoeMaxExperts && H > 0 && H % 16 == 0 && H <= kMaxW8K && I > 0 && I % 16 == 0 &&
+         I <= kMaxW8K;
+}
+
+int64_t w8a8_moe_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  if (!moe_extents_ok(T, k, E, H, I)) return -1;
+  return T == 0 ? 0 : w4a4::moe_workspace(T, k, I);
+}
+
+w4a4_status_t w8a8_moe(const int8_t* xq, const float* xs, const int32_t* ids, const float* weights, int64_t T, int64_t k,
+                       const int8_t* w13, const float* s13, const int8_t* w2, const float* s2,
+                       int64_t E, int64_t H, int64_t I, int32_t act, void* workspace, int64_t workspace_bytes,
+                       void* y, int32_t y_dtype, int64_t ldy, void* stream) {
+  if (!moe_extents_ok(T, k, E, H, I) || !act_ok(act)) return W4A4_E_SHAPE;
+  if (!x_dtype_ok(y_dtype)) return W4A4_E_DTYPE;
+  if (T == 0) return W4A4_OK;
+  const int64_t need = w8a8_moe_workspace(T, k, E, H, I);
+  if (ldy < H || workspace_bytes < need) return W4A4_E_SHAPE;
+  if (!xq || !xs || !ids || !weights || !w13 || !s13 || !w2 || !s2 || !y || !workspace) return W4A4_E_NULL;
+  if (!aligned(xq, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(workspace, 16) || !aligned(xs, 4) ||
+      !aligned(ids, 4) || !aligned(weights, 4) || !aligned(s13, 4) || !aligned(s2, 4) || !aligned(y, 2))
+    return W4A4_E_ALIGN;
+  w4a4::MoeArgs a = {};
+  a.xq = xq; a.xs = xs; a.ids = ids; a.weights = weights;
+  a.w13 = w13; a.s13 = s13; a.w2 = w2; a.s2 = s2;
+  a.T = (int)T; a.k = (int)k; a.E = (int)E; a.H = (int)H; a.I = (int)I;
+  a.act = act;
+  a.y = y; a.ydtype = y_dtype; a.ldy = ldy;
+  a.workspace = workspace;
+  w4a4::launch_w8a8_moe(a, as_stream(stream));
   return launched();
 }
 

@@ -97,6 +97,69 @@ void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream);
 bool w8a8_one_launch(int64_t M, int64_t N, int64_t K);
 void launch_w8a8_small(const W8GemmArgs& a, const void* x, int bf16, int64_t ldx, hipStream_t stream);
 
+// ---- Forms with an epilogue (w8a8_act.hip): y is fp16 or bf16. gated: channels 2n
+// and 2n + 1 of W are the gate and the value of output n (W8GemmArgs::N counts W's
+// channels).
+struct W8Epilogue {
+  int act;                // w4a4::ACT_*
+  bool gated;
+  const void* residual;   // [M][ldr] of y's type, or nullptr; may be y itself
+  int64_t ldr;
+  bool wide;              // w8a8_wide_rows of y and the residual
+};
+bool w8a8_wide_rows(int64_t outs, const void* y, int64_t ldy, const void* residual, int64_t ldr);
+int64_t w8a8_act_workspace(int64_t M, int64_t N, int64_t K, bool wide);
+void launch_w8a8_gemm_act(const W8GemmArgs& g, const W8Epilogue& e, hipStream_t stream);
+void launch_w8a8_gemm_gated(const W8GemmArgs& g, const W8Epilogue& e, hipStream_t stream);
+// in one launch, where w8a8_one_launch says so
+void launch_w8a8_small_act(const W8GemmArgs& g, const W8Epilogue& e, const void* x, int bf16, int64_t ldx,
+                           hipStream_t stream);
+
+void launch_w8a8_small_gated(const W8GemmArgs& g, const W8Epilogue& e, const void* x, int bf16, int64_t ldx,
+                             hipStream_t stream);
+
+// ---- RMS norm with INT8 output (norm8.hip). h: the sum x + residual, written where
+// there is a residual; y: the normed tokens, or nullptr.
+struct W8NormArgs {
+  const void* x;
+  const void* residual;
+  const void* weight;
+  void* h;
+  void* y;
+  int8_t* q;
+  float* s;
+  int64_t ldx, ldr, ldh, ldy, M, K;
+  float eps;
+  int bf16, weight_f32;
+};
+void launch_w8a8_rmsnorm(const W8NormArgs& a, hipStream_t stream);
+
+// ---- Mixture of experts (moe.hip)
+void launch_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int k, bool renorm,
+                      int32_t* ids, float* weights, hipStream_t stream);
+
+constexpr int kMoeMaxPairs = 512;    // T k
+constexpr int kMoeMaxExperts = 512;
+constexpr int kRouteMaxK = 64;       // a choice a lane
+struct MoeArgs {
+  const int8_t* xq;       // [T][H]
+  const float* xs;        // [T]
+  const int32_t* ids;     // [T][k]; others than 0 .. E - 1 are skipped
+  const float* weights;   // [T][k]
+  const int8_t* w13;      // [E][2 I][H], rows 2i gate and 2i + 1 up
+  const float* s13;       // [E][2 I]
+  const int8_t* w2;       // [E][H][I]
+  const float* s2;        // [E][H]
+  int T, k, E, H, I;
+  int act;
+  void* y;                // [T][ldy]
+  int ydtype;
+  int64_t ldy;
+  void* workspace;
+};
+int64_t moe_workspace(int64_t T, int64_t k, int64_t I);
+void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream);
+
 // ---- INT8 key/value cache (kv8_cache.hip, kv8_attention.hip)
 struct KvPool {
   int8_t* k;           // [num_pages][heads][page][dim]

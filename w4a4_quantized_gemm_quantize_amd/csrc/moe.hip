@@ -1,0 +1,517 @@
+// Mixture of experts for gfx950: the router, and a layer of INT8 experts for few
+// tokens.
+//
+// Router: per token the k largest logits, the lower index first among equals, and
+//   w_j = exp(l_j - m) / sum exp(l - m)   (over all experts, or the k chosen).
+//
+// Layer: for each pair p = (token t, choice j) with expert e = ids[t][j]
+//   g, u = rows 2i and 2i + 1 of  fl32(P) fl32(xs[t] s13[e]),  P = w13[e] xq[t]
+//   h[p] = act(g) u                                   (fp32)
+//   hq[p], hs[p] = INT8 codes and scale of h[p]       (the rule of quant8.h)
+//   y[t] = sum_j weights[t][j] fl32(P') fl32(hs[p] s2[e]),  P' = w2[e] hq[p]
+// with exact int32 sums P, P' and the sum over j in order, so results do not vary.
+#include <algorithm>
+
+#include "act8.h"
+#include "device.h"
+#include "launch.h"
+#include "quant8.h"
+
+namespace w4a4 {
+
+namespace {
+
+// ---- Router -----------------------------------------------------------------
+
+// A wave's maximum, in every lane.
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t m) {
+  m = dpp_max<DPP_HALF_MIRROR>(m);
+  m = dpp_max<DPP_QUAD_1032>(m);
+  m = dpp_max<DPP_QUAD_2301>(m);
+  m = dpp_max<DPP_ROW_MIRROR>(m);
+  const auto a = __builtin_amdgcn_permlane16_swap(m, m, false, false);
+  m = max(a[0], a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(m, m, false, false);
+  return max(b[0], b[1]);
+}
+__device__ __forceinline__ float wave_add(float v) {
+  v += dpp<DPP_HALF_MIRROR>(v);
+  v += dpp<DPP_QUAD_1032>(v);
+  v += dpp<DPP_QUAD_2301>(v);
+  v += dpp<DPP_ROW_MIRROR>(v);
+  v += __shfl_xor(v, 16);
+  v += __shfl_xor(v, 32);
+  return v;
+}
+
+// Floats to integers of the same order, minus infinity (and what counts as it) to 0.
+__device__ __forceinline__ uint32_t order_key(float v) {
+  if (!(v > -__builtin_inff())) return 0;               // NaN too
+  const uint32_t b = __float_as_uint(v + 0.0f);         // -0 as +0: they are equal
+  return b ^ ((uint32_t)((int)b >> 31) | 0x80000000u);
+}
+
+// One wave per token, NL consecutive experts per lane. A choice takes the largest
+// key, and of the lanes that hold it the lowest.
+template <int DT, int NL>
+__global__ __launch_bounds__(256) void k_moe_route(const void* __restrict__ logits, int64_t T, int E, int64_t ldl, int k,
+                                                   int renorm, int32_t* __restrict__ ids, float* __restrict__ weights) {
+  const int lane = threadIdx.x & 63;
+  const int64_t t = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (t >= T) return;                                   // whole waves
+  uint32_t key[NL];
+  float v[NL];
+#pragma unroll
+  for (int i = 0; i < NL; ++i) {
+    const int e = lane * NL + i;
+    v[i] = -__builtin_inff();
+    if (e < E) {
+      const int64_t at = t * ldl + e;
+      if constexpr (DT == 0) v[i] = static_cast<const float*>(logits)[at];
+      else if constexpr (DT == 1) v[i] = (float)static_cast<const _Float16*>(logits)[at];
+      else v[i] = __uint_as_float((uint32_t)static_cast<const uint16_t*>(logits)[at] << 16);
+      v[i] = v[i] > 3.402823466e38f ? 3.402823466e38f : v[i];
+    }
+    key[i] = order_key(v[i]);
+  }
+  auto best = [&]() {
+    uint32_t m = key[0];
+#pragma unroll
+    for (int i = 1; i < NL; ++i) m = max(m, key[i]);
+    return m;
+  };
+  uint32_t top = wave_max_u32(best());
+  float vmax = 0.0f, total = 0.0f;
+  if (top) {
+    vmax = __uint_as_float(top & 0x80000000u ? top ^ 0x80000000u : ~top);
+    if (!renorm) {
+#pragma unroll
+      for (int i = 0; i < NL; ++i) total += key[i] ? expf(v[i] - vmax) : 0.0f;
+      total = wave_add(total);
+    }
+  }
+  int my_id = -1;
+  float my_w = 0.0f, chosen = 0.0f;
+  for (int j = 0; j < k; ++j) {
+    if (top) {                                          // else nothing is left: id -1, weight 0
+      const uint32_t mine = best();
+      const int from = __builtin_ctzll(__ballot(mine == top));
+      int at = 0;
+#pragma unroll
+      for (int i = NL - 1; i >= 0; --i) at = key[i] == top ? i : at;
+      at = __builtin_amdgcn_readlane(at, from);
+      if (lane == from) {
+#pragma unroll
+        for (int i = 0; i < NL; ++i) key[i] = i == at ? 0 : key[i];
+      }
+      const float w = expf(__uint_as_float(top & 0x80000000u ? top ^ 0x80000000u : ~top) - vmax);
+      chosen += w;
+      if (lane == j) my_id = from * NL + at, my_w = w;
+      if (j + 1 < k) top = wave_max_u32(best());
+    }
+  }
+  if (lane < k) {
+    const float d = renorm ? chosen : total;
+    ids[t * k + lane] = my_id;
+    weights[t * k + lane] = my_id < 0 ? 0.0f : my_w / d;
+  }
+}
+
+// ---- Experts ----------------------------------------------------------------
+
+struct MoeParams {
+  const int8_t* a;        // UP: the tokens' codes [T][K]; DOWN: codes of h [P][K] (FUSED: not used)
+  const float* sa;        // their scales
+  const float* h;         // DOWN, FUSED: [P][K]
+  const int32_t* ids;
+  const float* weights;
+  const int8_t* w;        // [E][N][K]
+  const float* sw;        // [E][N]
+  int T, k, P, E, K, N, act;
+  float* h_out;           // UP: [P][N / 2]
+  void* y;                // DOWN
+  int ydtype;
+  int64_t ldy;
+};
+
+constexpr int kResLd = 20;         // ints per row of sums: the four row groups of a wave on their own banks
+constexpr size_t kLds = 64 * 1024;
+
+__host__ __device__ constexpr int max_entries(int P, int E, int RT) { return (P < E ? P : E) + P / (16 * RT); }
+__host__ __device__ constexpr int code_ld(int K, int CH) { return (K + 64 * CH - 1) / (64 * CH) * (64 * CH) + 16; }
+
+// LDS: sums, ids, counts / first positions, entries, pairs by position and back.
+inline size_t moe_lds(int P, int E, int RT) {
+  return (size_t)P * kResLd * 4 + P * 4 + E * 4 + (max_entries(P, E, RT) + 1) * 8 + ((P + 1) / 2) * 8 + 32;
+}
+inline size_t fused_lds(int P, int K, int CH) { return (size_t)P * code_ld(K, CH) + P * 4 + 16; }
+
+// The INT8 codes of a row of fp32 values by one wave, and its scale.
+__device__ __forceinline__ float quantize_row(const float* __restrict__ h, int K, int lane, int8_t* codes) {
+  constexpr int KEEP = 2;                              // 1024-element pieces that stay in registers
+  float v[KEEP][16];
+  uint32_t top = 0;
+  auto load = [&](float f[16], int k0) {
+    const float4* src = reinterpret_cast<const float4*>(h + k0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float4 q = k0 < K ? src[j] : float4{0, 0, 0, 0};
+      f[4 * j] = q.x; f[4 * j + 1] = q.y; f[4 * j + 2] = q.z; f[4 * j + 3] = q.w;
+    }
+  };
+  auto most = [&](const float f[16]) {
+#pragma unroll
+    for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(f[j]) & 0x7FFFFFFFu);
+  };
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) load(v[i], 1024 * i + 16 * lane);
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) most(v[i]);
+  for (int k0 = 1024 * KEEP + 16 * lane; k0 < K; k0 += 1024) {
+    float f[16];
+    load(f, k0);
+    most(f);
+  }
+  top = wave_max_u32(top);
+  const float s = __uint_as_float(top >= 0x7F800000u ? 0x7FC00000u : top) / 127.0f;
+  const float k = scale_guard(s);
+  const float sk = s * k;
+  const float rs = s == 0.0f ? 0.0f : 1.0f / sk;
+#pragma unroll
+  for (int i = 0; i < KEEP; ++i) {
+    const int k0 = 1024 * i + 16 * lane;
+    if (k0 < K) *reinterpret_cast<uint4*>(codes + k0) = codes16f(v[i], k, sk, rs);
+  }
+  for (int k0 = 1024 * KEEP + 16 * lane; k0 < K; k0 += 1024) {
+    float f[16];
+    load(f, k0);
+    *reinterpret_cast<uint4*>(codes + k0) = codes16f(f, k, sk, rs);
+  }
+  return s;
+}
+
+// A workgroup owns 16 channels (UP: 8 gates and their 8 values) of every expert, or of
+// a share of the experts that the tokens chose (UP, blockIdx.y). It sorts the pairs
+// by expert; an entry is up to 16 RT rows of one expert, and the entries' chunks of CH
+// 64-k steps are dealt to the waves in contiguous runs of equal length, whatever
+// experts they fall in. A wave streams the weights of its chunks from memory
+// straight into v_mfma_i32_16x16x64_i8, the next chunk's in flight, and adds an
+// entry's int32 sums to those in LDS (exact in any order).
+// FUSED: h is quantized here, into LDS, by every workgroup.
+enum { UP = 0, DOWN = 1 };
+template <int STAGE, int RT, int CH, int NW, bool FUSED>
+__global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
+  constexpr int NT = 64 * NW;
+  static_assert(kMoeMaxPairs <= NT && kMoeMaxExperts <= NT, "one a thread");
+  extern __shared__ __align__(16) uint8_t lds[];
+  __shared__ uint32_t wave_total[NW];
+  int* const sums = reinterpret_cast<int*>(lds);                     // [P][kResLd]
+  int* const id_of = sums + p.P * kResLd;                            // [P]
+  int* const first = id_of + p.P;                                    // [E] counts, then first positions
+  int2* const entry = reinterpret_cast<int2*>(lds + ((p.P * (kResLd + 1) + p.E) * 4 + 7) / 8 * 8);
+  uint16_t* const pair_of = reinterpret_cast<uint16_t*>(entry + max_entries(p.P, p.E, RT) + 1);
+  uint16_t* const pos_of = pair_of + (p.P + 1) / 2 * 2;
+  int8_t* const codes = reinterpret_cast<int8_t*>(lds) + ((reinterpret_cast<uint8_t*>(pos_of + p.P) - lds) + 15) / 16 * 16;
+  const int cld = FUSED ? code_ld(p.K, CH) : 0;
+  float* const hs = reinterpret_cast<float*>(codes + p.P * cld);     // [P], FUSED
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int c = lane & 15, g = lane >> 4;
+  const int n0 = (int)blockIdx.x * 16;
+
+  // The pairs by expert.
+  for (int i = tid; i < p.E; i += NT) first[i] = 0;
+  for (int i = tid; i < p.P * kResLd; i += NT) sums[i] = 0;
+  __syncthreads();
+  int my_id = -1, my_rank = 0;                                       // P <= kMoeMaxPairs <= NT: one pair a thread
+  if (tid < p.P) {
+    my_id = p.ids[tid];
+    my_id = my_id >= 0 && my_id < p.E ? my_id : -1;
+    id_of[tid] = my_id;
+    if (my_id >= 0) my_rank = atomicAdd(&first[my_id], 1);
+  }
+  __syncthreads();
+  const int count = tid < p.E ? first[tid] : 0;                      // E <= kMoeMaxExperts <= NT
+  const uint32_t own = (uint32_t)((count + 16 * RT - 1) / (16 * RT)) << 16 | (uint32_t)count;
+  uint32_t upto = own;                                               // entries << 16 | positions, up to this expert
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const uint32_t o = (uint32_t)__shfl_up((int)upto, d);
+    if (lane >= d) upto += o;
+  }
+  if (lane == 63) wave_total[wave] = upto;
+  __syncthreads();
+  uint32_t all = 0, before = upto - own;
+#pragma unroll
+  for (int w = 0; w < NW; ++w) {
+    if (w < wave) before += wave_total[w];
+    all += wave_total[w];
+  }
+  if (tid < p.E) {
+    first[tid] = (int)(before & 0xFFFFu);
+    for (int i = 0; 16 * RT * i < count; ++i)
+      entry[(before >> 16) + i] = int2{tid | min(16 * RT, count - 16 * RT * i) << 16, (int)(before & 0xFFFFu) + 16 * RT * i};
+  }
+  const int entries = __builtin_amdgcn_readfirstlane((int)(all >> 16)), positions = (int)(all & 0xFFFFu);
+  if (tid == 0) entry[entries] = int2{0, positions};
+  __syncthreads();
+  if (my_id >= 0) {
+    const int pos = first[my_id] + my_rank;
+    pair_of[pos] = (uint16_t)tid;
+    pos_of[tid] = (uint16_t)pos;
+  }
+  __syncthreads();
+
+  // This workgroup's entries, this wave's chunks.
+  const int shares = gridDim.y, share = blockIdx.y;
+  // A share holds whole experts: workgroups may differ in the order of an expert's rows.
+  auto whole = [&](int e) {
+    while (e > 0 && e < entries && (entry[e].x & 0xFFFF) == (entry[e - 1].x & 0xFFFF)) ++e;
+    return __builtin_amdgcn_readfirstlane(e);
+  };
+  const int ent0 = whole(entries * share / shares), ent1 = whole(entries * (share + 1) / shares);
+  const int nch = (p.K + 64 * CH - 1) / (64 * CH);
+  const int chunks = (ent1 - ent0) * nch;
+  const int ch0 = (int)((int64_t)chunks * wave / NW), ch1 = (int)((int64_t)chunks * (wave + 1) / NW);
+  struct Buf {
+    v4i w[CH];
+    v4i a[FUSED ? 1 : RT][FUSED ? 1 : CH];
+  };
+  // rows of an entry that this lane supplies (dropped ones past its end)
+  auto entry_at = [&](int e) {
+    const int2 v = entry[e];
+    return int2{__builtin_amdgcn_readfirstlane(v.x), __builtin_amdgcn_readfirstlane(v.y)};
+  };
+  const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, FUSED ? 0 : (STAGE == UP ? p.T : p.P) * p.K);
+  int l_ent = ent0 + (chunks ? ch0 / nch : 0), l_ch = chunks ? ch0 % nch : 0, l_at = ch0;
+  __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w, 0);
+  int off_a[RT];
+  auto enter_load = [&]() {
+    const int2 v = entry_at(l_ent);
+    const int e = v.x & 0xFFFF, n = v.x >> 16;
+    rW = buffer_rsrc(p.w + ((int64_t)e * p.N + n0) * p.K, 16 * p.K);
+    if constexpr (!FUSED) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        const int row = 16 * r + c;
+        const int pair = pair_of[v.y + min(row, n - 1)];
+        off_a[r] = row < n ? (STAGE == UP ? pair / p.k : pair) * p.K + 16 * g : kDroppedOffset;
+      }
+    }
+  };
+#pragma unroll
+  for (int r = 0; r < RT; ++r) off_a[r] = kDroppedOffset;
+  if (ch0 < ch1) enter_load();
+  auto fetch = [&](Buf& b) {
+    if (l_at < ch1 && l_ch == nch) {
+      l_ch = 0;
+      ++l_ent;
+      enter_load();
+    }
+#pragma unroll
+    for (int u = 0; u < CH; ++u) {
+      const int k0 = 64 * (l_ch * CH + u);
+      const int out = l_at < ch1 && k0 + 16 * g < p.K ? 0 : kDroppedOffset;
+      b.w[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, (c * p.K + 16 * g) | out, k0, 0));
+      if constexpr (!FUSED) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r)
+          b.a[r][u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, off_a[r] | out, k0, 0));
+      }
+    }
+    ++l_ch;
+    ++l_at;
+  };
+  Buf b0, b1;
+  fetch(b0);
+  fetch(b1);
+
+  if constexpr (FUSED) {
+    for (int i = wave; i < p.P; i += NW) {
+      if (__builtin_amdgcn_readfirstlane(id_of[i]) < 0) continue;
+      const float s = quantize_row(p.h + (int64_t)i * p.K, p.K, lane, codes + i * cld);
+      if (lane == 0) hs[i] = s;
+    }
+    __syncthreads();
+  }
+
+  int c_ent = l_ent, c_ch = chunks ? ch0 % nch : 0, c_n = 0, c_pos = 0;
+  if (ch0 < ch1) c_ent = ent0 + ch0 / nch;
+  const int8_t* row_a[RT];
+  v4i acc[RT];
+  auto enter = [&]() {
+    const int2 v = entry_at(c_ent);
+    c_n = v.x >> 16;
+    c_pos = v.y;
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      acc[r] = v4i{0, 0, 0, 0};
+      if constexpr (FUSED) row_a[r] = codes + pair_of[c_pos + min(16 * r + c, c_n - 1)] * cld + 16 * g;
+    }
+  };
+  auto consume = [&](const Buf& b) {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+      if (16 * r >= c_n) break;
+#pragma unroll
+      for (int u = 0; u < CH; ++u) {
+        v4i a;
+        if constexpr (FUSED) a = *reinterpret_cast<const v4i*>(row_a[r] + 64 * (c_ch * CH + u));
+        else a = b.a[r][u];
+        acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b.w[u], acc[r], 0, 0, 0);
+      }
+    }
+    if (++c_ch == nch) {
+      c_ch = 0;
+      return true;
+    }
+    return false;
+  };
+  auto flush = [&]() {
+#pragma unroll
+    for (int r = 0; r < RT; ++r) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = 16 * r + 4 * g + i;
+        if (row < c_n) atomicAdd(&sums[(c_pos + row) * kResLd + c], acc[r][i]);
+      }
+    }
+  };
+  if (ch0 < ch1) enter();
+  for (int at = ch0; at < ch1; at += 2) {
+    // the second of a pair past the run's end holds zeros of W
+    bool done = consume(b0);
+    fetch(b0);
+    if (done || at + 1 >= ch1) {
+      flush();
+      if (at + 1 >= ch1) break;
+      ++c_ent;
+      enter();
+    }
+    done = consume(b1);
+    fetch(b1);
+    if (done || at + 2 >= ch1) {
+      flush();
+      if (at + 2 >= ch1) break;
+      ++c_ent;
+      enter();
+    }
+  }
+  __syncthreads();
+
+  if constexpr (STAGE == UP) {
+    const int pos0 = entry[ent0].y, pos1 = entry[ent1].y, I = p.N >> 1;
+    for (int o = tid; o < (pos1 - pos0) * 8; o += NT) {
+      const int pos = pos0 + (o >> 3), i = o & 7;
+      const int pair = pair_of[pos];
+      const float sa = p.sa[pair / p.k];
+      const float* sw = p.sw + (int64_t)id_of[pair] * p.N + n0 + 2 * i;
+      const float gate = (float)sums[pos * kResLd + 2 * i] * (sa * sw[0]);
+      const float up = (float)sums[pos * kResLd + 2 * i + 1] * (sa * sw[1]);
+      p.h_out[(int64_t)pair * I + (n0 >> 1) + i] = activate(p.act, gate) * up;
+    }
+  } else {
+    for (int o = tid; o < p.T * 16; o += NT) {
+      const int t = o >> 4, n = o & 15;
+      float sum = 0.0f;
+#pragma unroll 4
+      for (int j = 0; j < p.k; ++j) {
+        const int pair = t * p.k + j, e = id_of[pair];
+        const float s = (FUSED ? hs[pair] : p.sa[pair]) * p.sw[(int64_t)max(e, 0) * p.N + n0 + n];
+        const float v = (float)sums[(e < 0 ? 0 : pos_of[pair]) * kResLd + n] * s;
+        const float f = p.weights[pair];
+        sum = e < 0 ? sum : fmaf(f, v, sum);
+      }
+      const int64_t at = t * p.ldy + n0 + n;
+      if (p.ydtype == 1) static_cast<_Float16*>(p.y)[at] = (_Float16)sum;
+      else static_cast<__bf16*>(p.y)[at] = (__bf16)sum;
+    }
+  }
+}
+
+// The codes of h for k_w8a8_moe without FUSED, one wave a pair. Pairs without an
+// expert have no h.
+__global__ __launch_bounds__(256) void k_moe_quant(const float* __restrict__ h, const int32_t* __restrict__ ids, int E,
+                                                   int P, int K, int8_t* __restrict__ codes, float* __restrict__ s) {
+  const int i = __builtin_amdgcn_readfirstlane((int)blockIdx.x * 4 + ((int)threadIdx.x >> 6)), lane = threadIdx.x & 63;
+  if (i >= P || ids[i] < 0 || ids[i] >= E) return;
+  const float v = quantize_row(h + (int64_t)i * K, K, lane, codes + (int64_t)i * K);
+  if (lane == 0) s[i] = v;
+}
+
+int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
+
+template <int STAGE, bool FUSED>
+void launch_stage(const MoeParams& p, int shares, int rt, hipStream_t stream) {
+  const dim3 grid((unsigned)(p.N / 16), (unsigned)shares);
+#define MOE_STAGE(RT, CH, NW)                                                                                  \
+  {                                                                                                            \
+    const size_t lds = moe_lds(p.P, p.E, RT) + (FUSED ? fused_lds(p.P, p.K, CH) : 0);                          \
+    hipLaunchKernelGGL((k_w8a8_moe<STAGE, RT, CH, NW, FUSED>), grid, dim3(64 * NW), (unsigned)lds, stream, p); \
+  }
+  if constexpr (FUSED) MOE_STAGE(1, 4, 16)
+  else if (rt == 1) MOE_STAGE(1, 4, (STAGE == UP ? 8 : 16))
+  else if (rt == 2) MOE_STAGE(2, 2, (STAGE == UP ? 8 : 16))
+  else MOE_STAGE(4, 2, 8)
+#undef MOE_STAGE
+}
+
+}  // namespace
+
+void launch_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int k, bool renorm,
+                      int32_t* ids, float* weights, hipStream_t stream) {
+  const dim3 grid((unsigned)((T + 3) / 4)), block(256);
+#define MOE_ROUTE(DT, NL) \
+  hipLaunchKernelGGL((k_moe_route<DT, NL>), grid, block, 0, stream, logits, T, (int)E, ldl, k, (int)renorm, ids, weights)
+#define MOE_ROUTE_E(DT)                   \
+  if (E <= 64) MOE_ROUTE(DT, 1);          \
+  else if (E <= 128) MOE_ROUTE(DT, 2);    \
+  else if (E <= 256) MOE_ROUTE(DT, 4);    \
+  else MOE_ROUTE(DT, 8)
+  if (dtype == 0) { MOE_ROUTE_E(0); }
+  else if (dtype == 1) { MOE_ROUTE_E(1); }
+  else { MOE_ROUTE_E(2); }
+#undef MOE_ROUTE_E
+#undef MOE_ROUTE
+}
+
+int64_t moe_workspace(int64_t T, int64_t k, int64_t I) {
+  const int64_t P = T * k;
+  return align256(4 * P * I) + align256(P * I) + align256(4 * P);
+}
+
+void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream) {
+  const int P = a.T * a.k;
+  float* const h = static_cast<float*>(a.workspace);
+  int8_t* const codes = static_cast<int8_t*>(a.workspace) + align256(4 * (int64_t)P * a.I);
+  float* const hs = reinterpret_cast<float*>(codes + align256((int64_t)P * a.I));
+  MoeParams p = {};
+  p.ids = a.ids;
+  p.weights = a.weights;
+  p.T = a.T; p.k = a.k; p.P = P; p.E = a.E;
+  p.act = a.act;
+  // rows an entry holds: an expert has at most T (or repeats), P / E on average
+  const int rt = a.T <= 16 ? 1 : a.T <= 32 || P <= 12 * a.E ? 2 : 4;
+
+  p.a = a.xq; p.sa = a.xs;
+  p.w = a.w13; p.sw = a.s13;
+  p.K = a.H; p.N = 2 * a.I;
+  p.h_out = h;
+  const int tiles = p.N / 16, used = std::min(P, a.E);
+  const int shares = std::max(1, std::min(used, 512 / tiles));
+  launch_stage<UP, false>(p, shares, rt, stream);
+
+  p.K = a.I; p.N = a.H;
+  p.w = a.w2; p.sw = a.s2;
+  p.y = a.y; p.ydtype = a.ydtype; p.ldy = a.ldy;
+  if (a.T <= 16 && (int64_t)P * a.I <= 32768 && moe_lds(P, a.E, 1) + fused_lds(P, a.I, 4) <= kLds) {
+    p.h = h;
+    launch_stage<DOWN, true>(p, 1, 1, stream);
+    return;
+  }
+  hipLaunchKernelGGL(k_moe_quant, dim3((unsigned)((P + 3) / 4)), dim3(256), 0, stream, h, a.ids, a.E, P, a.I, codes, hs);
+  p.a = codes; p.sa = hs;
+  launch_stage<DOWN, false>(p, 1, rt, stream);
+}
+
+}  // namespace w4a4

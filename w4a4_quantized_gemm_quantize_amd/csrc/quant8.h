@@ -1,4 +1,5 @@
-// Device helpers of the INT8 quantizers (w8a8_quantize_act, kv8_append): the rule
+// Device helpers of the INT8 quantizers (w8a8_quantize_act, w8a8_rmsnorm_quantize,
+// w8a8_moe, kv8_append): the rule
 // is a = max|x|, s = fl32(a / 127), q = rne(fl32(x / s)); s is NaN where a value
 // of the row is a NaN or an infinity.
 #pragma once
@@ -49,6 +50,21 @@ __device__ __forceinline__ uint4 codes16(const uint4 r[2], float k, float s, flo
       b[2 * i] = __float_as_uint(div_rn(lo_f32<BF>(w[2 * j + i]) * k, s, rs) + 12582912.0f);
       b[2 * i + 1] = __float_as_uint(div_rn(hi_f32<BF>(w[2 * j + i]) * k, s, rs) + 12582912.0f);
     }
+    const uint32_t p01 = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);
+    const uint32_t p23 = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
+    o[j] = p01 | p23;
+  }
+  return uint4{o[0], o[1], o[2], o[3]};
+}
+
+// The codes of 16 fp32 values, as codes16.
+__device__ __forceinline__ uint4 codes16f(const float t[16], float k, float s, float rs) {
+  uint32_t o[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t b[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(div_rn(t[4 * j + i] * k, s, rs) + 12582912.0f);
     const uint32_t p01 = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);
     const uint32_t p23 = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
     o[j] = p01 | p23;

@@ -1,0 +1,132 @@
+// W8A8 products with an epilogue for gfx950: bias, activation (or the gate of two
+// interleaved halves) and residual on the exact sums, rounded once to 16 bits.
+//
+//   v[m,n] = fl32(fl32(fl32(P) fl32(xs[m] ws[n])) + bias[n])
+//   Y[m,n] = act(v[m,n]) + R[m,n],  or gated  act(v[m,2n]) v[m,2n+1] + R[m,n]
+//
+// The products are those of w8a8.hip, K split where its plan splits.
+#pragma once
+
+#include "w8a8_kernels.h"
+
+namespace w4a4 {
+
+namespace {
+
+// Adds the K ranges' int32 sums and finishes them, one output a thread.
+template <int EPI>
+__global__ __launch_bounds__(kThreads) void k_w8a8_join_act(W8Params p, int splits) {
+  constexpr int C = EPI == EPI_GATED ? 2 : 1;              // channels of an output
+  const int outs = p.N / C;
+  const int64_t total = (int64_t)p.M * outs, plane = (int64_t)p.M * p.N;
+  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
+    const int64_t m = i / outs;
+    const int n = (int)(i - m * outs);
+    int v[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) v[c] = 0;
+    for (int s = 0; s < splits; ++s) {
+#pragma unroll
+      for (int c = 0; c < C; ++c) v[c] += p.part[s * plane + m * p.N + C * n + c];
+    }
+    float f[C];
+#pragma unroll
+    for (int c = 0; c < C; ++c) f[c] = scaled(v[c], p.sa[m], p.sw[C * n + c], p.bias ? p.bias[C * n + c] : 0.0f);
+    float y = activate(p.act, f[0]);
+    if constexpr (EPI == EPI_GATED) y *= f[1];
+    if (p.res) y = plus(y, load16(p.res, p.ydtype, m * p.ldr + n));
+    store_y(p.y, p.ydtype, m * p.ldy + n, y);
+  }
+}
+
+template <int BM, int BN, int WM, int WN, int S, int EPI>
+void launch_tiles_act(W8Params p, hipStream_t stream) {
+  const int64_t tiles = (int64_t)((p.M + BM - 1) / BM) * ((p.N + BN - 1) / BN);
+  p.stages = (p.K + 127) / 128;
+  const dim3 grid((unsigned)std::min<int64_t>(tiles, kCUs)), block(64 * WM * WN);
+#define W8A8_ACT(KIND)                                                                                                   \
+  if (p.ydtype == 1)                                                                                                     \
+    hipLaunchKernelGGL((k_w8a8_gemm_tiles<BM, BN, WM, WN, S, OUT_16, true, EPI, KIND, false>), grid, block, 0, stream, p); \
+  else                                                                                                                   \
+    hipLaunchKernelGGL((k_w8a8_gemm_tiles<BM, BN, WM, WN, S, OUT_16, true, EPI, KIND, true>), grid, block, 0, stream, p)
+  if (p.act == ACT_GELU) {
+    W8A8_ACT(KIND_ERF);
+  } else if (p.act == ACT_SILU || p.act == ACT_GELU_TANH) {
+    W8A8_ACT(KIND_SIGMOID);
+  } else {
+    W8A8_ACT(KIND_LINEAR);
+  }
+#undef W8A8_ACT
+}
+
+// int32 sums of `splits` K ranges into the workspace, then the join.
+template <int EPI>
+void launch_raw(W8Params p, int splits, hipStream_t stream) {
+  const int64_t tiles = (int64_t)((p.M + 127) / 128) * ((p.N + 127) / 128);
+  const int nk = (p.K + 127) / 128;
+  p.stages = (nk + splits - 1) / splits;
+  p.splits = splits = (nk + p.stages - 1) / p.stages;
+  const int64_t blocks = tiles * splits;
+  const bool wide = p.N % 4 == 0 && 128 * (int64_t)p.N * 4 < (int64_t{1} << 31);
+  if (wide)
+    hipLaunchKernelGGL((k_w8a8_gemm_tiles<128, 128, 2, 2, 3, OUT_RAW, true>), dim3((unsigned)std::min<int64_t>(blocks, kCUs)),
+                       dim3(256), 0, stream, p);
+  else
+    hipLaunchKernelGGL((k_w8a8_gemm_tiles<128, 128, 2, 2, 3, OUT_RAW, false>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  const int64_t outs = (int64_t)p.M * p.N / (EPI == EPI_GATED ? 2 : 1);
+  const int64_t jb = std::min<int64_t>((outs + kThreads - 1) / kThreads, 8192);
+  hipLaunchKernelGGL(k_w8a8_join_act<EPI>, dim3((unsigned)jb), dim3(kThreads), 0, stream, p, splits);
+}
+
+W8Params act_params(const W8GemmArgs& g, const W8Epilogue& e) {
+  W8Params p = params(g);
+  p.act = e.act;
+  p.res = static_cast<const uint16_t*>(e.residual);
+  p.ldr = e.ldr;
+  return p;
+}
+
+// Tiles that write outputs themselves need rows that take 16-byte stores; other
+// rows, of odd widths or strides, go through the int32 sums, as K ranges do.
+W8Plan plan_act(int64_t M, int64_t N, int64_t K, bool wide) {
+  W8Plan pl = plan_w8a8(M, N, K);
+  if (pl.tile != TILE_SMALL && !wide && pl.tile != TILE_128) pl = W8Plan{TILE_128, 1};
+  return pl;
+}
+bool sums_in_workspace(const W8Plan& pl, bool wide) { return pl.tile != TILE_SMALL && (pl.splits > 1 || !wide); }
+
+template <int EPI>
+void launch_gemm_act(const W8GemmArgs& g, const W8Epilogue& e, hipStream_t stream) {
+  W8Params p = act_params(g, e);
+  const W8Plan pl = plan_act(g.M, g.N, g.K, e.wide);
+  if (pl.tile == TILE_SMALL) {
+    launch_small<0, 0, EPI>(p, stream);
+  } else if (sums_in_workspace(pl, e.wide)) {
+    p.part = static_cast<int32_t*>(g.workspace);
+    launch_raw<EPI>(p, pl.splits, stream);
+  } else if (pl.tile == TILE_256) {
+    launch_tiles_act<256, 256, 2, 4, 2, EPI>(p, stream);
+  } else if (pl.tile == TILE_256_128) {
+    launch_tiles_act<256, 128, 4, 2, 3, EPI>(p, stream);
+  } else {
+    launch_tiles_act<128, 128, 2, 2, 3, EPI>(p, stream);
+  }
+}
+
+template <int EPI>
+void launch_small_act(const W8GemmArgs& g, const W8Epilogue& e, const void* x, int bf16, int64_t ldx,
+                      hipStream_t stream) {
+  W8Params p = act_params(g, e);
+  p.x = static_cast<const uint16_t*>(x);
+  p.ldx = ldx;
+  const int64_t pieces = pieces_per_wave(g.M, g.N, g.K);
+#define W8A8_SMALL(PIECES) bf16 ? launch_small<2, PIECES, EPI>(p, stream) : launch_small<1, PIECES, EPI>(p, stream)
+  if (pieces <= 1) W8A8_SMALL(1);
+  else if (pieces <= 2) W8A8_SMALL(2);
+  else W8A8_SMALL(4);
+#undef W8A8_SMALL
+}
+
+}  // namespace
+
+}  // namespace w4a4

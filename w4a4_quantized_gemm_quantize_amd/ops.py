@@ -642,6 +642,219 @@ def w8a8_linear(x: torch.Tensor, wq, ws, bias=None, out_dtype=torch.float32, out
     return y
 
 
+# ------------------------------------- around the W8A8 products: include/ffn8.h
+
+_ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
+
+
+def _activation(name) -> int:
+    if name not in _ACTIVATIONS:
+        raise ValueError(f"activation must be None, 'relu', 'silu', 'gelu' or 'gelu_tanh', got {name!r}")
+    return _ACTIVATIONS[name]
+
+
+def _need_rows(t, name: str, shape, dtype, device) -> int:
+    """Row stride of a checked 2-D operand of contiguous rows."""
+    _check_out(t, name, shape, dtype, device, row_stride_ok=True)
+    return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
+
+
+def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=None, return_normed: bool = False,
+                          out=None):
+    """RMS norm of fp16 or bf16 X[M, K] (row stride may exceed K) to INT8 codes and one
+    scale per row, the input of :func:`w8a8_gemm` and :func:`w8a8_moe`: ``(xq int8
+    [M, K], xs float32 [M])``, where ``xq * xs ~ h * weight / sqrt(mean(h^2) + eps)``.
+
+    With ``residual`` (X's shape and type) h is x + residual, rounded to X's type, and
+    comes third; with ``return_normed`` the normed rows in X's type come last. ``weight``:
+    [K], float32 or X's type. ``out``: the tuple of outputs to fill instead; its h may
+    be ``x`` or ``residual`` itself (in place). Rows that are not finite have NaN scales."""
+    dt = _x_dtype8(x, "x")
+    ldx = _rows_stride(x, "x")
+    M, K = x.shape
+    device, dtype = x.device, x.dtype
+    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.float32, dtype):
+        raise TypeError(f"weight must be a torch.float32 or {dtype} tensor")
+    if weight.shape != (K,) or not weight.is_contiguous() or weight.device != device:
+        raise ValueError(f"weight must be a contiguous [{K}] tensor on {device}")
+    if not 0.0 < eps < float("inf"):
+        raise ValueError("eps must be positive and finite")
+    ldr = 0 if residual is None else _need_rows(residual, "residual", (M, K), dtype, device)
+    count = 2 + (residual is not None) + bool(return_normed)
+    if out is None:
+        out = (torch.empty((M, K), dtype=torch.int8, device=device),
+               torch.empty((M,), dtype=torch.float32, device=device))
+        for _ in range(count - 2):
+            out += (torch.empty((M, K), dtype=dtype, device=device),)
+    else:
+        out = tuple(out)
+        if len(out) != count:
+            raise ValueError(f"out must hold {count} tensors")
+        _check_out(out[0], "xq", (M, K), torch.int8, device)
+        _check_out(out[1], "xs", (M,), torch.float32, device)
+    h = ldh = y = ldy = 0
+    if residual is not None:
+        ldh = _need_rows(out[2], "h", (M, K), dtype, device)
+        h = out[2].data_ptr()
+    if return_normed:
+        ldy = _need_rows(out[-1], "normed", (M, K), dtype, device)
+        y = out[-1].data_ptr()
+    _call8("w8a8_rmsnorm_quantize", device, x.data_ptr(), dt, ldx, 0 if residual is None else residual.data_ptr(), ldr,
+           weight.data_ptr(), _DTYPE8[weight.dtype], eps, M, K, out[0].data_ptr(), out[1].data_ptr(), h, ldh, y, ldy)
+    return out
+
+
+def w8a8_pack_gated(w_gate: torch.Tensor, w_up: torch.Tensor):
+    """Offline INT8 quantization of a gated layer's two weights (fp16 or bf16, both
+    [N, K], or [E, N, K] for experts), channels interleaved: rows 2n and 2n + 1 of the
+    result are the gate's and the other's row n. ``(wq int8 [2 N, K], ws float32
+    [2 N])``, with a leading E for experts."""
+    if w_gate.shape != w_up.shape or w_gate.dtype != w_up.dtype or w_gate.dim() not in (2, 3):
+        raise ValueError("w_gate and w_up must be alike, [N, K] or [E, N, K]")
+    w = torch.stack((w_gate, w_up), dim=-2).flatten(-3, -2)
+    wq, ws = w8a8_pack_weight(w.reshape(-1, w.shape[-1]))
+    return wq.view(w.shape), ws.view(w.shape[:-1])
+
+
+def _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out):
+    """Checked weights and output of a product with an epilogue:
+    (N, K, residual stride, y, dtype code, y's stride, wide)."""
+    C, K = _w8_weights(wq, ws, bias, device)
+    if gated and C % 2:
+        raise ValueError("gated weights hold two channels an output: an even number of rows")
+    N = C // 2 if gated else C
+    if out is None:
+        y = torch.empty((M, N), dtype=out_dtype, device=device)
+    else:
+        y = out
+        _check_out(y, "out", (M, N), getattr(y, "dtype", None), device, row_stride_ok=True)
+    if y.dtype is not torch.float16 and y.dtype is not torch.bfloat16:
+        raise TypeError("output dtype must be torch.float16 or torch.bfloat16")
+    ldy = y.stride(0) if M > 1 else max(N, 1)
+    wide = N % 8 == 0 and ldy % 8 == 0 and ldy < 1 << 22 and y.data_ptr() % 16 == 0
+    ldr = 0
+    if residual is not None:
+        ldr = _need_rows(residual, "residual", (M, N), y.dtype, device)
+        wide = wide and ldr % 8 == 0 and ldr < 1 << 22 and residual.data_ptr() % 16 == 0
+    return N, K, ldr, y, _DTYPE8[y.dtype], ldy, int(wide)
+
+
+def w8a8_gemm_act(xq, xs, wq, ws, bias=None, activation=None, gated: bool = False, residual=None,
+                  out_dtype=torch.float16, out=None, workspace=None):
+    """:func:`w8a8_gemm` with an epilogue: Y = act(v) + residual with v = (xq @ wq^T)
+    scaled + ``bias``, in fp32, rounded once to fp16 or bf16.
+
+    ``activation``: None, "relu", "silu", "gelu" or "gelu_tanh". ``gated``: ``wq`` [2 N, K] as
+    :func:`w8a8_pack_gated` lays it out, and Y[m, n] = act(v[m, 2n]) * v[m, 2n + 1] +
+    residual. ``residual``: [M, N] of Y's type; ``out`` may be it."""
+    _need(xq, torch.int8, "xq")
+    _need(xs, torch.float32, "xs")
+    if xq.dim() != 2 or not xq.is_contiguous() or not xs.is_contiguous():
+        raise ValueError("xq must be a contiguous 2-D tensor and xs contiguous")
+    M = xq.shape[0]
+    device = xq.device
+    if xs.shape != (M,):
+        raise ValueError("xs must hold one scale per row: shape (M,)")
+    _same_device(xq, xs=xs)
+    act, gated = _activation(activation), int(bool(gated))
+    N, K, ldr, y, dt, ldy, wide = _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out)
+    if xq.shape[1] != K:
+        raise ValueError("K of xq and wq differ")
+    held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_gemm_act_workspace", M, N, K, gated, wide), device)
+    _call8("w8a8_gemm_act", device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
+           0 if bias is None else bias.data_ptr(), act, gated, 0 if residual is None else residual.data_ptr(), ldr,
+           M, N, K, wptr, wbytes, y.data_ptr(), dt, ldy)
+    return y
+
+
+def w8a8_linear_act(x: torch.Tensor, wq, ws, bias=None, activation=None, gated: bool = False, residual=None,
+                    out_dtype=torch.float16, out=None, workspace=None):
+    """:func:`w8a8_linear` with the epilogue of :func:`w8a8_gemm_act`: fp16 or bf16
+    activations [M, K] quantized per token, the product, bias, activation or gate, and
+    residual, in one call."""
+    xdt = _x_dtype8(x, "x")
+    ld = _rows_stride(x, "x")
+    M = x.shape[0]
+    device = x.device
+    act, gated = _activation(activation), int(bool(gated))
+    N, K, ldr, y, dt, ldy, wide = _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out)
+    if x.shape[1] != K:
+        raise ValueError("K of x and wq differ")
+    held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_linear_act_workspace", M, N, K, gated, wide), device)
+    _call8("w8a8_linear_act", device, x.data_ptr(), xdt, M, K, ld, wq.data_ptr(), ws.data_ptr(),
+           0 if bias is None else bias.data_ptr(), act, gated, 0 if residual is None else residual.data_ptr(), ldr,
+           N, wptr, wbytes, y.data_ptr(), dt, ldy)
+    return y
+
+
+def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out=None):
+    """The ``top_k`` largest router logits of every token: ``(ids int32 [T, top_k], weights
+    float32 [T, top_k])``, largest first, the lower id first among equals; the weights
+    are a softmax over all experts, or with ``renormalize`` over the chosen ones.
+    ``logits``: [T, E] fp32, fp16 or bf16 (row stride may exceed E). Minus infinity and NaN are
+    never chosen: where fewer are left, ids are -1 and weights 0."""
+    if not isinstance(logits, torch.Tensor) or not logits.is_cuda:
+        raise TypeError("logits must be a CUDA (HIP) tensor")
+    dt = _y_dtype8(logits.dtype)
+    ld = _rows_stride(logits, "logits")
+    T, E = logits.shape
+    k = _need_max(top_k, "top_k")
+    if out is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
+        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+    else:
+        ids, weights = out
+        _check_out(ids, "ids", (T, k), torch.int32, logits.device)
+        _check_out(weights, "weights", (T, k), torch.float32, logits.device)
+    _call8("moe_route", logits.device, logits.data_ptr(), dt, T, E, ld, k, int(bool(renormalize)), ids.data_ptr(),
+           weights.data_ptr())
+    return ids, weights
+
+
+_MOE_TENSORS = (("xq", torch.int8, 2), ("xs", torch.float32, 1), ("ids", torch.int32, 2), ("weights", torch.float32, 2),
+                ("w13", torch.int8, 3), ("s13", torch.float32, 2), ("w2", torch.int8, 3), ("s2", torch.float32, 2))
+
+
+def w8a8_moe(xq, xs, ids, weights, w13, s13, w2, s2, activation="silu", out_dtype=torch.float16, out=None,
+             workspace=None):
+    """A mixture-of-experts layer of few tokens (T * k <= 512) on INT8 experts, in two
+    launches (three for many pairs): Y[T, H] = sum over a token's choices of weight *
+    (w2[e] @ quantized(act(gate) * up)), gate and up the interleaved channels of
+    w13[e] @ x.
+
+    ``xq`` int8 [T, H], ``xs`` float32 [T]: tokens as :func:`w8a8_rmsnorm_quantize` or
+    :func:`w8a8_quantize_act` give them. ``ids`` int32, ``weights`` float32 [T, k]: from
+    :func:`moe_route`; ids that are no expert add nothing. ``w13`` int8 [E, 2 I, H], ``s13``
+    float32 [E, 2 I]: from :func:`w8a8_pack_gated`; ``w2`` int8 [E, H, I], ``s2`` [E, H]: from
+    :func:`w8a8_pack_weight`. Longer batches go in slices of tokens. Y is fp16 or bf16."""
+    tensors = (xq, xs, ids, weights, w13, s13, w2, s2)
+    device = getattr(xq, "device", None)
+    for t, (name, dtype, dims) in zip(tensors, _MOE_TENSORS):
+        _need(t, dtype, name)
+        if t.dim() != dims or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dims}-D tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    (T, H), (E, two_i, _), k = xq.shape, w13.shape, ids.shape[1]
+    I = two_i // 2
+    if xs.shape != (T,) or ids.shape != (T, k) or weights.shape != (T, k):
+        raise ValueError("xs must be [T], ids and weights [T, k]")
+    if two_i % 2 or w13.shape != (E, 2 * I, H) or s13.shape != (E, 2 * I) or w2.shape != (E, H, I) or s2.shape != (E, H):
+        raise ValueError("w13 must be [E, 2 I, H], s13 [E, 2 I], w2 [E, H, I] and s2 [E, H]")
+    act = _activation(activation)
+    if out is None:
+        y = torch.empty((T, H), dtype=out_dtype, device=device)
+    else:
+        y = out
+        _check_out(y, "out", (T, H), getattr(y, "dtype", None), device, row_stride_ok=True)
+    dt = _x_dtype8(y, "out")
+    held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_moe_workspace", T, k, E, H, I), device)
+    _call8("w8a8_moe", device, xq.data_ptr(), xs.data_ptr(), ids.data_ptr(), weights.data_ptr(), T, k, w13.data_ptr(),
+           s13.data_ptr(), w2.data_ptr(), s2.data_ptr(), E, H, I, act, wptr, wbytes, y.data_ptr(), dt,
+           y.stride(0) if T > 1 else max(H, 1))
+    return y
+
+
 # ------------------------------------------------------ INT8 key/value cache
 
 def kv8_new_cache(num_pages: int, heads: int, page: int, dim: int, device="cuda"):
