@@ -255,6 +255,16 @@ def test_act_model_shapes(M, N, K, gated):
     act_case(M, N, K, "silu" if gated else None, gated, False, not gated, torch.bfloat16, seed=1)
 
 
+@pytest.mark.parametrize("M,N,K,gated", [(1030, 8192, 512, True), (4100, 8192, 512, False), (2052, 8192, 1024, False)])
+def test_act_tokens_past_a_multiple_of_256(M, N, K, gated):
+    """The last tokens take a launch of their own."""
+    import torch
+    x, q, s, wq, ws, b, r, y = act_case(M, N, K, "gelu", gated, True, True, torch.bfloat16, seed=2)
+    m = M - 20
+    assert torch.equal(y[m:], ops().w8a8_gemm_act(q[m:].contiguous(), s[m:].contiguous(), wq, ws, bias=b, activation="gelu",
+                                                  gated=gated, residual=r[m:], out_dtype=torch.bfloat16))
+
+
 def test_act_without_an_epilogue_is_the_gemm():
     import torch
     for M, N, K in [(3, 96, 256), (70, 512, 1024), (300, 72, 336), (300, 71, 336)]:

@@ -134,17 +134,25 @@ struct MoeParams {
   int64_t ldy;
 };
 
-constexpr int kResLd = 20;         // ints per row of sums: the four row groups of a wave on their own banks
 constexpr size_t kLds = 64 * 1024;
 
-__host__ __device__ constexpr int max_entries(int P, int E, int RT) { return (P < E ? P : E) + P / (16 * RT); }
-__host__ __device__ constexpr int code_ld(int K, int CH) { return (K + 64 * CH - 1) / (64 * CH) * (64 * CH) + 16; }
+// Ints per row of sums: the four row groups of a wave on their own banks.
+__host__ __device__ constexpr int sums_ld(int channels) { return channels + 4; }
+
+__host__ __device__ constexpr int max_entries(int P, int E, int rows) { return (P < E ? P : E) + P / rows; }
+__host__ __device__ constexpr int code_ld(int K, int span) { return (K + span - 1) / span * span + 16; }
 
 // LDS: sums, ids, counts / first positions, entries, pairs by position and back.
-inline size_t moe_lds(int P, int E, int RT) {
-  return (size_t)P * kResLd * 4 + P * 4 + E * 4 + (max_entries(P, E, RT) + 1) * 8 + ((P + 1) / 2) * 8 + 32;
+inline size_t moe_lds(int P, int E, int rows, int channels) {
+  return (size_t)P * sums_ld(channels) * 4 + P * 4 + E * 4 + (max_entries(P, E, rows) + 1) * 8 + ((P + 1) / 2) * 8 + 32;
 }
-inline size_t fused_lds(int P, int K, int CH) { return (size_t)P * code_ld(K, CH) + P * 4 + 16; }
+inline size_t fused_lds(int P, int K, int span) { return (size_t)P * code_ld(K, span) + P * 4 + 16; }
+
+// Another lane's value, 0 where there is none or the row is not in MASK.
+template <int CTRL, int MASK>
+__device__ __forceinline__ uint32_t dpp_from(uint32_t v) {
+  return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, MASK, 0xF, false);
+}
 
 // The INT8 codes of a row of fp32 values by one wave, and its scale.
 __device__ __forceinline__ float quantize_row(const float* __restrict__ h, int K, int lane, int8_t* codes) {
@@ -190,55 +198,68 @@ __device__ __forceinline__ float quantize_row(const float* __restrict__ h, int K
   return s;
 }
 
-// A workgroup owns 16 channels (UP: 8 gates and their 8 values) of every expert, or of
-// a share of the experts that the tokens chose (UP, blockIdx.y). It sorts the pairs
-// by expert; an entry is up to 16 RT rows of one expert, and the entries' chunks of CH
-// 64-k steps are dealt to the waves in contiguous runs of equal length, whatever
-// experts they fall in. A wave streams the weights of its chunks from memory
-// straight into v_mfma_i32_16x16x64_i8, the next chunk's in flight, and adds an
-// entry's int32 sums to those in LDS (exact in any order).
+// A workgroup owns CN channels (UP: CN / 2 gates and their values) of every expert, or
+// of a share of the experts that the tokens chose (UP, blockIdx.y). It sorts the pairs
+// by expert; an entry is up to ROWS rows of one expert, and the entries' chunks of CH
+// k-steps are dealt to the waves in contiguous runs of equal length, whatever experts
+// they fall in. A wave streams the weights of its chunks from memory straight into
+// v_mfma_i32_16x16x64_i8, the next two chunks in flight, and adds an entry's int32
+// sums to those in LDS (exact in any order).
+//
+// HALF: blocks of 8 rows and 8 channels that use both halves of the instruction's 16, the
+// upper ones for the next 64 of k: rows r and r + 8 hold the same token, columns c and
+// c + 8 the same channel, so D[r][c] + D[r + 8][c + 8] is the sum. A load then covers 8
+// whole 128-byte lines, and there are twice the workgroups.
+//
 // FUSED: h is quantized here, into LDS, by every workgroup.
+//
+// Bound by what a CU can have on its way from L2, weights and rows together (6.5 TB/s over
+// the chip): 64 tokens, 8 of 64 experts of 4096 x 1376, 1.04 GB of weights: 240 us, 4.4 TB/s;
+// 13 tokens, 4 of 32 of 3584 x 2368, 0.52 GB: 115 us, 4.6 TB/s; one token, 8 of 64 of 2048
+// x 1024, 50 MB: 19 us, of which 7 are two launches without any expert. More in
+// flight (chunks twice as long) was slower (16 rows: 119 -> 140 us, the 32 experts),
+// as were non-temporal loads (127 -> 135).
 enum { UP = 0, DOWN = 1 };
-template <int STAGE, int RT, int CH, int NW, bool FUSED>
+template <int STAGE, bool HALF, int RT, int CH, int CB, int NW, bool FUSED>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
-  constexpr int NT = 64 * NW;
+  constexpr int NT = 64 * NW, RB = HALF ? 8 : 16, CN = RB * CB, ROWS = RB * RT, LD = sums_ld(CN);
+  constexpr int KS = HALF ? 128 : 64, SPAN = KS * CH;
   static_assert(kMoeMaxPairs <= NT && kMoeMaxExperts <= NT, "one a thread");
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint32_t wave_total[NW];
-  int* const sums = reinterpret_cast<int*>(lds);                     // [P][kResLd]
-  int* const id_of = sums + p.P * kResLd;                            // [P]
+  int* const sums = reinterpret_cast<int*>(lds);                     // [P][LD]
+  int* const id_of = sums + p.P * LD;                                // [P]
   int* const first = id_of + p.P;                                    // [E] counts, then first positions
-  int2* const entry = reinterpret_cast<int2*>(lds + ((p.P * (kResLd + 1) + p.E) * 4 + 7) / 8 * 8);
-  uint16_t* const pair_of = reinterpret_cast<uint16_t*>(entry + max_entries(p.P, p.E, RT) + 1);
+  int2* const entry = reinterpret_cast<int2*>(lds + ((p.P * (LD + 1) + p.E) * 4 + 7) / 8 * 8);
+  uint16_t* const pair_of = reinterpret_cast<uint16_t*>(entry + max_entries(p.P, p.E, ROWS) + 1);
   uint16_t* const pos_of = pair_of + (p.P + 1) / 2 * 2;
   int8_t* const codes = reinterpret_cast<int8_t*>(lds) + ((reinterpret_cast<uint8_t*>(pos_of + p.P) - lds) + 15) / 16 * 16;
-  const int cld = FUSED ? code_ld(p.K, CH) : 0;
+  const int cld = FUSED ? code_ld(p.K, SPAN) : 0;
   float* const hs = reinterpret_cast<float*>(codes + p.P * cld);     // [P], FUSED
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int c = lane & 15, g = lane >> 4;
-  const int n0 = (int)blockIdx.x * 16;
+  const int cr = HALF ? c & 7 : c, kl = (HALF ? 64 * (c >> 3) : 0) + 16 * g;
+  const int n0 = (int)blockIdx.x * CN, rows_w = min(CN, p.N - n0);
 
-  // The pairs by expert.
+  // The pairs by expert, one a thread (P <= kMoeMaxPairs <= NT, E <= kMoeMaxExperts <= NT).
+  int my_id = tid < p.P ? p.ids[tid] : -1, my_rank = 0;
+  my_id = my_id >= 0 && my_id < p.E ? my_id : -1;
   for (int i = tid; i < p.E; i += NT) first[i] = 0;
-  for (int i = tid; i < p.P * kResLd; i += NT) sums[i] = 0;
+  for (int i = tid; i < p.P * LD; i += NT) sums[i] = 0;
   __syncthreads();
-  int my_id = -1, my_rank = 0;                                       // P <= kMoeMaxPairs <= NT: one pair a thread
-  if (tid < p.P) {
-    my_id = p.ids[tid];
-    my_id = my_id >= 0 && my_id < p.E ? my_id : -1;
-    id_of[tid] = my_id;
-    if (my_id >= 0) my_rank = atomicAdd(&first[my_id], 1);
-  }
+  if (tid < p.P) id_of[tid] = my_id;
+  if (my_id >= 0) my_rank = atomicAdd(&first[my_id], 1);
   __syncthreads();
-  const int count = tid < p.E ? first[tid] : 0;                      // E <= kMoeMaxExperts <= NT
-  const uint32_t own = (uint32_t)((count + 16 * RT - 1) / (16 * RT)) << 16 | (uint32_t)count;
+  const int count = tid < p.E ? first[tid] : 0;
+  const uint32_t own = (uint32_t)((count + ROWS - 1) / ROWS) << 16 | (uint32_t)count;
   uint32_t upto = own;                                               // entries << 16 | positions, up to this expert
-#pragma unroll
-  for (int d = 1; d < 64; d *= 2) {
-    const uint32_t o = (uint32_t)__shfl_up((int)upto, d);
-    if (lane >= d) upto += o;
-  }
+  upto += dpp_from<0x111, 0xF>(upto);                                // row_shr:1, 2, 4, 8: sums within rows of 16
+  upto += dpp_from<0x112, 0xF>(upto);
+  upto += dpp_from<0x114, 0xF>(upto);
+  upto += dpp_from<0x118, 0xF>(upto);
+  upto += dpp_from<0x142, 0xA>(upto);                                // row_bcast:15 into rows 1 and 3
+  upto += dpp_from<0x143, 0xC>(upto);                                // row_bcast:31 into rows 2 and 3
   if (lane == 63) wave_total[wave] = upto;
   __syncthreads();
   uint32_t all = 0, before = upto - own;
@@ -249,8 +270,8 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
   }
   if (tid < p.E) {
     first[tid] = (int)(before & 0xFFFFu);
-    for (int i = 0; 16 * RT * i < count; ++i)
-      entry[(before >> 16) + i] = int2{tid | min(16 * RT, count - 16 * RT * i) << 16, (int)(before & 0xFFFFu) + 16 * RT * i};
+    for (int i = 0; ROWS * i < count; ++i)
+      entry[(before >> 16) + i] = int2{tid | min(ROWS, count - ROWS * i) << 16, (int)(before & 0xFFFFu) + ROWS * i};
   }
   const int entries = __builtin_amdgcn_readfirstlane((int)(all >> 16)), positions = (int)(all & 0xFFFFu);
   if (tid == 0) entry[entries] = int2{0, positions};
@@ -270,11 +291,11 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
     return __builtin_amdgcn_readfirstlane(e);
   };
   const int ent0 = whole(entries * share / shares), ent1 = whole(entries * (share + 1) / shares);
-  const int nch = (p.K + 64 * CH - 1) / (64 * CH);
+  const int nch = (p.K + SPAN - 1) / SPAN;
   const int chunks = (ent1 - ent0) * nch;
   const int ch0 = (int)((int64_t)chunks * wave / NW), ch1 = (int)((int64_t)chunks * (wave + 1) / NW);
   struct Buf {
-    v4i w[CH];
+    v4i w[CH][CB];
     v4i a[FUSED ? 1 : RT][FUSED ? 1 : CH];
   };
   // rows of an entry that this lane supplies (dropped ones past its end)
@@ -285,17 +306,18 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
   const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, FUSED ? 0 : (STAGE == UP ? p.T : p.P) * p.K);
   int l_ent = ent0 + (chunks ? ch0 / nch : 0), l_ch = chunks ? ch0 % nch : 0, l_at = ch0;
   __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w, 0);
-  int off_a[RT];
+  int off_a[RT], l_n = 0;
   auto enter_load = [&]() {
     const int2 v = entry_at(l_ent);
     const int e = v.x & 0xFFFF, n = v.x >> 16;
-    rW = buffer_rsrc(p.w + ((int64_t)e * p.N + n0) * p.K, 16 * p.K);
+    l_n = n;
+    rW = buffer_rsrc(p.w + ((int64_t)e * p.N + n0) * p.K, rows_w * p.K);
     if constexpr (!FUSED) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const int row = 16 * r + c;
+        const int row = RB * r + cr;
         const int pair = pair_of[v.y + min(row, n - 1)];
-        off_a[r] = row < n ? (STAGE == UP ? pair / p.k : pair) * p.K + 16 * g : kDroppedOffset;
+        off_a[r] = row < n ? (STAGE == UP ? pair / p.k : pair) * p.K + kl : kDroppedOffset;
       }
     }
   };
@@ -310,13 +332,23 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
     }
 #pragma unroll
     for (int u = 0; u < CH; ++u) {
-      const int k0 = 64 * (l_ch * CH + u);
-      const int out = l_at < ch1 && k0 + 16 * g < p.K ? 0 : kDroppedOffset;
-      b.w[u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, (c * p.K + 16 * g) | out, k0, 0));
-      if constexpr (!FUSED) {
+      const int k0 = KS * (l_ch * CH + u);
+      const int out = l_at < ch1 && k0 + kl < p.K ? 0 : kDroppedOffset;
 #pragma unroll
-        for (int r = 0; r < RT; ++r)
+      for (int cb = 0; cb < CB; ++cb)
+        b.w[u][cb] = __builtin_bit_cast(
+            v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, ((RB * cb + cr) * p.K + kl) | out, k0, 0));
+    }
+    if constexpr (!FUSED) {
+#pragma unroll
+      for (int r = 0; r < RT; ++r) {
+        if (r > 0 && l_n <= RB * r) break;             // a block of rows that the entry does not have
+#pragma unroll
+        for (int u = 0; u < CH; ++u) {
+          const int k0 = KS * (l_ch * CH + u);
+          const int out = l_at < ch1 && k0 + kl < p.K ? 0 : kDroppedOffset;
           b.a[r][u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, off_a[r] | out, k0, 0));
+        }
       }
     }
     ++l_ch;
@@ -338,27 +370,30 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
   int c_ent = l_ent, c_ch = chunks ? ch0 % nch : 0, c_n = 0, c_pos = 0;
   if (ch0 < ch1) c_ent = ent0 + ch0 / nch;
   const int8_t* row_a[RT];
-  v4i acc[RT];
+  v4i acc[RT][CB];
   auto enter = [&]() {
     const int2 v = entry_at(c_ent);
     c_n = v.x >> 16;
     c_pos = v.y;
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      acc[r] = v4i{0, 0, 0, 0};
-      if constexpr (FUSED) row_a[r] = codes + pair_of[c_pos + min(16 * r + c, c_n - 1)] * cld + 16 * g;
+#pragma unroll
+      for (int cb = 0; cb < CB; ++cb) acc[r][cb] = v4i{0, 0, 0, 0};
+      if constexpr (FUSED) row_a[r] = codes + pair_of[c_pos + min(RB * r + cr, c_n - 1)] * cld + kl;
     }
   };
   auto consume = [&](const Buf& b) {
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
-      if (16 * r >= c_n) break;
+      if (RB * r >= c_n) break;
 #pragma unroll
       for (int u = 0; u < CH; ++u) {
         v4i a;
-        if constexpr (FUSED) a = *reinterpret_cast<const v4i*>(row_a[r] + 64 * (c_ch * CH + u));
+        if constexpr (FUSED) a = *reinterpret_cast<const v4i*>(row_a[r] + KS * (c_ch * CH + u));
         else a = b.a[r][u];
-        acc[r] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b.w[u], acc[r], 0, 0, 0);
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          acc[r][cb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b.w[u][cb], acc[r][cb], 0, 0, 0);
       }
     }
     if (++c_ch == nch) {
@@ -372,8 +407,10 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
     for (int r = 0; r < RT; ++r) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = 16 * r + 4 * g + i;
-        if (row < c_n) atomicAdd(&sums[(c_pos + row) * kResLd + c], acc[r][i]);
+        const int row = RB * r + 4 * (HALF ? g & 1 : g) + i;
+#pragma unroll
+        for (int cb = 0; cb < CB; ++cb)
+          if (row < c_n && (!HALF || c >> 3 == g >> 1)) atomicAdd(&sums[(c_pos + row) * LD + RB * cb + cr], acc[r][cb][i]);
       }
     }
   };
@@ -401,24 +438,26 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
 
   if constexpr (STAGE == UP) {
     const int pos0 = entry[ent0].y, pos1 = entry[ent1].y, I = p.N >> 1;
-    for (int o = tid; o < (pos1 - pos0) * 8; o += NT) {
-      const int pos = pos0 + (o >> 3), i = o & 7;
+    for (int o = tid; o < (pos1 - pos0) * (CN / 2); o += NT) {
+      const int pos = pos0 + o / (CN / 2), i = o % (CN / 2);
+      if (2 * i >= rows_w) continue;
       const int pair = pair_of[pos];
       const float sa = p.sa[pair / p.k];
       const float* sw = p.sw + (int64_t)id_of[pair] * p.N + n0 + 2 * i;
-      const float gate = (float)sums[pos * kResLd + 2 * i] * (sa * sw[0]);
-      const float up = (float)sums[pos * kResLd + 2 * i + 1] * (sa * sw[1]);
+      const float gate = (float)sums[pos * LD + 2 * i] * (sa * sw[0]);
+      const float up = (float)sums[pos * LD + 2 * i + 1] * (sa * sw[1]);
       p.h_out[(int64_t)pair * I + (n0 >> 1) + i] = activate(p.act, gate) * up;
     }
   } else {
-    for (int o = tid; o < p.T * 16; o += NT) {
-      const int t = o >> 4, n = o & 15;
+    for (int o = tid; o < p.T * CN; o += NT) {
+      const int t = o / CN, n = o % CN;
+      if (n >= rows_w) continue;
       float sum = 0.0f;
 #pragma unroll 4
       for (int j = 0; j < p.k; ++j) {
         const int pair = t * p.k + j, e = id_of[pair];
         const float s = (FUSED ? hs[pair] : p.sa[pair]) * p.sw[(int64_t)max(e, 0) * p.N + n0 + n];
-        const float v = (float)sums[(e < 0 ? 0 : pos_of[pair]) * kResLd + n] * s;
+        const float v = (float)sums[(e < 0 ? 0 : pos_of[pair]) * LD + n] * s;
         const float f = p.weights[pair];
         sum = e < 0 ? sum : fmaf(f, v, sum);
       }
@@ -441,18 +480,23 @@ __global__ __launch_bounds__(256) void k_moe_quant(const float* __restrict__ h, 
 
 int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
 
+// Stage 0 (UP) or 1 (DOWN) of a layer whose experts have few rows, or more.
 template <int STAGE, bool FUSED>
-void launch_stage(const MoeParams& p, int shares, int rt, hipStream_t stream) {
-  const dim3 grid((unsigned)(p.N / 16), (unsigned)shares);
-#define MOE_STAGE(RT, CH, NW)                                                                                  \
-  {                                                                                                            \
-    const size_t lds = moe_lds(p.P, p.E, RT) + (FUSED ? fused_lds(p.P, p.K, CH) : 0);                          \
-    hipLaunchKernelGGL((k_w8a8_moe<STAGE, RT, CH, NW, FUSED>), grid, dim3(64 * NW), (unsigned)lds, stream, p); \
+void launch_stage(const MoeParams& p, int shares, bool few_rows, hipStream_t stream) {
+#define MOE_STAGE(HALF, RT, CH, CB, NW)                                                                                \
+  {                                                                                                                    \
+    constexpr int RB = HALF ? 8 : 16, SPAN = (HALF ? 128 : 64) * CH;                                                   \
+    const dim3 grid((unsigned)((p.N + RB * CB - 1) / (RB * CB)), (unsigned)shares);                                    \
+    const size_t lds = moe_lds(p.P, p.E, RB * RT, RB * CB) + (FUSED ? fused_lds(p.P, p.K, SPAN) : 0);                  \
+    hipLaunchKernelGGL((k_w8a8_moe<STAGE, HALF, RT, CH, CB, NW, FUSED>), grid, dim3(64 * NW), (unsigned)lds, stream, p); \
+    return;                                                                                                            \
   }
-  if constexpr (FUSED) MOE_STAGE(1, 4, 16)
-  else if (rt == 1) MOE_STAGE(1, 4, (STAGE == UP ? 8 : 16))
-  else if (rt == 2) MOE_STAGE(2, 2, (STAGE == UP ? 8 : 16))
-  else MOE_STAGE(4, 2, 8)
+  if constexpr (FUSED) {
+    MOE_STAGE(true, 1, 2, 1, 16)
+  } else {
+    if (few_rows) MOE_STAGE(true, 1, (STAGE == UP ? 1 : 2), (STAGE == UP ? 2 : 1), 8)
+    MOE_STAGE(false, 2, 2, (STAGE == UP ? 2 : 1), 8)
+  }
 #undef MOE_STAGE
 }
 
@@ -490,28 +534,40 @@ void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream) {
   p.weights = a.weights;
   p.T = a.T; p.k = a.k; p.P = P; p.E = a.E;
   p.act = a.act;
-  // rows an entry holds: an expert has at most T (or repeats), P / E on average
-  const int rt = a.T <= 16 ? 1 : a.T <= 32 || P <= 12 * a.E ? 2 : 4;
+  // Tiles of 8 channels and 8 rows where an expert has few, of 16 channels and 32 rows
+  // where it has more and their codes weigh beside the weights (us; T, H, I, E, k): 4,
+  // 2048, 1024, 64, 8 42.3 and 50.5; 8, the same 55.8 and 66.9; 16, the same 67.3 and
+  // 79.3; 16, 2048, 1024, 16, 8 40.8 and 38.3; 32, 4096, 1376, 16, 4 92.3 and 72.6; 64, 4096, 1376, 64,
+  // 8 310 and 240. 16 and 64 rows were between or slower everywhere.
+  const bool few_rows = a.T <= 8 || P <= 4 * a.E;
 
   p.a = a.xq; p.sa = a.xs;
   p.w = a.w13; p.sw = a.s13;
   p.K = a.H; p.N = 2 * a.I;
   p.h_out = h;
-  const int tiles = p.N / 16, used = std::min(P, a.E);
-  const int shares = std::max(1, std::min(used, 512 / tiles));
-  launch_stage<UP, false>(p, shares, rt, stream);
+  // Shares of the experts, so that a workgroup streams some 128 KiB of weights: enough
+  // of them to fill the chip with few experts, and to end evenly with many (8 of 64 experts of
+  // 2048 x 1024 for one token: both stages 20.6 us with 256 workgroups, 21.3 with 1024; 32 of 3584 x
+  // 2368 for 13: 145 with 296, 115 with 2072).
+  const int used = std::min(P, a.E);
+  const int64_t target = std::min<int64_t>(2048, (int64_t)used * p.N * p.K >> 17);
+  const int shares = (int)std::max<int64_t>(1, std::min<int64_t>(used, target * 16 / p.N));
+  launch_stage<UP, false>(p, shares, few_rows, stream);
 
   p.K = a.I; p.N = a.H;
   p.w = a.w2; p.sw = a.s2;
   p.y = a.y; p.ydtype = a.ydtype; p.ldy = a.ldy;
-  if (a.T <= 16 && (int64_t)P * a.I <= 32768 && moe_lds(P, a.E, 1) + fused_lds(P, a.I, 4) <= kLds) {
+  // Every workgroup of the second stage quantizes h itself up to 16384 values; above, a
+  // launch does (T, I, k with H = 2048: 1, 1024, 8 19.1 us in two launches, 21 in
+  // three; 16, 1024, 2 21.2 and 20.5; 4, 1024, 8 41.1 and 40.3).
+  if (few_rows && (int64_t)P * a.I <= 16384 && moe_lds(P, a.E, 8, 8) + fused_lds(P, a.I, 256) <= kLds) {
     p.h = h;
-    launch_stage<DOWN, true>(p, 1, 1, stream);
+    launch_stage<DOWN, true>(p, 1, true, stream);
     return;
   }
   hipLaunchKernelGGL(k_moe_quant, dim3((unsigned)((P + 3) / 4)), dim3(256), 0, stream, h, a.ids, a.E, P, a.I, codes, hs);
   p.a = codes; p.sa = hs;
-  launch_stage<DOWN, false>(p, 1, rt, stream);
+  launch_stage<DOWN, false>(p, 1, few_rows, stream);
 }
 
 }  // namespace w4a4

@@ -11,8 +11,10 @@ bool w8a8_wide_rows(int64_t outs, const void* y, int64_t ldy, const void* residu
 }
 
 int64_t w8a8_act_workspace(int64_t M, int64_t N, int64_t K, bool wide) {
-  const W8Plan pl = plan_act(M, N, K, wide);
-  return sums_in_workspace(pl, wide) ? (int64_t)pl.splits * M * N * 4 : 0;
+  const ActPlan a = plan_act(M, N, K, wide);
+  auto sums = [&](int64_t m, const W8Plan& pl) { return sums_in_workspace(pl, wide) ? (int64_t)pl.splits * m * N * 4 : 0; };
+  const int64_t n = a.first == M ? sums(M, a.plan) : std::max(sums(a.first, a.plan), sums(M - a.first, a.rest));
+  return wide ? n : std::max(n, w8a8_act_workspace(M, N, K, true));   // never less for other rows
 }
 
 void launch_w8a8_gemm_act(const W8GemmArgs& g, const W8Epilogue& e, hipStream_t stream) {

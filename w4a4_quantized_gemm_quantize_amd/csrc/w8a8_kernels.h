@@ -627,36 +627,34 @@ void k_w8a8_gemm_tiles(W8Params p) {
 //
 // Above 16 tokens, the tile whose estimated time is least: rounds of tiles over
 // the CUs times (stages x the tile's time per 128-k stage + its start and
-// output). The times (us: 256 x 256 tiles 1.15 a stage, 256 x 128 0.8, 128 x 128
-// 0.5) are fitted to measured shapes, tokens x channels x K, among them those named
-// here, where the choice is the fastest; us of the three in turn: 4096 x 4096 x 4096 62.6, 70.7, 80.9; 1024 x 8192 x 28672 229, 224,
-// 290; 512 x 8192 x 8192 74, 55.2, 43.4. 128 x 128 tiles may also split K, which
-// costs a launch and 8 bytes per output and range through the caches (64 x 8192
-// x 8192: 35.6 us whole, 25.5 in two ranges, 21.2 in four; 512 x 4096 x 11008:
-// 53.8, 41.7, 50.1; 256 x 11008 x 4096: 24.1, 41.5, 44.7).
+// output). The times (us: 256 x 256 tiles 1.6 a stage, 256 x 128 0.95, 128 x 128
+// 0.55) are fitted to measured shapes, tokens x channels x K, among them those named
+// here, where the choice is the fastest; us of the three in turn: 4096 x 4096 x 4096
+// 62.6, 70.7, 80.9; 1024 x 8192 x 28672 229, 224, 290; 512 x 8192 x 8192 74, 55.2,
+// 43.4; 777 x 18944 x 3584 96.3, 84.2, 84.9; 2048 x 4096 x 11008 121, 88, 109. 128 x
+// 128 tiles may also split K, which costs a launch and 8 bytes per output and range
+// through the caches (64 x 8192 x 8192: 35.6 us whole, 25.5 in two ranges, 21.2 in
+// four; 512 x 4096 x 11008: 53.8, 41.7, 50.1; 256 x 11008 x 4096: 24.1, 41.5, 44.7).
 enum { TILE_SMALL = 0, TILE_256 = 1, TILE_256_128 = 2, TILE_128 = 3 };
 struct W8Plan {
   int tile, splits;
+  double us;              // the estimate
 };
 W8Plan plan_w8a8(int64_t M, int64_t N, int64_t K) {
-  if (M <= 8 || (M <= 16 && N * K <= (int64_t{1} << 26))) return W8Plan{TILE_SMALL, 1};
+  if (M <= 8 || (M <= 16 && N * K <= (int64_t{1} << 26))) return W8Plan{TILE_SMALL, 1, 4.0 + N * K / 5.2e6};
   const int64_t nk = (K + 127) / 128;
-  W8Plan best{TILE_256, 1};
-  double best_us = 1e30;
+  W8Plan best{TILE_256, 1, 1e30};
   auto consider = [&](int tile, int64_t bm, int64_t bn, double stage, double start, int splits) {
     const int64_t tiles = ((M + bm - 1) / bm) * ((N + bn - 1) / bn);
     const int64_t rounds = (tiles * splits + kCUs - 1) / kCUs;
     double us = rounds * (((nk + splits - 1) / splits) * stage + start);
     if (splits > 1) us += 4.0 + 8.0 * splits * M * N / 2.5e6;
-    if (us < best_us) {
-      best_us = us;
-      best = W8Plan{tile, splits};
-    }
+    if (us < best.us) best = W8Plan{tile, splits, us};
   };
-  consider(TILE_256, 256, 256, 1.15, 3.0, 1);
-  consider(TILE_256_128, 256, 128, 0.8, 2.5, 1);
+  consider(TILE_256, 256, 256, 1.6, 4.0, 1);
+  consider(TILE_256_128, 256, 128, 0.95, 3.0, 1);
   for (int splits = 1; splits <= 16 && splits * 2 <= nk; splits *= 2)
-    consider(TILE_128, 128, 128, 0.5, 2.0, splits);
+    consider(TILE_128, 128, 128, 0.55, 2.5, splits);
   return best;
 }
 

@@ -480,6 +480,7 @@ def nvfp4_scales_to_rows(s: torch.Tensor, rows: int, K: int):
 # ------------------------------------------------------- 8-bit linear layers
 
 _DTYPE8 = {torch.float32: Y_F32, torch.float16: Y_F16, torch.bfloat16: Y_BF16}
+_I8, _F32, _I32 = torch.int8, torch.float32, torch.int32
 
 
 def _x_dtype8(t, name: str) -> int:
@@ -655,6 +656,12 @@ def _activation(name) -> int:
 
 def _need_rows(t, name: str, shape, dtype, device) -> int:
     """Row stride of a checked 2-D operand of contiguous rows."""
+    try:                                               # the checks of _check_out, at a third of its time
+        rows, one = t.stride()
+        if t.dtype is dtype and t.shape == shape and one == 1 and rows >= shape[1] and t.device == device:
+            return rows if shape[0] > 1 else max(shape[1], 1)
+    except (AttributeError, TypeError, ValueError):    # not a 2-D tensor
+        pass
     _check_out(t, name, shape, dtype, device, row_stride_ok=True)
     return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
 
@@ -671,36 +678,45 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
     be ``x`` or ``residual`` itself (in place). Rows that are not finite have NaN scales."""
     dt = _x_dtype8(x, "x")
     ldx = _rows_stride(x, "x")
-    M, K = x.shape
-    device, dtype = x.device, x.dtype
-    if not isinstance(weight, torch.Tensor) or weight.dtype not in (torch.float32, dtype):
+    shape, device, dtype = x.shape, x.device, x.dtype
+    M, K = shape
+    if not isinstance(weight, torch.Tensor) or (weight.dtype is not torch.float32 and weight.dtype is not dtype):
         raise TypeError(f"weight must be a torch.float32 or {dtype} tensor")
     if weight.shape != (K,) or not weight.is_contiguous() or weight.device != device:
         raise ValueError(f"weight must be a contiguous [{K}] tensor on {device}")
     if not 0.0 < eps < float("inf"):
         raise ValueError("eps must be positive and finite")
-    ldr = 0 if residual is None else _need_rows(residual, "residual", (M, K), dtype, device)
-    count = 2 + (residual is not None) + bool(return_normed)
+    r = ldr = h = ldh = y = ldy = 0
+    if residual is not None:
+        ldr = _need_rows(residual, "residual", shape, dtype, device)
+        r = residual.data_ptr()
     if out is None:
-        out = (torch.empty((M, K), dtype=torch.int8, device=device),
-               torch.empty((M,), dtype=torch.float32, device=device))
-        for _ in range(count - 2):
-            out += (torch.empty((M, K), dtype=dtype, device=device),)
+        new = x.new_empty
+        xq, xs = new(shape, dtype=torch.int8), new((M,), dtype=torch.float32)
+        out = xq, xs
+        if r:
+            ldh = max(K, 1)
+            out += (new(shape),)
+            h = out[2].data_ptr()
+        if return_normed:
+            ldy = max(K, 1)
+            out += (new(shape),)
+            y = out[-1].data_ptr()
     else:
         out = tuple(out)
-        if len(out) != count:
-            raise ValueError(f"out must hold {count} tensors")
-        _check_out(out[0], "xq", (M, K), torch.int8, device)
-        _check_out(out[1], "xs", (M,), torch.float32, device)
-    h = ldh = y = ldy = 0
-    if residual is not None:
-        ldh = _need_rows(out[2], "h", (M, K), dtype, device)
-        h = out[2].data_ptr()
-    if return_normed:
-        ldy = _need_rows(out[-1], "normed", (M, K), dtype, device)
-        y = out[-1].data_ptr()
-    _call8("w8a8_rmsnorm_quantize", device, x.data_ptr(), dt, ldx, 0 if residual is None else residual.data_ptr(), ldr,
-           weight.data_ptr(), _DTYPE8[weight.dtype], eps, M, K, out[0].data_ptr(), out[1].data_ptr(), h, ldh, y, ldy)
+        if len(out) != 2 + (residual is not None) + bool(return_normed):
+            raise ValueError(f"out must hold {2 + (residual is not None) + bool(return_normed)} tensors")
+        xq, xs = out[:2]
+        _check_out(xq, "xq", shape, torch.int8, device)
+        _check_out(xs, "xs", (M,), torch.float32, device)
+        if residual is not None:
+            ldh = _need_rows(out[2], "h", shape, dtype, device)
+            h = out[2].data_ptr()
+        if return_normed:
+            ldy = _need_rows(out[-1], "normed", shape, dtype, device)
+            y = out[-1].data_ptr()
+    _call8("w8a8_rmsnorm_quantize", device, x.data_ptr(), dt, ldx, r, ldr, weight.data_ptr(), _DTYPE8[weight.dtype], eps,
+           M, K, xq.data_ptr(), xs.data_ptr(), h, ldh, y, ldy)
     return out
 
 
@@ -815,6 +831,17 @@ _MOE_TENSORS = (("xq", torch.int8, 2), ("xs", torch.float32, 1), ("ids", torch.i
                 ("w13", torch.int8, 3), ("s13", torch.float32, 2), ("w2", torch.int8, 3), ("s2", torch.float32, 2))
 
 
+def _moe_refuse(tensors):
+    """Raises for the first of w8a8_moe's operands that a kernel cannot take."""
+    device = next((t.device for t in tensors if isinstance(t, torch.Tensor)), None)
+    for t, (name, dtype, dims) in zip(tensors, _MOE_TENSORS):
+        _need(t, dtype, name)
+        if t.dim() != dims or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dims}-D tensor")
+        if t.device != device:
+            raise ValueError(f"{name} is on {t.device}, expected {device}")
+
+
 def w8a8_moe(xq, xs, ids, weights, w13, s13, w2, s2, activation="silu", out_dtype=torch.float16, out=None,
              workspace=None):
     """A mixture-of-experts layer of few tokens (T * k <= 512) on INT8 experts, in two
@@ -827,14 +854,20 @@ def w8a8_moe(xq, xs, ids, weights, w13, s13, w2, s2, activation="silu", out_dtyp
     :func:`moe_route`; ids that are no expert add nothing. ``w13`` int8 [E, 2 I, H], ``s13``
     float32 [E, 2 I]: from :func:`w8a8_pack_gated`; ``w2`` int8 [E, H, I], ``s2`` [E, H]: from
     :func:`w8a8_pack_weight`. Longer batches go in slices of tokens. Y is fp16 or bf16."""
-    tensors = (xq, xs, ids, weights, w13, s13, w2, s2)
-    device = getattr(xq, "device", None)
-    for t, (name, dtype, dims) in zip(tensors, _MOE_TENSORS):
-        _need(t, dtype, name)
-        if t.dim() != dims or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dims}-D tensor")
-        if t.device != device:
-            raise ValueError(f"{name} is on {t.device}, expected {device}")
+    try:                                               # the checks of _moe_refuse, at a third of its time
+        at = xq.get_device()
+        fine = (at >= 0 and xq.dtype is _I8 and xs.dtype is _F32 and ids.dtype is _I32 and weights.dtype is _F32 and
+                w13.dtype is _I8 and s13.dtype is _F32 and w2.dtype is _I8 and s2.dtype is _F32 and
+                at == xs.get_device() == ids.get_device() == weights.get_device() == w13.get_device() ==
+                s13.get_device() == w2.get_device() == s2.get_device() and
+                xq.is_contiguous() and xs.is_contiguous() and ids.is_contiguous() and weights.is_contiguous() and
+                w13.is_contiguous() and s13.is_contiguous() and w2.is_contiguous() and s2.is_contiguous() and
+                xq.dim() == ids.dim() == 2 and w13.dim() == 3)
+    except AttributeError:                             # not a tensor
+        fine = False
+    if not fine:
+        _moe_refuse((xq, xs, ids, weights, w13, s13, w2, s2))
+    device = xq.device
     (T, H), (E, two_i, _), k = xq.shape, w13.shape, ids.shape[1]
     I = two_i // 2
     if xs.shape != (T,) or ids.shape != (T, k) or weights.shape != (T, k):
@@ -842,6 +875,8 @@ def w8a8_moe(xq, xs, ids, weights, w13, s13, w2, s2, activation="silu", out_dtyp
     if two_i % 2 or w13.shape != (E, 2 * I, H) or s13.shape != (E, 2 * I) or w2.shape != (E, H, I) or s2.shape != (E, H):
         raise ValueError("w13 must be [E, 2 I, H], s13 [E, 2 I], w2 [E, H, I] and s2 [E, H]")
     act = _activation(activation)
+    if out_dtype is not torch.float16 and out_dtype is not torch.bfloat16:
+        raise TypeError("out_dtype must be torch.float16 or torch.bfloat16")
     if out is None:
         y = torch.empty((T, H), dtype=out_dtype, device=device)
     else:
@@ -873,7 +908,6 @@ def kv8_new_cache(num_pages: int, heads: int, page: int, dim: int, device="cuda"
 _KV_TENSORS = (("k_cache", torch.int8), ("v_cache", torch.int8), ("k_scale", torch.float32),
                ("v_scale", torch.float32), ("block_table", torch.int32), ("cu_seqlens", torch.int32),
                ("seq_lens", torch.int32))
-_I8, _F32, _I32 = torch.int8, torch.float32, torch.int32
 
 
 def _kv_refuse(tensors):
