@@ -58,7 +58,7 @@ w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx,
  *   N         outputs. wq, ws, bias hold N channels, or 2 N when gated: channel 2n
  *             is output n's gate, 2n + 1 what it multiplies
  *   residual  NULL or [M][ldr] of y_dtype; may be y itself (same pointer and stride),
- *             else must not overlap y
+ *             else must not overlap y (nor may the other inputs)
  *   xq, xs, wq, ws, bias, M, K, y, ldy: as for w8a8_gemm (channels < 2^24)
  *   workspace at least w8a8_gemm_act_workspace(M, N, K, gated, wide) bytes, 16-byte
  *             aligned, overwritten; may be NULL when that is 0
@@ -75,7 +75,8 @@ int64_t w8a8_gemm_act_workspace(int64_t M, int64_t N, int64_t K, int32_t gated, 
 
 /*
  * A W8A8 linear layer with an epilogue: w8a8_quantize_act of X, then w8a8_gemm_act
- * (few tokens: one launch without a workspace). Arguments as for those.
+ * (few tokens: one launch without a workspace). Arguments as for those; y must not
+ * overlap x.
  */
 w4a4_status_t w8a8_linear_act(const void* x, int32_t x_dtype, int64_t M, int64_t K, int64_t ldx,
                               const int8_t* wq, const float* ws, const float* bias, int32_t act, int32_t gated,
@@ -94,7 +95,7 @@ int64_t w8a8_linear_act_workspace(int64_t M, int64_t N, int64_t K, int32_t gated
  * the other ids are -1 and their weights 0. Plus infinity counts as the largest
  * finite value.
  *
- *   logits   [T][ldl] of dtype (any W4A4_Y_*), ldl >= E;  E <= 512, 0 < k <= 64, T < 2^28
+ *   logits   [T][ldl] of dtype (any W4A4_Y_*), ldl >= E;  E <= 512, 0 < k <= 64, T < 2^24
  *   ids      out: int32 [T][k];  weights  out: f32 [T][k]
  */
 w4a4_status_t moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ldl, int64_t k,

@@ -78,7 +78,7 @@ def test_act_workspace():
 def test_route_validation():
     def f(x=P, dt=F32, T=4, E=64, ld=64, k=8, ids=P, w=P):
         return _lib.status_of("moe_route", x, dt, T, E, ld, k, 1, ids, w, None)
-    assert f(dt=3) == E_DTYPE and f(T=-1) == E_SHAPE and f(T=1 << 28) == E_SHAPE
+    assert f(dt=3) == E_DTYPE and f(T=-1) == E_SHAPE and f(T=1 << 24) == E_SHAPE
     assert f(E=0) == E_SHAPE and f(E=513, ld=513) == E_SHAPE and f(ld=63) == E_SHAPE
     assert f(k=0) == E_SHAPE and f(k=65) == E_SHAPE
     assert f(x=None) == E_NULL and f(ids=None) == E_NULL and f(w=None) == E_NULL

@@ -412,7 +412,7 @@ w4a4_status_t w8a8_linear_act(const void* x, int32_t x_dtype, int64_t M, int64_t
 w4a4_status_t moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ldl, int64_t k,
                         int32_t renormalize, int32_t* ids, float* weights, void* stream) {
   if (!y_dtype_ok(dtype)) return W4A4_E_DTYPE;
-  if (T < 0 || T >= kMaxTokens || E <= 0 || E > w4a4::kMoeMaxExperts || ldl < E || k <= 0 || k > w4a4::kRouteMaxK)
+  if (T < 0 || T >= kMaxW8Rows || E <= 0 || E > w4a4::kMoeMaxExperts || ldl < E || k <= 0 || k > w4a4::kRouteMaxK)
     return W4A4_E_SHAPE;
   if (T == 0) return W4A4_OK;
   if (!logits || !ids || !weights) return W4A4_E_NULL;

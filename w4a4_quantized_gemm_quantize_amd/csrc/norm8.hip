@@ -12,6 +12,13 @@
 // because that is what the residual stream holds afterwards. Sums are fp32, 16
 // NC squares per lane and then a tree. A row with a NaN or an infinity (in h or
 // t) has scale NaN.
+//
+// Bound by HBM: 4096 x 8192 bf16 with a residual, 7 bytes per element, 47.7 us, 4.9 TB/s (a
+// copy by PyTorch 5.3); without, 3 bytes, 24 us, 4.2 TB/s (w8a8_quantize_act, which has no
+// weights to read, 20.7 in the same loop); one row of 4096 2.7 us, a launch. Tried: weights
+// kept in registers over several rows with the next row on its way 45.5 and 24.2 us, rows of
+// 28672 slower (24.1 -> 27.3), not kept; non-temporal stores 46.9 and 20.0, but what reads
+// the codes next pays more (the norm and a reader of the codes 122.8 -> 152.8).
 #include "device.h"
 #include "launch.h"
 #include "quant8.h"
@@ -51,6 +58,8 @@ __device__ __forceinline__ void weights16(const void* w, int i, float g[16]) {
     }
   }
 }
+
+constexpr int64_t kNormRows = int64_t{1} << 22;
 
 struct NormParams {
   const uint16_t* x;
@@ -255,9 +264,10 @@ void launch_norm(const NormParams& p, hipStream_t stream) {
 #define W8A8_NORM(NW, RPB, NC)                                                                       \
   hipLaunchKernelGGL((k_w8a8_rmsnorm<BF, W32, RES, NW, RPB, NC>), dim3((unsigned)((p.M + RPB - 1) / RPB)), \
                      dim3(64 * NW), 0, stream, p)
+  // waves a row, chunks a lane (4096 x 8192 with a residual: 2 waves 53.6 us, 4 51.4, 8 47.7)
   if (p.K <= 1024) W8A8_NORM(4, 4, 1);
   else if (p.K <= 4096) W8A8_NORM(4, 1, 1);
-  else if (p.K <= 8192) W8A8_NORM(4, 1, 2);
+  else if (p.K <= 8192) W8A8_NORM(8, 1, 1);
   else if (p.K <= 16384) W8A8_NORM(8, 1, 2);
   else if (p.K <= 32768) W8A8_NORM(8, 1, 4);
   else W8A8_NORM(8, 1, 0);
@@ -276,7 +286,6 @@ void launch_w8a8_rmsnorm(const W8NormArgs& a, hipStream_t stream) {
   p.q = a.q;
   p.s = a.s;
   p.ldx = a.ldx; p.ldr = a.ldr; p.ldh = a.ldh; p.ldy = a.ldy;
-  p.M = a.M;
   p.K = (int)a.K;
   p.eps = a.eps;
 #define W8A8_NORM_OF(BF)                                                               \
@@ -285,7 +294,16 @@ void launch_w8a8_rmsnorm(const W8NormArgs& a, hipStream_t stream) {
   } else {                                                                             \
     if (p.r) launch_norm<BF, false, true>(p, stream); else launch_norm<BF, false, false>(p, stream); \
   }
-  if (a.bf16) { W8A8_NORM_OF(true) } else { W8A8_NORM_OF(false) }
+  // up to 2^22 rows a launch, so that its threads stay under 2^32
+  for (int64_t left = a.M; left > 0; left -= p.M) {
+    p.M = left < kNormRows ? left : kNormRows;
+    if (a.bf16) { W8A8_NORM_OF(true) } else { W8A8_NORM_OF(false) }
+    p.x += p.M * p.ldx;
+    if (p.r) p.r += p.M * p.ldr, p.h += p.M * p.ldh;
+    if (p.y) p.y += p.M * p.ldy;
+    p.q += p.M * p.K;
+    p.s += p.M;
+  }
 #undef W8A8_NORM_OF
 }
 

@@ -692,14 +692,14 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
         r = residual.data_ptr()
     if out is None:
         new = x.new_empty
-        xq, xs = new(shape, dtype=torch.int8), new((M,), dtype=torch.float32)
+        xq, xs = new(shape, dtype=_I8), new(M, dtype=_F32)
         out = xq, xs
-        if r:
-            ldh = max(K, 1)
+        if residual is not None:
+            ldh = K
             out += (new(shape),)
             h = out[2].data_ptr()
         if return_normed:
-            ldy = max(K, 1)
+            ldy = K
             out += (new(shape),)
             y = out[-1].data_ptr()
     else:
