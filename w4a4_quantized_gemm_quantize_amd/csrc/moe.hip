@@ -146,6 +146,7 @@ __host__ __device__ constexpr int code_ld(int K, int span) { return (K + span - 
 inline size_t moe_lds(int P, int E, int rows, int channels) {
   return (size_t)P * sums_ld(channels) * 4 + P * 4 + E * 4 + (max_entries(P, E, rows) + 1) * 8 + ((P + 1) / 2) * 8 + 32;
 }
+constexpr int kFusedSpan = 512;    // a chunk of k_w8a8_moe with FUSED
 inline size_t fused_lds(int P, int K, int span) { return (size_t)P * code_ld(K, span) + P * 4 + 16; }
 
 // Another lane's value, 0 where there is none or the row is not in MASK.
@@ -200,33 +201,38 @@ __device__ __forceinline__ float quantize_row(const float* __restrict__ h, int K
 
 // A workgroup owns CN channels (UP: CN / 2 gates and their values) of every expert, or
 // of a share of the experts that the tokens chose (UP, blockIdx.y). It sorts the pairs
-// by expert; an entry is up to ROWS rows of one expert, and the entries' chunks of CH
-// k-steps are dealt to the waves in contiguous runs of equal length, whatever experts
-// they fall in. A wave streams the weights of its chunks from memory straight into
-// v_mfma_i32_16x16x64_i8, the next two chunks in flight, and adds an entry's int32
-// sums to those in LDS (exact in any order).
+// by expert; an entry is up to ROWS rows of one expert, and the entries' chunks of
+// four k-steps are dealt to the waves in contiguous runs of equal length, whatever
+// experts they fall in. A wave streams its chunks, the next on its way, and adds an
+// entry's int32 sums to those in LDS (exact in any order).
+//
+// The operands of v_mfma_i32_16x16x64_i8 want 16 rows in 16 neighbouring lanes; loaded
+// so, a load touches 64 pieces of 16 bytes, and the cache serves about 0.65 of them a
+// clock (counted: 54.5 million in 142 us on 256 CUs). Chunks are therefore loaded in
+// whole runs of a row, 256 bytes for 16 lanes, and turned by LDS (64 tokens, 8 of 64
+// experts of 4096 x 1376: 240 -> 213 us).
 //
 // HALF: blocks of 8 rows and 8 channels that use both halves of the instruction's 16, the
 // upper ones for the next 64 of k: rows r and r + 8 hold the same token, columns c and
-// c + 8 the same channel, so D[r][c] + D[r + 8][c + 8] is the sum. A load then covers 8
-// whole 128-byte lines, and there are twice the workgroups.
+// c + 8 the same channel, so D[r][c] + D[r + 8][c + 8] is the sum: longer runs of a row.
 //
 // FUSED: h is quantized here, into LDS, by every workgroup.
 //
-// Bound by what a CU can have on its way from L2, weights and rows together (6.5 TB/s over
-// the chip): 64 tokens, 8 of 64 experts of 4096 x 1376, 1.04 GB of weights: 240 us, 4.4 TB/s;
-// 13 tokens, 4 of 32 of 3584 x 2368, 0.52 GB: 115 us, 4.6 TB/s; one token, 8 of 64 of 2048
-// x 1024, 50 MB: 19 us, of which 7 are two launches without any expert. More in
-// flight (chunks twice as long) was slower (16 rows: 119 -> 140 us, the 32 experts),
-// as were non-temporal loads (127 -> 135).
+// Bound by HBM, the rows' codes from L2 on top: 64 tokens, 8 of 64 experts of 4096 x 1376,
+// 1.04 GB of weights: 207 us, 5.0 TB/s; 13 tokens, 4 of 32 of 3584 x 2368, 0.52 GB: 108 us,
+// 4.8 TB/s; the first stage for one token and all 64 experts 123 us, 5.9 TB/s; one token, 8
+// of 64 of 2048 x 1024, 50 MB: 18 us, of which 7 are two launches without any expert. Two
+// chunks on their way instead of one, or 16 waves, were slower (212 -> 236 us, -> 234).
 enum { UP = 0, DOWN = 1 };
-template <int STAGE, bool HALF, int RT, int CH, int CB, int NW, bool FUSED>
+template <int STAGE, bool HALF, int RT, int CB, int NW, bool FUSED>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
   constexpr int NT = 64 * NW, RB = HALF ? 8 : 16, CN = RB * CB, ROWS = RB * RT, LD = sums_ld(CN);
-  constexpr int KS = HALF ? 128 : 64, SPAN = KS * CH;
+  constexpr int KS = HALF ? 128 : 64, SPAN = 4 * KS, ROW_LANES = SPAN / 16, ROWS_L = 64 / ROW_LANES;
+  constexpr int D = FUSED ? 2 : 1;                                   // chunks on their way
   static_assert(kMoeMaxPairs <= NT && kMoeMaxExperts <= NT, "one a thread");
   extern __shared__ __align__(16) uint8_t lds[];
   __shared__ uint32_t wave_total[NW];
+  __shared__ __align__(16) uint8_t stage[NW][4096];
   int* const sums = reinterpret_cast<int*>(lds);                     // [P][LD]
   int* const id_of = sums + p.P * LD;                                // [P]
   int* const first = id_of + p.P;                                    // [E] counts, then first positions
@@ -294,10 +300,13 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
   const int nch = (p.K + SPAN - 1) / SPAN;
   const int chunks = (ent1 - ent0) * nch;
   const int ch0 = (int)((int64_t)chunks * wave / NW), ch1 = (int)((int64_t)chunks * (wave + 1) / NW);
+  // A block is RB rows of SPAN bytes: 4 loads, of which each covers whole rows (a lane's
+  // address in its place of the block: row ROWS_L j + lr, 16-byte piece lp).
   struct Buf {
-    v4i w[CH][CB];
-    v4i a[FUSED ? 1 : RT][FUSED ? 1 : CH];
+    v4i w[CB][4];
+    v4i a[FUSED ? 1 : RT][4];
   };
+  const int lr = lane / ROW_LANES, lp = lane % ROW_LANES;
   // rows of an entry that this lane supplies (dropped ones past its end)
   auto entry_at = [&](int e) {
     const int2 v = entry[e];
@@ -306,7 +315,7 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
   const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, FUSED ? 0 : (STAGE == UP ? p.T : p.P) * p.K);
   int l_ent = ent0 + (chunks ? ch0 / nch : 0), l_ch = chunks ? ch0 % nch : 0, l_at = ch0;
   __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w, 0);
-  int off_a[RT], l_n = 0;
+  int off_a[FUSED ? 1 : RT][4], l_n = 0;
   auto enter_load = [&]() {
     const int2 v = entry_at(l_ent);
     const int e = v.x & 0xFFFF, n = v.x >> 16;
@@ -314,15 +323,19 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
     rW = buffer_rsrc(p.w + ((int64_t)e * p.N + n0) * p.K, rows_w * p.K);
     if constexpr (!FUSED) {
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const int row = RB * r + cr;
-        const int pair = pair_of[v.y + min(row, n - 1)];
-        off_a[r] = row < n ? (STAGE == UP ? pair / p.k : pair) * p.K + kl : kDroppedOffset;
-      }
+      for (int r = 0; r < RT; ++r)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int row = RB * r + ROWS_L * j + lr;
+          const int pair = pair_of[v.y + min(row, n - 1)];
+          off_a[r][j] = row < n ? (STAGE == UP ? pair / p.k : pair) * p.K + 16 * lp : kDroppedOffset;
+        }
     }
   };
 #pragma unroll
-  for (int r = 0; r < RT; ++r) off_a[r] = kDroppedOffset;
+  for (int r = 0; r < (FUSED ? 1 : RT); ++r)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) off_a[r][j] = kDroppedOffset;
   if (ch0 < ch1) enter_load();
   auto fetch = [&](Buf& b) {
     if (l_at < ch1 && l_ch == nch) {
@@ -330,33 +343,50 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
       ++l_ent;
       enter_load();
     }
+    const int k0 = SPAN * l_ch;
+    const int out = l_at < ch1 && k0 + 16 * lp < p.K ? 0 : kDroppedOffset;
 #pragma unroll
-    for (int u = 0; u < CH; ++u) {
-      const int k0 = KS * (l_ch * CH + u);
-      const int out = l_at < ch1 && k0 + kl < p.K ? 0 : kDroppedOffset;
+    for (int cb = 0; cb < CB; ++cb)
 #pragma unroll
-      for (int cb = 0; cb < CB; ++cb)
-        b.w[u][cb] = __builtin_bit_cast(
-            v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, ((RB * cb + cr) * p.K + kl) | out, k0, 0));
-    }
+      for (int j = 0; j < 4; ++j)
+        b.w[cb][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+            rW, ((RB * cb + ROWS_L * j + lr) * p.K + 16 * lp) | out, k0, 0));
     if constexpr (!FUSED) {
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         if (r > 0 && l_n <= RB * r) break;             // a block of rows that the entry does not have
 #pragma unroll
-        for (int u = 0; u < CH; ++u) {
-          const int k0 = KS * (l_ch * CH + u);
-          const int out = l_at < ch1 && k0 + kl < p.K ? 0 : kDroppedOffset;
-          b.a[r][u] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, off_a[r] | out, k0, 0));
-        }
+        for (int j = 0; j < 4; ++j)
+          b.a[r][j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, off_a[r][j] | out, k0, 0));
       }
     }
     ++l_ch;
     ++l_at;
   };
-  Buf b0, b1;
-  fetch(b0);
-  fetch(b1);
+  // A block into operands: lane (c, g) of k-step u takes row cr at KS u + kl. Pieces are
+  // swizzled by their row, so that 16 lanes meet 16 bank groups both ways. The region is
+  // the wave's own, whose LDS operations complete in order.
+  int put[4], take[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    auto place = [](int row, int piece) {
+      return row * SPAN + 16 * (piece ^ (HALF ? (row & 3) | (row & 4) << 1 : row));
+    };
+    put[j] = place(ROWS_L * j + lr, lp);
+    take[j] = place(cr, (KS * j + kl) / 16);
+  }
+  uint8_t* const mine = stage[wave];
+  auto operands = [&](const v4i raw[4], v4i op[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(mine + put[j]) = raw[j];
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int u = 0; u < 4; ++u) op[u] = *reinterpret_cast<const v4i*>(mine + take[u]);
+    asm volatile("" ::: "memory");
+  };
+  Buf b[D];
+#pragma unroll
+  for (int d = 0; d < D; ++d) fetch(b[d]);
 
   if constexpr (FUSED) {
     for (int i = wave; i < p.P; i += NW) {
@@ -383,18 +413,24 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
     }
   };
   auto consume = [&](const Buf& b) {
+    v4i w[CB][4];
+#pragma unroll
+    for (int cb = 0; cb < CB; ++cb) operands(b.w[cb], w[cb]);
 #pragma unroll
     for (int r = 0; r < RT; ++r) {
       if (RB * r >= c_n) break;
+      v4i a[4];
+      if constexpr (FUSED) {
 #pragma unroll
-      for (int u = 0; u < CH; ++u) {
-        v4i a;
-        if constexpr (FUSED) a = *reinterpret_cast<const v4i*>(row_a[r] + KS * (c_ch * CH + u));
-        else a = b.a[r][u];
+        for (int u = 0; u < 4; ++u) a[u] = *reinterpret_cast<const v4i*>(row_a[r] + SPAN * c_ch + KS * u);
+      } else {
+        operands(b.a[r], a);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u)
 #pragma unroll
         for (int cb = 0; cb < CB; ++cb)
-          acc[r][cb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b.w[u][cb], acc[r][cb], 0, 0, 0);
-      }
+          acc[r][cb] = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], w[cb][u], acc[r][cb], 0, 0, 0);
     }
     if (++c_ch == nch) {
       c_ch = 0;
@@ -415,23 +451,18 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
     }
   };
   if (ch0 < ch1) enter();
-  for (int at = ch0; at < ch1; at += 2) {
-    // the second of a pair past the run's end holds zeros of W
-    bool done = consume(b0);
-    fetch(b0);
-    if (done || at + 1 >= ch1) {
-      flush();
-      if (at + 1 >= ch1) break;
-      ++c_ent;
-      enter();
-    }
-    done = consume(b1);
-    fetch(b1);
-    if (done || at + 2 >= ch1) {
-      flush();
-      if (at + 2 >= ch1) break;
-      ++c_ent;
-      enter();
+  for (int at = ch0; at < ch1;) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+      const bool done = consume(b[d]);
+      fetch(b[d]);
+      ++at;
+      if (done || at >= ch1) {
+        flush();
+        if (at >= ch1) break;
+        ++c_ent;
+        enter();
+      }
     }
   }
   __syncthreads();
@@ -449,17 +480,34 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
       p.h_out[(int64_t)pair * I + (n0 >> 1) + i] = activate(p.act, gate) * up;
     }
   } else {
+    // Every pair's share of the output in place of its sums, all loads at once; then
+    // the shares of a token in the order of its choices.
+    constexpr int AT_ONCE = 4;
+    for (int o = tid; o < positions * CN; o += AT_ONCE * NT) {
+      float f[AT_ONCE], s[AT_ONCE];
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int at = min(o + i * NT, positions * CN - 1), pair = pair_of[at / CN];
+        s[i] = (FUSED ? hs[pair] : p.sa[pair]) * p.sw[(int64_t)id_of[pair] * p.N + min(n0 + at % CN, p.N - 1)];
+        f[i] = p.weights[pair];
+      }
+#pragma unroll
+      for (int i = 0; i < AT_ONCE; ++i) {
+        const int at = o + i * NT;
+        if (at < positions * CN) {
+          int* const v = sums + at / CN * LD + at % CN;
+          *v = __float_as_int(f[i] * ((float)*v * s[i]));
+        }
+      }
+    }
+    __syncthreads();
     for (int o = tid; o < p.T * CN; o += NT) {
       const int t = o / CN, n = o % CN;
       if (n >= rows_w) continue;
       float sum = 0.0f;
-#pragma unroll 4
       for (int j = 0; j < p.k; ++j) {
-        const int pair = t * p.k + j, e = id_of[pair];
-        const float s = (FUSED ? hs[pair] : p.sa[pair]) * p.sw[(int64_t)max(e, 0) * p.N + n0 + n];
-        const float v = (float)sums[(e < 0 ? 0 : pos_of[pair]) * LD + n] * s;
-        const float f = p.weights[pair];
-        sum = e < 0 ? sum : fmaf(f, v, sum);
+        const int pair = t * p.k + j;
+        if (id_of[pair] >= 0) sum += __int_as_float(sums[pos_of[pair] * LD + n]);
       }
       const int64_t at = t * p.ldy + n0 + n;
       if (p.ydtype == 1) static_cast<_Float16*>(p.y)[at] = (_Float16)sum;
@@ -483,19 +531,19 @@ int64_t align256(int64_t n) { return (n + 255) & ~int64_t{255}; }
 // Stage 0 (UP) or 1 (DOWN) of a layer whose experts have few rows, or more.
 template <int STAGE, bool FUSED>
 void launch_stage(const MoeParams& p, int shares, bool few_rows, hipStream_t stream) {
-#define MOE_STAGE(HALF, RT, CH, CB, NW)                                                                                \
+#define MOE_STAGE(HALF, RT, CB)                                                                                        \
   {                                                                                                                    \
-    constexpr int RB = HALF ? 8 : 16, SPAN = (HALF ? 128 : 64) * CH;                                                   \
+    constexpr int RB = HALF ? 8 : 16;                                                                                  \
     const dim3 grid((unsigned)((p.N + RB * CB - 1) / (RB * CB)), (unsigned)shares);                                    \
-    const size_t lds = moe_lds(p.P, p.E, RB * RT, RB * CB) + (FUSED ? fused_lds(p.P, p.K, SPAN) : 0);                  \
-    hipLaunchKernelGGL((k_w8a8_moe<STAGE, HALF, RT, CH, CB, NW, FUSED>), grid, dim3(64 * NW), (unsigned)lds, stream, p); \
+    const size_t lds = moe_lds(p.P, p.E, RB * RT, RB * CB) + (FUSED ? fused_lds(p.P, p.K, kFusedSpan) : 0);            \
+    hipLaunchKernelGGL((k_w8a8_moe<STAGE, HALF, RT, CB, 8, FUSED>), grid, dim3(512), (unsigned)lds, stream, p);        \
     return;                                                                                                            \
   }
   if constexpr (FUSED) {
-    MOE_STAGE(true, 1, 2, 1, 16)
+    MOE_STAGE(true, 1, 1)
   } else {
-    if (few_rows) MOE_STAGE(true, 1, (STAGE == UP ? 1 : 2), (STAGE == UP ? 2 : 1), 8)
-    MOE_STAGE(false, 2, 2, (STAGE == UP ? 2 : 1), 8)
+    if (few_rows) MOE_STAGE(STAGE == DOWN, 1, (STAGE == UP ? 1 : 2))
+    MOE_STAGE(false, 2, 1)
   }
 #undef MOE_STAGE
 }
@@ -534,11 +582,11 @@ void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream) {
   p.weights = a.weights;
   p.T = a.T; p.k = a.k; p.P = P; p.E = a.E;
   p.act = a.act;
-  // Tiles of 8 channels and 8 rows where an expert has few, of 16 channels and 32 rows
-  // where it has more and their codes weigh beside the weights (us; T, H, I, E, k): 4,
-  // 2048, 1024, 64, 8 42.3 and 50.5; 8, the same 55.8 and 66.9; 16, the same 67.3 and
-  // 79.3; 16, 2048, 1024, 16, 8 40.8 and 38.3; 32, 4096, 1376, 16, 4 92.3 and 72.6; 64, 4096, 1376, 64,
-  // 8 310 and 240. 16 and 64 rows were between or slower everywhere.
+  // Entries of 16 rows (second stage: 8 rows, two blocks of 8 channels) where an expert
+  // has few, of 32 rows where it has more (us with one and the other in the second
+  // stage; T, H, I, E, k): 16, 2048, 1024, 64, 8 65.1 and 69.2; 16, 4096, 1376, 64, 8 142
+  // and 151; 13, 3584, 2368, 32, 4 111 and 114; 64, 2048, 1024, 64, 8 126 and 123; 64, 4096,
+  // 1376, 64, 8 271 and 262; in the first stage 2 us either way.
   const bool few_rows = a.T <= 8 || P <= 4 * a.E;
 
   p.a = a.xq; p.sa = a.xs;
@@ -560,7 +608,7 @@ void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream) {
   // Every workgroup of the second stage quantizes h itself up to 16384 values; above, a
   // launch does (T, I, k with H = 2048: 1, 1024, 8 19.1 us in two launches, 21 in
   // three; 16, 1024, 2 21.2 and 20.5; 4, 1024, 8 41.1 and 40.3).
-  if (few_rows && (int64_t)P * a.I <= 16384 && moe_lds(P, a.E, 8, 8) + fused_lds(P, a.I, 256) <= kLds) {
+  if (few_rows && (int64_t)P * a.I <= 16384 && moe_lds(P, a.E, 8, 8) + fused_lds(P, a.I, kFusedSpan) <= kLds) {
     p.h = h;
     launch_stage<DOWN, true>(p, 1, true, stream);
     return;
