@@ -64,14 +64,19 @@ __device__ __forceinline__ float load16(const uint16_t* r, int ydt, int64_t i) {
 // epilogue write fp16 or bf16, rounded once.
 enum { EPI_PLAIN = 0, EPI_ACT = 1, EPI_GATED = 2 };
 
-// ---- Up to 16 tokens: W streamed once from HBM straight into the operands -----
+// ---- Up to 16 tokens: W streamed once from HBM into the operands ---------------
 // A workgroup of NW waves owns 16 channels and splits K across its waves
-// (contiguous runs of 64-k steps). v_mfma_i32_16x16x64_i8: lane l supplies 16
-// consecutive k of row l % 16 at k offset 16 (l / 16), so a step is one 16-byte
-// load per operand and lane, with no LDS on the way; RING steps are in flight
-// per wave. The waves' int32 sums meet in LDS (exact in any order). K is a
-// multiple of 16: the last step's lanes beyond K, and steps beyond a wave's
-// run, read zeros of W.
+// (contiguous runs of blocks of four 64-k steps, the next block on its way). The
+// waves' int32 sums meet in LDS (exact in any order). K is a multiple of 16: lanes
+// beyond K, and steps beyond a wave's run, read zeros of W.
+//
+// v_mfma_i32_16x16x64_i8: lane l supplies 16 consecutive k of row l % 16 at k offset
+// 16 (l / 16), so 16 neighbouring lanes want 16 rows; loaded so, a load touches 64
+// pieces of 16 bytes, and the cache serves about 0.65 of them a clock. Blocks are
+// loaded in whole runs of a row, 256 bytes for 16 lanes, and turned by LDS (us, W from
+// HBM, tokens x channels x K, loads straight into the operands and these: 16 x 8192 x 8192
+// 20 and 15; 8 x 28672 x 8192 57 and 43; 16 x 4096 x 11008 17.2 and 13; 8 x 11008 x 4096 15.0 and
+// 12.1; one token 4096 x 11008 11.9 and 11.7, 1024 x 8192 7.3 and 5.8).
 //
 // XT 0: the tokens' codes come from memory. XT 1, 2 (fp16, bf16 tokens): every
 // workgroup quantizes all of them itself, in pieces of 1024 elements per wave
@@ -79,37 +84,39 @@ enum { EPI_PLAIN = 0, EPI_ACT = 1, EPI_GATED = 2 };
 // their way; that saves a launch and the wait for it.
 //
 // Bound by the W stream: one token 4096 -> 128256 86.9 us, 6.0 TB/s of weights;
-// 8192 -> 28672 43.7 us, 5.4 TB/s; small ones by the launch and the loads'
-// latency (8192 -> 1024, 8 MB: 7.6 us). With more tokens by the L2 traffic of
-// their codes, which every workgroup reads again (M / 16 of W's bytes): see the
-// plan. RING 8 measured as 4.
-template <int XT, int NW, int RING, int PIECES, int EPI>
+// 8192 -> 28672 44 us, 5.3 TB/s; small ones by the launch and the loads' latency
+// (8192 -> 1024, 8 MB: 5.8 us).
+template <int XT, int NW, int PIECES, int EPI>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
   constexpr bool BF = XT == 2;
   __shared__ int red[NW - 1][4][64];
   __shared__ float row_scale[16];
+  __shared__ __align__(16) uint8_t turn[NW][4096];
   __shared__ uint32_t row_max[16];
   extern __shared__ __align__(16) uint8_t codes[];     // XT > 0: [M][K rounded up to 64]
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int c = lane & 15, g = lane >> 4;
   const int n0 = (int)blockIdx.x * 16;
-  const int steps = (p.K + 63) >> 6;
-  const int h0 = (int)((int64_t)steps * wave / NW), h1 = (int)((int64_t)steps * (wave + 1) / NW);
+  const int steps = (p.K + 63) >> 6, blocks = (steps + 3) >> 2;
+  const int h0 = (int)((int64_t)blocks * wave / NW) * 4, h1 = min((int)((int64_t)blocks * (wave + 1) / NW) * 4, steps);
   const int w_rows = min(16, p.N - n0);
   const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, XT ? 0 : p.M * p.K);
   const __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w + (int64_t)n0 * p.K, w_rows * p.K);
-  const int offA = c < p.M ? c * p.K + 16 * g : kDroppedOffset;
-  const int offW = c < w_rows ? c * p.K + 16 * g : kDroppedOffset;
-  struct Step {
-    v4i a, w;
-  };
-  Step ring[RING];
-  auto load = [&](Step& st, int h) {
-    const int out = h < h1 && 64 * h + 16 * g < p.K ? 0 : kDroppedOffset;
-    st.w = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rW, offW | out, 64 * h, 0));
-    if constexpr (XT == 0)
-      st.a = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(rA, offA | out, 64 * h, 0));
+  // load j of a block: row 4 j + lane / 16, 16 bytes of its 256
+  const int run_row = lane >> 4, run_k = 16 * (lane & 15);
+  v4i next_w[4], next_a[XT ? 1 : 4];
+  auto load = [&](int h) {
+    const int out = h < h1 && 64 * h + run_k < p.K ? 0 : kDroppedOffset;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int row = 4 * j + run_row;
+      next_w[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+          rW, (row < w_rows ? row * p.K + run_k : kDroppedOffset) | out, 64 * h, 0));
+      if constexpr (XT == 0)
+        next_a[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+            rA, (row < p.M ? row * p.K + run_k : kDroppedOffset) | out, 64 * h, 0));
+    }
   };
   const int KP = steps * 64;
   if constexpr (XT > 0) {
@@ -126,8 +133,7 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
       raw[i][0] = src[0];
       raw[i][1] = src[1];
     }
-#pragma unroll
-    for (int u = 0; u < RING; ++u) load(ring[u], h0 + u);
+    load(h0);
     __syncthreads();                                     // row_max is cleared
 #pragma unroll
     for (int i = 0; i < PIECES; ++i) {
@@ -148,19 +154,39 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
     }
     __syncthreads();
   } else {
-#pragma unroll
-    for (int u = 0; u < RING; ++u) load(ring[u], h0 + u);
+    load(h0);
   }
   const uint8_t* const la = codes + (c < p.M ? c : 0) * KP + 16 * g;   // rows past M: their sums are not stored
-  v4i acc = {0, 0, 0, 0};
-  for (int h = h0; h < h1; h += RING) {
+  // The region is the wave's own, whose LDS operations complete in order; 16-byte
+  // pieces are swizzled by their row, so that 16 lanes meet 16 bank groups both ways.
+  uint8_t* const mine = turn[wave];
+  int put[4], take[4];
 #pragma unroll
-    for (int u = 0; u < RING; ++u) {
-      v4i a = ring[u].a;
-      if constexpr (XT > 0) a = *reinterpret_cast<const v4i*>(la + 64 * min(h + u, steps - 1));
-      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a, ring[u].w, acc, 0, 0, 0);
-      load(ring[u], h + u + RING);
+  for (int j = 0; j < 4; ++j) {
+    put[j] = (4 * j + run_row) * 256 + 16 * ((lane & 15) ^ (4 * j + run_row));
+    take[j] = c * 256 + 16 * ((4 * j + g) ^ c);
+  }
+  auto operands = [&](const v4i* from, v4i to[4]) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) *reinterpret_cast<v4i*>(mine + put[j]) = from[j];
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int u = 0; u < 4; ++u) to[u] = *reinterpret_cast<const v4i*>(mine + take[u]);
+    asm volatile("" ::: "memory");
+  };
+  v4i acc = {0, 0, 0, 0};
+  for (int h = h0; h < h1; h += 4) {
+    v4i w[4], a[4];
+    operands(next_w, w);
+    if constexpr (XT == 0) {
+      operands(next_a, a);
+    } else {
+#pragma unroll
+      for (int u = 0; u < 4; ++u) a[u] = *reinterpret_cast<const v4i*>(la + 64 * min(h + u, steps - 1));
     }
+    load(h + 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], w[u], acc, 0, 0, 0);
   }
   if (wave > 0) {
 #pragma unroll
@@ -618,12 +644,9 @@ void k_w8a8_gemm_tiles(W8Params p) {
 
 // Which kernel, and into how many K ranges.
 //
-// Up to 16 tokens the W stream decides (k_w8a8_gemm_small), but that kernel's
-// workgroups each read all tokens' codes: with more than 8 tokens and W above
-// 64 MiB 128-channel tiles take over, which read them 8 times less often (16 x
-// 28672 x 8192: 53.5 us, 60 in the small kernel; 16 x 8192 x 28672: 47 and 54;
-// 16 x 18944 x 3584: 19.5 and 22.4; below, 16 x 8192 x 8192: 21.8 and 20.1; all
-// with W from HBM).
+// Up to 16 tokens the W stream decides (k_w8a8_gemm_small; us there and in tiles, W
+// from HBM: 16 x 28672 x 8192 46 and 53, 16 x 8192 x 28672 45 and 50, 16 x 18944 x 3584
+// 16.5 and 19.4, 9 x the same 15.6 and 19.3, 16 x 4096 x 14336 15 both).
 //
 // Above 16 tokens, the tile whose estimated time is least: rounds of tiles over
 // the CUs times (stages x the tile's time per 128-k stage + its start and
@@ -641,7 +664,7 @@ struct W8Plan {
   double us;              // the estimate
 };
 W8Plan plan_w8a8(int64_t M, int64_t N, int64_t K) {
-  if (M <= 8 || (M <= 16 && N * K <= (int64_t{1} << 26))) return W8Plan{TILE_SMALL, 1, 4.0 + N * K / 5.2e6};
+  if (M <= 16) return W8Plan{TILE_SMALL, 1, 4.0 + N * K / 5.2e6};
   const int64_t nk = (K + 127) / 128;
   W8Plan best{TILE_256, 1, 1e30};
   auto consider = [&](int tile, int64_t bm, int64_t bn, double stage, double start, int splits) {
@@ -684,8 +707,8 @@ template <int XT, int PIECES, int EPI = EPI_PLAIN>
 void launch_small(const W8Params& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.N + 15) / 16));
   const unsigned lds = XT ? (unsigned)(p.M * ((p.K + 63) / 64 * 64)) : 0;
-  if (four_waves(p.N)) hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 4, 4, PIECES, EPI>), grid, dim3(256), lds, stream, p);
-  else hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 8, 4, PIECES, EPI>), grid, dim3(512), lds, stream, p);
+  if (four_waves(p.N)) hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 4, PIECES, EPI>), grid, dim3(256), lds, stream, p);
+  else hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 8, PIECES, EPI>), grid, dim3(512), lds, stream, p);
 }
 
 // Pieces of 1024 elements per wave that a workgroup of k_w8a8_gemm_small has to
