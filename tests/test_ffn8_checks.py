@@ -129,6 +129,12 @@ def test_wrappers_refuse_host_tensors_and_bad_names():
         ops.w8a8_pack_gated(x, x[:2])
 
 
+def test_overlap():
+    t = torch.zeros((8, 64), dtype=torch.float16)
+    assert ops._overlap(t, t) and ops._overlap(t[:4], t[3:]) and ops._overlap(t[:, :8], t[:, 56:])
+    assert not ops._overlap(t[:4], t[4:]) and not ops._overlap(t[:0], t) and not ops._overlap(t[0:1, :32], t[0:1, 32:])
+
+
 def test_public_names():
     import w4a4_quantized_gemm_quantize_amd as pkg
     for name in ("w8a8_rmsnorm_quantize", "w8a8_gemm_act", "w8a8_linear_act", "w8a8_pack_gated", "moe_route", "w8a8_moe"):

@@ -623,6 +623,12 @@ def test_refusals_launch_nothing():
             o.w8a8_linear_act(x, q, s, **bad)
     with pytest.raises(ValueError):
         o.w8a8_gemm_act(q, s, q[:3], s[:3], gated=True)
+    square, ones = torch.zeros((64, 64), dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    with pytest.raises(ValueError):
+        o.w8a8_linear_act(x, square, ones, residual=x, out=x)
+    wide = torch.zeros((4, 128), dtype=torch.float16, device="cuda")
+    with pytest.raises(ValueError):
+        o.w8a8_linear_act(wide[:, :64], square, ones, out=wide[:, 32:96])
     with pytest.raises(ValueError):
         o.w8a8_gemm_act(q, s, torch.zeros((4, 80), dtype=torch.int8, device="cuda"), s)
     for k in (0, 65, -1, 2.0, True):

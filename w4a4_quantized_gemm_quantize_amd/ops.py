@@ -732,6 +732,16 @@ def w8a8_pack_gated(w_gate: torch.Tensor, w_up: torch.Tensor):
     return wq.view(w.shape), ws.view(w.shape[:-1])
 
 
+def _overlap(a, b) -> bool:
+    """Whether the address ranges of two 2-D tensors of 16-bit rows meet."""
+    def span(t):
+        rows, cols = t.shape
+        start = t.data_ptr()
+        return start, start + 2 * ((rows - 1) * t.stride(0) + cols) if rows and cols else start
+    (a0, a1), (b0, b1) = span(a), span(b)
+    return a0 < b1 and b0 < a1
+
+
 def _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out):
     """Checked weights and output of a product with an epilogue:
     (N, K, residual stride, y, dtype code, y's stride, wide)."""
@@ -787,7 +797,8 @@ def w8a8_linear_act(x: torch.Tensor, wq, ws, bias=None, activation=None, gated: 
                     out_dtype=torch.float16, out=None, workspace=None):
     """:func:`w8a8_linear` with the epilogue of :func:`w8a8_gemm_act`: fp16 or bf16
     activations [M, K] quantized per token, the product, bias, activation or gate, and
-    residual, in one call."""
+    residual, in one call. ``out`` may be ``residual`` but not overlap ``x``, which every
+    workgroup reads."""
     xdt = _x_dtype8(x, "x")
     ld = _rows_stride(x, "x")
     M = x.shape[0]
@@ -796,6 +807,8 @@ def w8a8_linear_act(x: torch.Tensor, wq, ws, bias=None, activation=None, gated: 
     N, K, ldr, y, dt, ldy, wide = _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out)
     if x.shape[1] != K:
         raise ValueError("K of x and wq differ")
+    if out is not None and _overlap(x, out):
+        raise ValueError("out overlaps x")
     held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_linear_act_workspace", M, N, K, gated, wide), device)
     _call8("w8a8_linear_act", device, x.data_ptr(), xdt, M, K, ld, wq.data_ptr(), ws.data_ptr(),
            0 if bias is None else bias.data_ptr(), act, gated, 0 if residual is None else residual.data_ptr(), ldr,
