@@ -829,8 +829,8 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out=No
     T, E = logits.shape
     k = _need_max(top_k, "top_k")
     if out is None:
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device)
-        weights = torch.empty((T, k), dtype=torch.float32, device=logits.device)
+        ids = logits.new_empty((T, k), dtype=_I32)
+        weights = logits.new_empty((T, k), dtype=_F32)
     else:
         ids, weights = out
         _check_out(ids, "ids", (T, k), torch.int32, logits.device)
