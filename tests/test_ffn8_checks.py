@@ -43,7 +43,7 @@ def test_act_validation():
     for f in (gemm_act, linear_act):
         assert f(K=72) == E_SHAPE and f(K=131072) == E_SHAPE and f(M=-1) == E_SHAPE and f(N=-1) == E_SHAPE
         assert f(M=1 << 24) == E_SHAPE and f(N=1 << 24, ldy=1 << 24) == E_SHAPE
-        assert f(N=1 << 23, ldy=1 << 23, gated=1) == E_SHAPE             # 2^24 channels
+        assert f(N=1 << 22, ldy=1 << 22) == E_SHAPE and f(N=1 << 21, ldy=1 << 21, gated=1) == E_SHAPE    # 2^22 channels
         assert f(act=5) == E_SHAPE and f(act=-1) == E_SHAPE
         assert f(dt=F32) == E_DTYPE and f(dt=9) == E_DTYPE
         assert f(ldy=7) == E_SHAPE and f(res=P, ldr=7) == E_SHAPE
@@ -61,8 +61,8 @@ def test_act_workspace():
     assert gemm(4, 8, 72, 0, 1) == -1 and lin(4, 8, 72, 0, 1) == -1 and gemm(0, 8, 64, 0, 1) == 0
     assert gemm(300, 1000, 336, 0, 1) == 0                               # tiles write the outputs
     assert gemm(300, 1000, 336, 0, 0) == 300 * 1000 * 4                  # other rows: int32 sums first
-    assert gemm(300, 1001, 336, 0, 1) == 300 * 1001 * 4
-    assert gemm(300, 1001, 336, 1, 1) == 300 * 2002 * 4
+    assert gemm(300, 1001, 336, 0, 1) == 300 * 1004 * 4                  # in rows of whole 16-byte stores
+    assert gemm(300, 1001, 336, 1, 1) == 300 * 2004 * 4
     for M, N, K in [(64, 8192, 8192), (4096, 4096, 4096), (17, 100, 1040), (512, 4096, 11008)]:
         for gated in (0, 1):
             assert gemm(M, N, K, gated, 0) >= gemm(M, N, K, gated, 1)

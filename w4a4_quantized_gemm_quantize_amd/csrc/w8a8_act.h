@@ -18,7 +18,7 @@ template <int EPI>
 __global__ __launch_bounds__(kThreads) void k_w8a8_join_act(W8Params p, int splits) {
   constexpr int C = EPI == EPI_GATED ? 2 : 1;              // channels of an output
   const int outs = p.N / C;
-  const int64_t total = (int64_t)p.M * outs, plane = (int64_t)p.M * p.N;
+  const int64_t total = (int64_t)p.M * outs, plane = (int64_t)p.M * p.part_ld;
   for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
     const int64_t m = i / outs;
     const int n = (int)(i - m * outs);
@@ -27,7 +27,7 @@ __global__ __launch_bounds__(kThreads) void k_w8a8_join_act(W8Params p, int spli
     for (int c = 0; c < C; ++c) v[c] = 0;
     for (int s = 0; s < splits; ++s) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[c] += p.part[s * plane + m * p.N + C * n + c];
+      for (int c = 0; c < C; ++c) v[c] += p.part[s * plane + m * p.part_ld + C * n + c];
     }
     float f[C];
 #pragma unroll
@@ -59,6 +59,9 @@ void launch_tiles_act(W8Params p, hipStream_t stream) {
 #undef W8A8_ACT
 }
 
+// Ints per row of sums: whole 16-byte stores whatever the width.
+int64_t sums_ld(int64_t N) { return (N + 3) & ~int64_t{3}; }
+
 // int32 sums of `splits` K ranges into the workspace, then the join.
 template <int EPI>
 void launch_raw(W8Params p, int splits, hipStream_t stream) {
@@ -67,12 +70,9 @@ void launch_raw(W8Params p, int splits, hipStream_t stream) {
   p.stages = (nk + splits - 1) / splits;
   p.splits = splits = (nk + p.stages - 1) / p.stages;
   const int64_t blocks = tiles * splits;
-  const bool wide = p.N % 4 == 0 && 128 * (int64_t)p.N * 4 < (int64_t{1} << 31);
-  if (wide)
-    hipLaunchKernelGGL((k_w8a8_gemm_tiles<128, 128, 2, 2, 3, OUT_RAW, true>), dim3((unsigned)std::min<int64_t>(blocks, kCUs)),
-                       dim3(256), 0, stream, p);
-  else
-    hipLaunchKernelGGL((k_w8a8_gemm_tiles<128, 128, 2, 2, 3, OUT_RAW, false>), dim3((unsigned)blocks), dim3(256), 0, stream, p);
+  p.part_ld = (int)sums_ld(p.N);
+  hipLaunchKernelGGL((k_w8a8_gemm_tiles<128, 128, 2, 2, 3, OUT_RAW, true>), dim3((unsigned)std::min<int64_t>(blocks, kCUs)),
+                     dim3(256), 0, stream, p);
   const int64_t outs = (int64_t)p.M * p.N / (EPI == EPI_GATED ? 2 : 1);
   const int64_t jb = std::min<int64_t>((outs + kThreads - 1) / kThreads, 8192);
   hipLaunchKernelGGL(k_w8a8_join_act<EPI>, dim3((unsigned)jb), dim3(kThreads), 0, stream, p, splits);
@@ -87,7 +87,9 @@ W8Params act_params(const W8GemmArgs& g, const W8Epilogue& e) {
 }
 
 // Tiles that write outputs themselves need rows that take 16-byte stores; other
-// rows, of odd widths or strides, go through the int32 sums, as K ranges do. Where
+// rows, of odd widths or strides, go through the int32 sums, as K ranges do (written
+// element by element instead: 4000 x 4084 x 1024 84.6 us for 73.2, 797 x 142 x 736 with
+// a residual 31.6 for 15.8). Where
 // few tokens follow a multiple of 256, they may take a launch of their own, so that
 // they cost no further row of tiles (777 x 18944 x 3584 with GELU, us: 112.0, 96.6 and 99.6 in
 // 256 x 256, 256 x 128 and 128 x 128 tiles, 63.7 + 18.9 as 768 and 9 tokens).

@@ -12,7 +12,7 @@ bool w8a8_wide_rows(int64_t outs, const void* y, int64_t ldy, const void* residu
 
 int64_t w8a8_act_workspace(int64_t M, int64_t N, int64_t K, bool wide) {
   const ActPlan a = plan_act(M, N, K, wide);
-  auto sums = [&](int64_t m, const W8Plan& pl) { return sums_in_workspace(pl, wide) ? (int64_t)pl.splits * m * N * 4 : 0; };
+  auto sums = [&](int64_t m, const W8Plan& pl) { return sums_in_workspace(pl, wide) ? (int64_t)pl.splits * m * sums_ld(N) * 4 : 0; };
   const int64_t n = a.first == M ? sums(M, a.plan) : std::max(sums(a.first, a.plan), sums(M - a.first, a.rest));
   return wide ? n : std::max(n, w8a8_act_workspace(M, N, K, true));   // never less for other rows
 }

@@ -31,7 +31,8 @@ struct W8Params {
   void* y;
   int ydtype;
   int64_t ldy;
-  int32_t* part;              // [splits][M][N] int32 sums, or nullptr
+  int32_t* part;              // [splits][M][part_ld] int32 sums, or nullptr
+  int part_ld;
   int splits;                 // K ranges
   int stages;                 // 128-k stages per range
   int act;                    // forms with an epilogue: ACT_*, and the residual [M][ldr] or nullptr
@@ -485,9 +486,9 @@ void k_w8a8_gemm_tiles(W8Params p) {
     return __half_as_ushort(__float2half_rn(lo)) | (uint32_t)__half_as_ushort(__float2half_rn(hi)) << 16;
   };
   auto store_tile = [&](int m0, int n0, int pt) {
-    uint8_t* y = OUT == OUT_RAW ? reinterpret_cast<uint8_t*>(p.part + (int64_t)pt * p.M * p.N)
+    uint8_t* y = OUT == OUT_RAW ? reinterpret_cast<uint8_t*>(p.part + (int64_t)pt * p.M * p.part_ld)
                                 : static_cast<uint8_t*>(p.y);
-    const int64_t ldy = OUT == OUT_RAW ? p.N : p.ldy;
+    const int64_t ldy = OUT == OUT_RAW ? p.part_ld : p.ldy;
     // WIDE: y's rows of this tile as one buffer (< 2^31 bytes, checked by the
     // host); a lane outside M x N gets an offset past it
     const int ldb = WIDE ? (int)(ldy * esz) : 0;
@@ -695,6 +696,7 @@ W8Params params(const W8GemmArgs& a) {
   p.ydtype = a.ydtype;
   p.ldy = a.ldy;
   p.splits = 1;
+  p.part_ld = p.N;
   return p;
 }
 
