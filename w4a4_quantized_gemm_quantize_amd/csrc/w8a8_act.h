@@ -13,25 +13,33 @@ namespace w4a4 {
 
 namespace {
 
-// Adds the K ranges' int32 sums and finishes them, one output a thread.
+// Adds the K ranges' int32 sums and finishes them: a thread one output of every
+// gridDim.y-th row.
 template <int EPI>
 __global__ __launch_bounds__(kThreads) void k_w8a8_join_act(W8Params p, int splits) {
   constexpr int C = EPI == EPI_GATED ? 2 : 1;              // channels of an output
-  const int outs = p.N / C;
-  const int64_t total = (int64_t)p.M * outs, plane = (int64_t)p.M * p.part_ld;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += (int64_t)gridDim.x * kThreads) {
-    const int64_t m = i / outs;
-    const int n = (int)(i - m * outs);
+  const int n = (int)blockIdx.x * kThreads + (int)threadIdx.x;
+  if (C * n >= p.N) return;
+  const int64_t plane = (int64_t)p.M * p.part_ld;
+  float sw[C], b[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    sw[c] = p.sw[C * n + c];
+    b[c] = p.bias ? p.bias[C * n + c] : 0.0f;
+  }
+  for (int64_t m = blockIdx.y; m < p.M; m += gridDim.y) {
     int v[C];
 #pragma unroll
     for (int c = 0; c < C; ++c) v[c] = 0;
-    for (int s = 0; s < splits; ++s) {
+    const int32_t* at = p.part + m * p.part_ld + C * n;
+    for (int s = 0; s < splits; ++s, at += plane) {
 #pragma unroll
-      for (int c = 0; c < C; ++c) v[c] += p.part[s * plane + m * p.part_ld + C * n + c];
+      for (int c = 0; c < C; ++c) v[c] += at[c];
     }
+    const float sa = p.sa[m];
     float f[C];
 #pragma unroll
-    for (int c = 0; c < C; ++c) f[c] = scaled(v[c], p.sa[m], p.sw[C * n + c], p.bias ? p.bias[C * n + c] : 0.0f);
+    for (int c = 0; c < C; ++c) f[c] = scaled(v[c], sa, sw[c], b[c]);
     float y = activate(p.act, f[0]);
     if constexpr (EPI == EPI_GATED) y *= f[1];
     if (p.res) y = plus(y, load16(p.res, p.ydtype, m * p.ldr + n));
@@ -73,9 +81,9 @@ void launch_raw(W8Params p, int splits, hipStream_t stream) {
   p.part_ld = (int)sums_ld(p.N);
   hipLaunchKernelGGL((k_w8a8_gemm_tiles<128, 128, 2, 2, 3, OUT_RAW, true>), dim3((unsigned)std::min<int64_t>(blocks, kCUs)),
                      dim3(256), 0, stream, p);
-  const int64_t outs = (int64_t)p.M * p.N / (EPI == EPI_GATED ? 2 : 1);
-  const int64_t jb = std::min<int64_t>((outs + kThreads - 1) / kThreads, 8192);
-  hipLaunchKernelGGL(k_w8a8_join_act<EPI>, dim3((unsigned)jb), dim3(kThreads), 0, stream, p, splits);
+  const int64_t cols = (p.N / (EPI == EPI_GATED ? 2 : 1) + kThreads - 1) / kThreads;
+  const int64_t rows = std::min<int64_t>(p.M, std::max<int64_t>(1, 8192 / cols));
+  hipLaunchKernelGGL(k_w8a8_join_act<EPI>, dim3((unsigned)cols, (unsigned)rows), dim3(kThreads), 0, stream, p, splits);
 }
 
 W8Params act_params(const W8GemmArgs& g, const W8Epilogue& e) {
