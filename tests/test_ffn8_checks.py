@@ -131,8 +131,23 @@ def test_wrappers_refuse_host_tensors_and_bad_names():
 
 def test_overlap():
     t = torch.zeros((8, 64), dtype=torch.float16)
-    assert ops._overlap(t, t) and ops._overlap(t[:4], t[3:]) and ops._overlap(t[:, :8], t[:, 56:])
+    assert ops._overlap(t, t) and ops._overlap(t[:4], t[3:])
     assert not ops._overlap(t[:4], t[4:]) and not ops._overlap(t[:0], t) and not ops._overlap(t[0:1, :32], t[0:1, 32:])
+
+
+def test_overlap_of_columns_and_in_place():
+    t = torch.zeros((8, 64), dtype=torch.float16)
+    assert not ops._overlap(t[:, :32], t[:, 32:]) and not ops._overlap(t[:, 32:], t[:, :32])
+    assert not ops._overlap(t[:6, 48:], t[2:, :48]) and not ops._overlap(t[1:7, :8], t[:, 56:])
+    assert ops._overlap(t[:, :33], t[:, 32:]) and ops._overlap(t[:, 16:48], t[2:, :17])
+    assert ops._overlap(t[1:, 60:], t[:7].view(-1)[56:].as_strided((7, 16), (64, 1)))      # round the row's end
+    assert ops._overlap(t[:, :8], t.view(16, 32)[:, 16:])                                  # other strides: as ranges
+    ops._in_place_or_apart(t, t, "a and b")
+    ops._in_place_or_apart(t[:, :8], t[:, 8:16], "a and b")
+    ops._in_place_or_apart(t[:1], t.view(16, 32)[:1], "a and b")
+    for a, b in ((t[1:], t[:7]), (t[:, 1:9], t[:, :8]), (t[:4], t.view(16, 32)[:4])):
+        with pytest.raises(ValueError):
+            ops._in_place_or_apart(a, b, "a and b")
 
 
 def test_public_names():

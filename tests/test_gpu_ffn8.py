@@ -596,6 +596,29 @@ def test_a_block_of_all_of_them():
 
 # ---------------------------------------------------------------- refusals
 
+def test_outputs_that_meet_inputs_are_refused():
+    import torch
+    o = ops()
+    buf = torch.ones((6, 192), dtype=torch.float16, device="cuda")
+    x, r, h, y = buf[:4, :64], buf[:4, 64:128], buf[:4, 128:], torch.ones((4, 64), dtype=torch.float16, device="cuda")
+    w = torch.ones(64, device="cuda")
+    q, s = o.w8a8_quantize_act(x)
+    norm = lambda h, y: o.w8a8_rmsnorm_quantize(x, w, residual=r, return_normed=True, out=(q, s, h, y))
+    for bad in ((buf[1:5, :64], y), (buf[:4, 8:72], y), (buf[2:, 64:128], y), (h, x), (h, r), (h, h), (h, buf[:4, 96:160])):
+        with pytest.raises(ValueError):
+            norm(*bad)
+    wq, ws = torch.ones((64, 64), dtype=torch.int8, device="cuda"), torch.ones(64, device="cuda")
+    for call, a in ((o.w8a8_gemm_act, (q, s)), (o.w8a8_linear_act, (x,))):
+        for bad in (buf[1:5, 64:128], buf[:4, 72:136]):
+            with pytest.raises(ValueError):
+                call(*a, wq, ws, residual=r, out=bad)
+    assert bool((buf == 1).all()) and bool((y == 1).all())
+    apart = o.w8a8_linear_act(x, wq, ws, residual=r, out=h)      # three columns of one buffer
+    assert torch.equal(apart, o.w8a8_linear_act(x.clone(), wq, ws, residual=r.clone()))
+    norm(h, y)
+    assert torch.equal(h, x + r)
+
+
 def test_refusals_launch_nothing():
     import torch
     o = ops()

@@ -666,6 +666,30 @@ def _need_rows(t, name: str, shape, dtype, device) -> int:
     return t.stride(0) if shape[0] > 1 else max(shape[1], 1)
 
 
+def _overlap(a, b) -> bool:
+    """Whether two 2-D tensors of contiguous rows share memory (columns apart in rows of
+    one stride do not)."""
+    def span(t):
+        rows, cols = t.shape
+        start = t.data_ptr()
+        return start, start + t.element_size() * ((rows - 1) * t.stride(0) + cols) if rows and cols else start
+    (a0, a1), (b0, b1) = span(a), span(b)
+    if a0 >= b1 or b0 >= a1:
+        return False
+    size, pitch = a.element_size(), a.stride(0)
+    if a.shape[0] > 1 and b.shape[0] > 1 and size == b.element_size() and pitch == b.stride(0) and (b0 - a0) % size == 0:
+        apart = (b0 - a0) // size % pitch
+        return apart < a.shape[1] or apart + b.shape[1] > pitch
+    return True
+
+
+def _in_place_or_apart(out, t, names: str) -> None:
+    """An output may be the input ``t`` itself, or must not meet it."""
+    same = out.data_ptr() == t.data_ptr() and (out.shape[0] == 1 or out.stride(0) == t.stride(0))
+    if not same and _overlap(out, t):
+        raise ValueError(f"{names} overlap without being the same tensor")
+
+
 def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=None, return_normed: bool = False,
                           out=None):
     """RMS norm of fp16 or bf16 X[M, K] (row stride may exceed K) to INT8 codes and one
@@ -675,7 +699,8 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
     With ``residual`` (X's shape and type) h is x + residual, rounded to X's type, and
     comes third; with ``return_normed`` the normed rows in X's type come last. ``weight``:
     [K], float32 or X's type. ``out``: the tuple of outputs to fill instead; its h may
-    be ``x`` or ``residual`` itself (in place). Rows that are not finite have NaN scales."""
+    be ``x`` or ``residual`` itself (in place), else they lie apart. Rows that are not finite
+    have NaN scales."""
     dt = _x_dtype8(x, "x")
     ldx = _rows_stride(x, "x")
     shape, device, dtype = x.shape, x.device, x.dtype
@@ -712,9 +737,14 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
         if residual is not None:
             ldh = _need_rows(out[2], "h", shape, dtype, device)
             h = out[2].data_ptr()
+            _in_place_or_apart(out[2], x, "h and x")
+            _in_place_or_apart(out[2], residual, "h and residual")
         if return_normed:
             ldy = _need_rows(out[-1], "normed", shape, dtype, device)
             y = out[-1].data_ptr()
+            for t in (x, *((residual, out[2]) if residual is not None else ())):
+                if _overlap(out[-1], t):
+                    raise ValueError("normed overlaps x, residual or h")
     _call8("w8a8_rmsnorm_quantize", device, x.data_ptr(), dt, ldx, r, ldr, weight.data_ptr(), _DTYPE8[weight.dtype], eps,
            M, K, xq.data_ptr(), xs.data_ptr(), h, ldh, y, ldy)
     return out
@@ -730,16 +760,6 @@ def w8a8_pack_gated(w_gate: torch.Tensor, w_up: torch.Tensor):
     w = torch.stack((w_gate, w_up), dim=-2).flatten(-3, -2)
     wq, ws = w8a8_pack_weight(w.reshape(-1, w.shape[-1]))
     return wq.view(w.shape), ws.view(w.shape[:-1])
-
-
-def _overlap(a, b) -> bool:
-    """Whether the address ranges of two 2-D tensors of 16-bit rows meet."""
-    def span(t):
-        rows, cols = t.shape
-        start = t.data_ptr()
-        return start, start + 2 * ((rows - 1) * t.stride(0) + cols) if rows and cols else start
-    (a0, a1), (b0, b1) = span(a), span(b)
-    return a0 < b1 and b0 < a1
 
 
 def _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out):
@@ -762,6 +782,8 @@ def _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out):
     if residual is not None:
         ldr = _need_rows(residual, "residual", (M, N), y.dtype, device)
         wide = wide and ldr % 8 == 0 and ldr < 1 << 22 and residual.data_ptr() % 16 == 0
+        if out is not None:
+            _in_place_or_apart(out, residual, "out and residual")
     return N, K, ldr, y, _DTYPE8[y.dtype], ldy, int(wide)
 
 
@@ -772,7 +794,7 @@ def w8a8_gemm_act(xq, xs, wq, ws, bias=None, activation=None, gated: bool = Fals
 
     ``activation``: None, "relu", "silu", "gelu" or "gelu_tanh". ``gated``: ``wq`` [2 N, K] as
     :func:`w8a8_pack_gated` lays it out, and Y[m, n] = act(v[m, 2n]) * v[m, 2n + 1] +
-    residual. ``residual``: [M, N] of Y's type; ``out`` may be it."""
+    residual; ``bias`` is interleaved alike. ``residual``: [M, N] of Y's type; ``out`` may be it."""
     _need(xq, torch.int8, "xq")
     _need(xs, torch.float32, "xs")
     if xq.dim() != 2 or not xq.is_contiguous() or not xs.is_contiguous():
