@@ -485,6 +485,41 @@ def test_moe(T, H, I, E, k):
         check_moe(moe_inputs(T, H, I, E, k, seed=T + H + i), act, ("float16", "bfloat16")[(i + T) % 2])
 
 
+@pytest.mark.parametrize("T,H,I,E,k", [(12, 400, 1040, 24, 4), (20, 1040, 704, 60, 8), (33, 272, 3232, 10, 3),
+                                       (9, 2560, 1056, 16, 6), (170, 512, 592, 130, 3)])
+def test_moe_few_channels(T, H, I, E, k):
+    # the second stage in shares of the experts, against tokens on their own
+    import torch
+    args = moe_inputs(T, H, I, E, k, seed=H)
+    ids = args[2]
+    ids[1::3, 0] = -1
+    ids[2::4, k - 1] = ids[2::4, 1]
+    ids[T // 2] = E
+    buf = torch.full((T + 1, H + 5), 3.0, dtype=torch.float16, device="cuda")
+    out = buf[:T, 3:3 + H]
+    ops().w8a8_moe(*args, out=out)
+    for t in range(T):
+        one = [a[t:t + 1].contiguous() if i < 4 else a for i, a in enumerate(args)]
+        assert torch.equal(ops().w8a8_moe(*one)[0], out[t])
+    assert bool((out[T // 2] == 0).all())
+    assert bool((buf[T] == 3).all()) and bool((buf[:, :3] == 3).all()) and bool((buf[:, 3 + H:] == 3).all())
+    check_moe(moe_inputs(T, H, I, E, k, seed=T), "gelu", "bfloat16")
+    # two captured calls with their own workspaces, replayed in turn with eager ones
+    calls = [moe_inputs(T, H, I, E, k, seed=s) for s in (1, 2)]
+    want = [ops().w8a8_moe(*a) for a in calls]
+    graph, got = torch.cuda.CUDAGraph(), []
+    with torch.cuda.graph(graph):
+        for a in calls:
+            got.append(ops().w8a8_moe(*a))
+    for _ in range(3):
+        for y in got:
+            y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(ops().w8a8_moe(*calls[0]), want[0])
+        assert all(torch.equal(y, w) for y, w in zip(got, want))
+
+
 def test_moe_ids_that_repeat_or_are_no_expert():
     import torch
     for T, k, E in [(1, 4, 8), (5, 4, 3), (20, 6, 4), (64, 8, 16)]:

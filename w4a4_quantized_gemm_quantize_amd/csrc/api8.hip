@@ -430,7 +430,7 @@ static bool moe_extents_ok(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I
 
 int64_t w8a8_moe_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   if (!moe_extents_ok(T, k, E, H, I)) return -1;
-  return T == 0 ? 0 : w4a4::moe_workspace(T, k, I);
+  return T == 0 ? 0 : w4a4::moe_workspace(T, k, E, H, I);
 }
 
 w4a4_status_t w8a8_moe(const int8_t* xq, const float* xs, const int32_t* ids, const float* weights, int64_t T, int64_t k,

@@ -157,7 +157,7 @@ struct MoeArgs {
   int64_t ldy;
   void* workspace;
 };
-int64_t moe_workspace(int64_t T, int64_t k, int64_t I);
+int64_t moe_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I);
 void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream);
 
 // ---- INT8 key/value cache (kv8_cache.hip, kv8_attention.hip)

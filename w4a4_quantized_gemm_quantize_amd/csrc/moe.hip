@@ -129,6 +129,7 @@ struct MoeParams {
   const float* sw;        // [E][N]
   int T, k, P, E, K, N, act;
   float* h_out;           // UP: [P][N / 2]
+  float* part;            // DOWN in shares: [P][N], a pair's part of its token's output
   void* y;                // DOWN
   int ydtype;
   int64_t ldy;
@@ -200,7 +201,7 @@ __device__ __forceinline__ float quantize_row(const float* __restrict__ h, int K
 }
 
 // A workgroup owns CN channels (UP: CN / 2 gates and their values) of every expert, or
-// of a share of the experts that the tokens chose (UP, blockIdx.y). It sorts the pairs
+// of a share of the experts that the tokens chose (blockIdx.y). It sorts the pairs
 // by expert; an entry is up to ROWS rows of one expert, and the entries' chunks of
 // four k-steps are dealt to the waves in contiguous runs of equal length, whatever
 // experts they fall in. A wave streams its chunks, the next on its way, and adds an
@@ -480,26 +481,32 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
       p.h_out[(int64_t)pair * I + (n0 >> 1) + i] = activate(p.act, gate) * up;
     }
   } else {
-    // Every pair's share of the output in place of its sums, all loads at once; then
-    // the shares of a token in the order of its choices.
+    // Every pair's part of the output in place of its sums, all loads at once; then
+    // the parts of a token in the order of its choices, by k_moe_join where they come
+    // from several shares.
     constexpr int AT_ONCE = 4;
-    for (int o = tid; o < positions * CN; o += AT_ONCE * NT) {
+    const bool alone = FUSED || shares == 1;             // FUSED has one share
+    const int at0 = alone ? 0 : entry[ent0].y * CN, at1 = alone ? positions * CN : entry[ent1].y * CN;
+    for (int o = at0 + tid; o < at1; o += AT_ONCE * NT) {
       float f[AT_ONCE], s[AT_ONCE];
 #pragma unroll
       for (int i = 0; i < AT_ONCE; ++i) {
-        const int at = min(o + i * NT, positions * CN - 1), pair = pair_of[at / CN];
+        const int at = min(o + i * NT, at1 - 1), pair = pair_of[at / CN];
         s[i] = (FUSED ? hs[pair] : p.sa[pair]) * p.sw[(int64_t)id_of[pair] * p.N + min(n0 + at % CN, p.N - 1)];
         f[i] = p.weights[pair];
       }
 #pragma unroll
       for (int i = 0; i < AT_ONCE; ++i) {
         const int at = o + i * NT;
-        if (at < positions * CN) {
+        if (at < at1) {
           int* const v = sums + at / CN * LD + at % CN;
-          *v = __float_as_int(f[i] * ((float)*v * s[i]));
+          const float part = f[i] * ((float)*v * s[i]);
+          if (alone) *v = __float_as_int(part);
+          else if (at % CN < rows_w) p.part[(int64_t)pair_of[at / CN] * p.N + n0 + at % CN] = part;
         }
       }
     }
+    if (!alone) return;
     __syncthreads();
     for (int o = tid; o < p.T * CN; o += NT) {
       const int t = o / CN, n = o % CN;
@@ -514,6 +521,20 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_moe(MoeParams p) {
       else static_cast<__bf16*>(p.y)[at] = (__bf16)sum;
     }
   }
+}
+
+// The parts of a token's output, in the order of its choices: a thread a column.
+__global__ __launch_bounds__(256) void k_moe_join(MoeParams p) {
+  const int n = (int)blockIdx.x * 256 + (int)threadIdx.x, t = blockIdx.y;
+  if (n >= p.N) return;
+  float sum = 0.0f;
+  for (int j = 0; j < p.k; ++j) {
+    const int pair = t * p.k + j, id = p.ids[pair];
+    if (id >= 0 && id < p.E) sum += p.part[(int64_t)pair * p.N + n];
+  }
+  const int64_t at = t * p.ldy + n;
+  if (p.ydtype == 1) static_cast<_Float16*>(p.y)[at] = (_Float16)sum;
+  else static_cast<__bf16*>(p.y)[at] = (__bf16)sum;
 }
 
 // The codes of h for k_w8a8_moe without FUSED, one wave a pair. Pairs without an
@@ -548,6 +569,46 @@ void launch_stage(const MoeParams& p, int shares, bool few_rows, hipStream_t str
 #undef MOE_STAGE
 }
 
+// How a layer is run, from its extents (times in us; sizes T, H, I, E, k).
+struct MoePlan {
+  // Entries of 16 rows (second stage: 8 rows, two blocks of 8 channels) where an expert
+  // has few, of 32 rows where it has more (one and the other in the second stage: 16,
+  // 2048, 1024, 64, 8 65.1 and 69.2; 16, 4096, 1376, 64, 8 142 and 151; 13, 3584, 2368, 32, 4
+  // 111 and 114; 64, 2048, 1024, 64, 8 126 and 123; 64, 4096, 1376, 64, 8 271 and 262; in the
+  // first stage 2 either way).
+  bool few_rows;
+  // Every workgroup of the second stage quantizes h itself up to 16384 values; above, a
+  // launch does (T, I, k with H = 2048: 1, 1024, 8 19.1 in two launches, 21 in three;
+  // 16, 1024, 2 21.2 and 20.5; 4, 1024, 8 41.1 and 40.3).
+  bool fused;
+  // Shares of the experts in the first stage, so that a workgroup streams some 128 KiB
+  // of weights: enough of them to fill the chip with few experts, and to end evenly with
+  // many (1, 2048, 1024, 64, 8: both stages 20.6 with 256 workgroups, 21.3 with 1024; 13,
+  // 3584, 2368, 32, 4: 145 with 296, 115 with 2072); at least about 256 workgroups (with
+  // those of 128 KiB alone 21, 560, 192, 32, 4 26.6, now 24.0; 2, 688, 144, 64, 6 15.0 and 12.9;
+  // 11, 1952, 160, 60, 1 16.9 and 13.8).
+  int up;
+  // Shares in the second stage where its channels fill at most 128 workgroups and it
+  // reads 8 MB or more: up to 512 of them, each with 96 KiB or more, and a launch that
+  // joins their parts (one share and several: 64, 2048, 1408, 64, 6 129.5 and 115.0; 51,
+  // 1040, 736, 60, 8 66.8 and 53.9; 39, 528, 1136, 32, 4 38.8 and 30.7; they cost elsewhere:
+  // 64, 4096, 1376, 64, 8 212.8 and 220.6; 16, 2880, 1024, 32, 4 58.2 and 61.2; 1, 448, 2848, 60,
+  // 6 21.5 and 22.6).
+  int down;
+};
+MoePlan plan_moe(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
+  MoePlan m;
+  const int64_t P = T * k, used = std::min(P, E), columns = H / 16;
+  m.few_rows = T <= 8 || P <= 4 * E;
+  m.fused = m.few_rows && P * I <= 16384 && moe_lds((int)P, (int)E, 8, 8) + fused_lds((int)P, (int)I, kFusedSpan) <= kLds;
+  const int64_t target = std::clamp<int64_t>(used * 2 * I * H >> 17, 256, 2048);
+  m.up = (int)std::max<int64_t>(1, std::min(used, target * 16 / (2 * I)));
+  m.down = 1;
+  if (!m.fused && columns <= 128 && used * H * I >= 8000000)
+    m.down = (int)std::max<int64_t>(1, std::min({used, 512 / columns, used * 16 * I / 98304}));
+  return m;
+}
+
 }  // namespace
 
 void launch_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64_t ldl, int k, bool renorm,
@@ -567,9 +628,9 @@ void launch_moe_route(const void* logits, int dtype, int64_t T, int64_t E, int64
 #undef MOE_ROUTE
 }
 
-int64_t moe_workspace(int64_t T, int64_t k, int64_t I) {
+int64_t moe_workspace(int64_t T, int64_t k, int64_t E, int64_t H, int64_t I) {
   const int64_t P = T * k;
-  return align256(4 * P * I) + align256(P * I) + align256(4 * P);
+  return align256(4 * P * I) + align256(P * I) + align256(4 * P) + (plan_moe(T, k, E, H, I).down > 1 ? 4 * P * H : 0);
 }
 
 void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream) {
@@ -578,44 +639,32 @@ void launch_w8a8_moe(const MoeArgs& a, hipStream_t stream) {
   int8_t* const codes = static_cast<int8_t*>(a.workspace) + align256(4 * (int64_t)P * a.I);
   float* const hs = reinterpret_cast<float*>(codes + align256((int64_t)P * a.I));
   MoeParams p = {};
+  p.part = reinterpret_cast<float*>(reinterpret_cast<int8_t*>(hs) + align256(4 * (int64_t)P));
   p.ids = a.ids;
   p.weights = a.weights;
   p.T = a.T; p.k = a.k; p.P = P; p.E = a.E;
   p.act = a.act;
-  // Entries of 16 rows (second stage: 8 rows, two blocks of 8 channels) where an expert
-  // has few, of 32 rows where it has more (us with one and the other in the second
-  // stage; T, H, I, E, k): 16, 2048, 1024, 64, 8 65.1 and 69.2; 16, 4096, 1376, 64, 8 142
-  // and 151; 13, 3584, 2368, 32, 4 111 and 114; 64, 2048, 1024, 64, 8 126 and 123; 64, 4096,
-  // 1376, 64, 8 271 and 262; in the first stage 2 us either way.
-  const bool few_rows = a.T <= 8 || P <= 4 * a.E;
+  const MoePlan m = plan_moe(a.T, a.k, a.E, a.H, a.I);
 
   p.a = a.xq; p.sa = a.xs;
   p.w = a.w13; p.sw = a.s13;
   p.K = a.H; p.N = 2 * a.I;
   p.h_out = h;
-  // Shares of the experts, so that a workgroup streams some 128 KiB of weights: enough
-  // of them to fill the chip with few experts, and to end evenly with many (8 of 64 experts of
-  // 2048 x 1024 for one token: both stages 20.6 us with 256 workgroups, 21.3 with 1024; 32 of 3584 x
-  // 2368 for 13: 145 with 296, 115 with 2072).
-  const int used = std::min(P, a.E);
-  const int64_t target = std::min<int64_t>(2048, (int64_t)used * p.N * p.K >> 17);
-  const int shares = (int)std::max<int64_t>(1, std::min<int64_t>(used, target * 16 / p.N));
-  launch_stage<UP, false>(p, shares, few_rows, stream);
+  launch_stage<UP, false>(p, m.up, m.few_rows, stream);
 
   p.K = a.I; p.N = a.H;
   p.w = a.w2; p.sw = a.s2;
   p.y = a.y; p.ydtype = a.ydtype; p.ldy = a.ldy;
-  // Every workgroup of the second stage quantizes h itself up to 16384 values; above, a
-  // launch does (T, I, k with H = 2048: 1, 1024, 8 19.1 us in two launches, 21 in
-  // three; 16, 1024, 2 21.2 and 20.5; 4, 1024, 8 41.1 and 40.3).
-  if (few_rows && (int64_t)P * a.I <= 16384 && moe_lds(P, a.E, 8, 8) + fused_lds(P, a.I, kFusedSpan) <= kLds) {
+  if (m.fused) {
     p.h = h;
     launch_stage<DOWN, true>(p, 1, true, stream);
     return;
   }
   hipLaunchKernelGGL(k_moe_quant, dim3((unsigned)((P + 3) / 4)), dim3(256), 0, stream, h, a.ids, a.E, P, a.I, codes, hs);
   p.a = codes; p.sa = hs;
-  launch_stage<DOWN, false>(p, 1, few_rows, stream);
+  launch_stage<DOWN, false>(p, m.down, m.few_rows, stream);
+  if (m.down > 1)
+    hipLaunchKernelGGL(k_moe_join, dim3((unsigned)((p.N + 255) / 256), (unsigned)a.T), dim3(256), 0, stream, p);
 }
 
 }  // namespace w4a4

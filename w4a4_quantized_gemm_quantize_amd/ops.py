@@ -880,7 +880,7 @@ def _moe_refuse(tensors):
 def w8a8_moe(xq, xs, ids, weights, w13, s13, w2, s2, activation="silu", out_dtype=torch.float16, out=None,
              workspace=None):
     """A mixture-of-experts layer of few tokens (T * k <= 512) on INT8 experts, in two
-    launches (three for many pairs): Y[T, H] = sum over a token's choices of weight *
+    launches (up to four for many pairs): Y[T, H] = sum over a token's choices of weight *
     (w2[e] @ quantized(act(gate) * up)), gate and up the interleaved channels of
     w13[e] @ x.
 
