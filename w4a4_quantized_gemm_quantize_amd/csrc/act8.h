@@ -39,7 +39,7 @@ __device__ __forceinline__ float gelu_act(float v) {
   const float tail = z * t * q * __builtin_amdgcn_exp2f(z * z * -0.721347520444481704f);
   return (v < 0.0f ? 0.0f : v) - tail;                  // a NaN stays
 }
-__device__ __forceinline__ float sigmoid_a(int act) { return act == ACT_SILU ? 1.0f : 1.59576912160573072f; }
+__device__ __forceinline__ float sigmoid_a(int act) { return act == ACT_SILU ? 1.0f : 1.59576912f; }
 __device__ __forceinline__ float sigmoid_b(int act) { return act == ACT_SILU ? 0.0f : 0.0713548162726009f; }
 
 // The residual's addition: a rounding of its own on every path, so that all give the
