@@ -106,8 +106,8 @@ struct ActPlan {
   W8Plan plan, rest;
 };
 // K ranges for rows that go through the sums in any case: rounds of tiles, and the
-// sums written and read (tokens x K x channels: 1210 x 2528 x 748 with SiLU and a residual 28.0 us in one range, 24.8 in four;
-// 797 x 736 x 142 12.5, 11.4).
+// sums written and read (tokens x K x channels: 1210 x 2528 x 748 with SiLU and a
+// residual 28.0 us in one range, 24.8 split; 797 x 736 x 142 12.5 and 11.4).
 W8Plan plan_sums(int64_t M, int64_t N, int64_t K) {
   const int64_t nk = (K + 127) / 128, tiles = ((M + 127) / 128) * ((N + 127) / 128);
   W8Plan best{TILE_128, 1, 1e30};
