@@ -28,11 +28,12 @@ enum {
  * Residual addition, RMS norm and symmetric INT8 quantization per row, in one pass:
  *   h = x + residual, rounded to x's type (h = x without a residual)
  *   t = fl32(h * weight);  rstd = 1 / sqrt(mean(h^2) + eps);  a = max|t|
- *   xq = rne(fl32(t / fl32(a / 127))), in [-127, 127];  xs = fl32(fl32(a rstd) / 127)
+ *   xq = rne(fl32(t / fl32(a / 127))), held in [-127, 127];  xs = fl32(fl32(a rstd) / 127)
  *   y = t rstd, rounded to x's type
  * xq * xs stands for t rstd; the row's factor rstd does not enter the codes. A row
- * with a = 0 gives xs = 0 and codes 0; one with a NaN or an infinity in h or t gives
- * xs = NaN and any codes. Squares past fp32's range (bf16) do not overflow.
+ * with a = 0 gives xs = 0 and codes 0 (codes 0 also where a / 127 rounds to 0); one
+ * with a NaN or an infinity in h or t gives xs = NaN and any codes. Squares past fp32's
+ * range (bf16) do not overflow.
  *
  *   x         [M][ldx] of x_dtype W4A4_Y_F16 or W4A4_Y_BF16, 16-byte aligned, ldx % 8 == 0
  *   residual  NULL or [M][ldr], as x
@@ -106,7 +107,7 @@ w4a4_status_t moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E,
  * expert e = ids[t][j], and exact integer products:
  *   h = act(g) * u,  g and u channels 2i and 2i + 1 of w13[e] on (xq[t], xs[t]), as v of
  *       w8a8_gemm_act;  (hq, hs) = INT8 codes and scale of h (the rule of
- *       w8a8_quantize_act, on fp32 values)
+ *       w8a8_quantize_act, on fp32 values, codes held in [-127, 127])
  *   y[t] = sum_j weights[t][j] * fl32(fl32(P') * fl32(hs * s2[e])), P' = w2[e] hq
  * summed over j in order and rounded once. An id outside 0 .. E - 1 adds nothing
  * (experts of another rank; the ids of a token may repeat).

@@ -3,7 +3,7 @@
 //
 //   h = rne16(fl32(x + r))  (h = x without a residual),  t = fl32(h g),
 //   rstd = 1 / sqrt(mean h^2 + eps),  a = max |t|,
-//   q = rne(fl32(t / fl32(a / 127))),  s = fl32(fl32(a rstd) / 127),
+//   q = rne(fl32(t / fl32(a / 127))) within -127 .. 127,  s = fl32(fl32(a rstd) / 127),
 //   y = rne16(fl32(t rstd))
 //
 // q s stands for t rstd. The factor rstd > 0 is common to the row, so it leaves

@@ -1,7 +1,7 @@
 // Device helpers of the INT8 quantizers (w8a8_quantize_act, w8a8_rmsnorm_quantize,
 // w8a8_moe, kv8_append): the rule
-// is a = max|x|, s = fl32(a / 127), q = rne(fl32(x / s)); s is NaN where a value
-// of the row is a NaN or an infinity.
+// is a = max|x|, s = fl32(a / 127), q = rne(fl32(x / s)), within -127 .. 127; s is NaN
+// where a value of the row is a NaN or an infinity.
 #pragma once
 
 #include "quant_common.h"
@@ -57,14 +57,24 @@ __device__ __forceinline__ uint4 codes16(const uint4 r[2], float k, float s, flo
   return uint4{o[0], o[1], o[2], o[3]};
 }
 
-// The codes of 16 fp32 values, as codes16.
+// The codes of 16 fp32 values, as codes16. Their quotients may pass 127: s, off by half a
+// unit of 2^-149, is off by up to a third where a is a few hundred units (16-bit values
+// have a >= 2^-133: 127.2 at most). They stop at 127, which the low byte holds; only rows
+// whose scale is guarded (k) can be such.
 __device__ __forceinline__ uint4 codes16f(const float t[16], float k, float s, float rs) {
+  float q[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) q[i] = div_rn(t[i] * k, s, rs);
+  if (k != 1.0f) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q[i] = __builtin_amdgcn_fmed3f(q[i], -127.0f, 127.0f);
+  }
   uint32_t o[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t b[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(div_rn(t[4 * j + i] * k, s, rs) + 12582912.0f);
+    for (int i = 0; i < 4; ++i) b[i] = __float_as_uint(q[4 * j + i] + 12582912.0f);
     const uint32_t p01 = __builtin_amdgcn_perm(b[1], b[0], 0x0C0C0400u);
     const uint32_t p23 = __builtin_amdgcn_perm(b[3], b[2], 0x04000C0Cu);
     o[j] = p01 | p23;
