@@ -67,3 +67,42 @@ def test_moe_codes_of_subnormal_scales():
         s = (h.abs().amax(dim=1, keepdim=True) / 127).round()     # fl32(a / 127): whole units
         assert bool((h.abs() / s).amax() > 127.5)
         assert torch.equal(y.double(), (h / s).round().clamp(-127, 127) * s), act
+
+
+# ------------------------------------------------------------------- long rows
+
+@pytest.mark.parametrize("K", [65552, 1 << 17, (1 << 20) + 16, 1 << 24])
+def test_norm_of_long_rows(K):
+    """The sum of squares of long rows keeps its bound: rows of one value, and others."""
+    import torch
+    for dtype in (torch.float16, torch.bfloat16):
+        x = torch.full((2, K), 1.7, device="cuda").to(dtype)
+        x[1] = torch.randn(K, generator=gen(K), device="cuda").to(dtype)
+        w = torch.ones(K, dtype=dtype, device="cuda")
+        w[K // 2:] = 0.75
+        for r in (None, torch.ones_like(x)):
+            got = ops().w8a8_rmsnorm_quantize(x, w, residual=r)
+            h, q, s, _ = norm_ref(x, w, 1e-6, r)
+            assert np.array_equal(got[0].cpu().numpy(), q)
+            assert_within(got[1], s, 76 * U * s, f"scale {dtype}")
+    big = torch.full((1, K), 3e25, dtype=torch.bfloat16, device="cuda")       # squares past fp32's range
+    s = norm_ref(big, w, 1e-6)[2]
+    assert_within(ops().w8a8_rmsnorm_quantize(big, w)[1], s, 76 * U * s, "scale, rescaled")
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_norm_of_more_than_2_22_rows(residual):
+    """Rows past a launch's 2^22, in every input and output."""
+    import torch
+    M, K = (1 << 22) + 37, 16
+    x = torch.randn(M, K, generator=gen(1), device="cuda").half()
+    r = torch.randn(M, K, generator=gen(2), device="cuda").half() if residual else None
+    w = torch.rand(K, generator=gen(3), device="cuda") + 0.5
+    got = ops().w8a8_rmsnorm_quantize(x, w, residual=r, return_normed=True)
+    m = (1 << 22) - 40
+    part = ops().w8a8_rmsnorm_quantize(x[m:].clone(), w, residual=r[m:].clone() if residual else None, return_normed=True)
+    for a, b in zip(got, part):
+        assert torch.equal(a[m:], b)
+    h, q, s, y = norm_ref(x[:64], w, 1e-6, r[:64] if residual else None)
+    assert np.array_equal(got[0][:64].cpu().numpy(), q)
+    assert_within(got[1][:64], s, 76 * U * s, "scale")

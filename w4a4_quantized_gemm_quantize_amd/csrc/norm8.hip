@@ -9,9 +9,10 @@
 // q s stands for t rstd. The factor rstd > 0 is common to the row, so it leaves
 // the codes as they are: sum and maximum come out of one pass and one reduction,
 // and the codes depend on no rounding of a sum. h is rounded before the norm
-// because that is what the residual stream holds afterwards. Sums are fp32, 16
-// NC squares per lane and then a tree. A row with a NaN or an infinity (in h or
-// t) has scale NaN.
+// because that is what the residual stream holds afterwards. Sums are fp32: a lane's
+// chunks of 16 squares, at most 4 of them in one chain, more with the rounding of each
+// addition carried along (a row of 2^24 equal values was off by 6e-5 in one chain of 2^15
+// squares a lane), then a tree. A row with a NaN or an infinity (in h or t) has scale NaN.
 //
 // Bound by HBM: 4096 x 8192 bf16 with a residual, 7 bytes per element, 47.7 us, 4.9 TB/s (a
 // copy by PyTorch 5.3); without, 3 bytes, 24 us, 4.2 TB/s (w8a8_quantize_act, which has no
@@ -136,14 +137,21 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_rmsnorm(NormParams p) {
     return sum;
   };
 
+  // sum + part, where a lane sums many parts: `lost` is what the sums so far rounded away
+  auto carry = [](float sum, float part, float& lost) {
+    const float add = part - lost, s = sum + add;
+    lost = s < __builtin_inff() ? s - sum - add : 0.0f;   // an infinite sum stays one
+    return s;
+  };
+
   uint4 raw[NC > 0 ? NC : 1][2];
-  float sum = 0.0f;
+  float sum = 0.0f, lost = 0.0f;
   uint32_t top = 0;
   auto first = [&](const uint4 v[2], int i) {
     float g[16], t[16];
     weights16<BF, W32>(p.w, 16 * i, g);
     terms(v, g, t);
-    sum = squares(v, 1.0f, sum);
+    sum = NC > 0 ? squares(v, 1.0f, sum) : carry(sum, squares(v, 1.0f, 0.0f), lost);
 #pragma unroll
     for (int j = 0; j < 16; ++j) top = max(top, __float_as_uint(t[j]) & 0x7FFFFFFFu);
   };
@@ -206,9 +214,10 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_rmsnorm(NormParams p) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) small = squares(raw[c], 0x1p-80f, small);   // chunks past the row are zeros
     } else {
+      lost = 0.0f;
       for (int i = t0; i < n16; i += 64 * WPR) {
         const uint4 v[2] = {again[2 * i], again[2 * i + 1]};
-        small = squares(v, 0x1p-80f, small);
+        small = carry(small, squares(v, 0x1p-80f, 0.0f), lost);
       }
     }
     small = wave_sum(small);
