@@ -38,7 +38,7 @@ enum {
  *   x         [M][ldx] of x_dtype W4A4_Y_F16 or W4A4_Y_BF16, 16-byte aligned, ldx % 8 == 0
  *   residual  NULL or [M][ldr], as x
  *   weight    [K] of w_dtype W4A4_Y_F32 or x_dtype, 16-byte aligned
- *   eps       > 0, finite
+ *   eps       >= 2^-126 (fp32's smallest normal value), finite
  *   M, K      K > 0, K % 16 == 0, K <= 2^30, M < 2^24
  *   xq, xs    out: int8 [M][K], 16-byte aligned; f32 [M] (the input of w8a8_gemm)
  *   h         out, with a residual: [M][ldh] as x; may be x or residual itself (same

@@ -154,3 +154,12 @@ def test_public_names():
     import w4a4_quantized_gemm_quantize_amd as pkg
     for name in ("w8a8_rmsnorm_quantize", "w8a8_gemm_act", "w8a8_linear_act", "w8a8_pack_gated", "moe_route", "w8a8_moe"):
         assert getattr(pkg, name) is getattr(ops, name)
+
+
+def test_rmsnorm_eps_is_a_normal_number():
+    """Squares below fp32's normal range lose bits that only a larger eps hides."""
+    f = lambda eps: _lib.status_of("w8a8_rmsnorm_quantize", P, F16, 64, None, 0, P, F32, eps, 0, 64, P, P, None, 0, None, 0,
+                                   None)
+    assert f(2.0 ** -126) == OK and f(1e-6) == OK
+    for eps in (2.0 ** -127, 2.0 ** -149, 1e-40):
+        assert f(eps) == E_SHAPE

@@ -298,7 +298,8 @@ w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx,
   if (!x_dtype_ok(x_dtype) || (w_dtype != W4A4_Y_F32 && w_dtype != x_dtype)) return W4A4_E_DTYPE;
   if (M < 0 || M >= kMaxW8Rows || K <= 0 || K % 16 || K > (int64_t{1} << 30) || ldx < K) return W4A4_E_SHAPE;
   if ((residual && (ldr < K || ldh < K)) || (y && ldy < K)) return W4A4_E_SHAPE;
-  if (!(eps > 0.0f) || !(eps < __builtin_inff())) return W4A4_E_SHAPE;
+  // a mean of squares below 2^-126 is off by up to 2^-150: nothing beside a normal eps
+  if (!(eps >= 0x1p-126f) || !(eps < __builtin_inff())) return W4A4_E_SHAPE;
   if (ldx % 8 || (residual && (ldr % 8 || ldh % 8)) || (y && ldy % 8)) return W4A4_E_ALIGN;
   if (M == 0) return W4A4_OK;
   if (!x || !weight || !xq || !xs || (residual && !h)) return W4A4_E_NULL;

@@ -699,8 +699,8 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
     With ``residual`` (X's shape and type) h is x + residual, rounded to X's type, and
     comes third; with ``return_normed`` the normed rows in X's type come last. ``weight``:
     [K], float32 or X's type. ``out``: the tuple of outputs to fill instead; its h may
-    be ``x`` or ``residual`` itself (in place), else they lie apart. Rows that are not finite
-    have NaN scales."""
+    be ``x`` or ``residual`` itself (in place), else they lie apart. ``eps``: at least
+    2^-126. Rows that are not finite have NaN scales."""
     dt = _x_dtype8(x, "x")
     ldx = _rows_stride(x, "x")
     shape, device, dtype = x.shape, x.device, x.dtype
@@ -709,8 +709,8 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
         raise TypeError(f"weight must be a torch.float32 or {dtype} tensor")
     if weight.shape != (K,) or not weight.is_contiguous() or weight.device != device:
         raise ValueError(f"weight must be a contiguous [{K}] tensor on {device}")
-    if not 0.0 < eps < float("inf"):
-        raise ValueError("eps must be positive and finite")
+    if not 2.0 ** -126 <= eps < 2.0 ** 128:
+        raise ValueError("eps must be at least 2^-126 and finite as a float32")
     r = ldr = h = ldh = y = ldy = 0
     if residual is not None:
         ldr = _need_rows(residual, "residual", shape, dtype, device)
