@@ -54,7 +54,8 @@ w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx,
  *   v[m,n] = fl32(fl32(fl32(P) * fl32(xs[m] * ws[n])) + bias[n])
  *   Y[m,n] = act(v[m,n]) + residual[m,n]                       (gated == 0)
  *   Y[m,n] = act(v[m,2n]) * v[m,2n+1] + residual[m,n]          (gated != 0)
- * in fp32, rounded once to y_dtype (W4A4_Y_F16 or W4A4_Y_BF16).
+ * in fp32, rounded once to y_dtype (W4A4_Y_F16 or W4A4_Y_BF16). The residual is +0 where
+ * there is none.
  *
  *   N         outputs. wq, ws, bias hold N channels, or 2 N when gated: channel 2n
  *             is output n's gate, 2n + 1 what it multiplies

@@ -106,3 +106,37 @@ def test_norm_of_more_than_2_22_rows(residual):
     h, q, s, y = norm_ref(x[:64], w, 1e-6, r[:64] if residual else None)
     assert np.array_equal(got[0][:64].cpu().numpy(), q)
     assert_within(got[1][:64], s, 76 * U * s, "scale")
+
+
+# ---------------------------------------------------------------- zeros' signs
+
+@pytest.mark.parametrize("gated", [False, True])
+@pytest.mark.parametrize("act", [None, "relu", "silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("residual", [False, True])
+def test_act_bits_of_zeros(act, gated, residual):
+    """Closed gates and saturated activations: the sign bit of a zero is the same from the
+    streaming kernel, the tiles, and the sums with their join."""
+    import torch
+    o, g = ops(), gen(7)
+    M, N, K = 300, 272, 64
+    C = 2 * N if gated else N
+    q = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
+    wq = torch.randint(-127, 128, (C, K), generator=g, device="cuda", dtype=torch.int8)
+    wq[::5] = 0
+    ws = 0.02 * torch.rand(C, generator=g, device="cuda")           # |v| up to some thousands: sigmoids of 0 and 1
+    s = torch.randn(M, generator=g, device="cuda")
+    s[::7] = 0
+    r = torch.zeros((M, N), dtype=torch.float16, device="cuda") if residual else None
+    if residual:
+        r[::2] = -0.0
+    call = lambda m, out: o.w8a8_gemm_act(q[:m], s[:m], wq, ws, activation=act, gated=gated,
+                                          residual=None if r is None else r[:m], out_dtype=torch.float16, out=out)
+    bits = lambda t: t.contiguous().view(torch.int16)
+    tiles = call(M, None)
+    narrow = torch.empty((M, N + 1), dtype=torch.float16, device="cuda")[:, :N]       # no 16-byte stores: the join
+    assert _lib.workspace_bytes("w8a8_gemm_act_workspace", M, N, K, int(gated), 1) == 0
+    assert _lib.workspace_bytes("w8a8_gemm_act_workspace", M, N, K, int(gated), 0) > 0
+    assert bool((tiles == 0).any())
+    assert torch.equal(bits(call(M, narrow)), bits(tiles))
+    for m in (3, 16):
+        assert torch.equal(bits(call(m, None)), bits(tiles[:m]))

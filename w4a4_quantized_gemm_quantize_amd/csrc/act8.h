@@ -43,7 +43,7 @@ __device__ __forceinline__ float sigmoid_a(int act) { return act == ACT_SILU ? 1
 __device__ __forceinline__ float sigmoid_b(int act) { return act == ACT_SILU ? 0.0f : 0.0713548162726009f; }
 
 // The residual's addition: a rounding of its own on every path, so that all give the
-// same bits.
+// same bits. Without a residual +0 is added, which the tiles read for it: a zero is +0.
 __device__ __forceinline__ float plus(float a, float r) {
 #pragma clang fp contract(off)
   return a + r;

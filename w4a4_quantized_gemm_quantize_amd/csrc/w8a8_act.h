@@ -42,8 +42,7 @@ __global__ __launch_bounds__(kThreads) void k_w8a8_join_act(W8Params p, int spli
     for (int c = 0; c < C; ++c) f[c] = scaled(v[c], sa, sw[c], b[c]);
     float y = activate(p.act, f[0]);
     if constexpr (EPI == EPI_GATED) y *= f[1];
-    if (p.res) y = plus(y, load16(p.res, p.ydtype, m * p.ldr + n));
-    store_y(p.y, p.ydtype, m * p.ldy + n, y);
+    store_y(p.y, p.ydtype, m * p.ldy + n, plus(y, p.res ? load16(p.res, p.ydtype, m * p.ldr + n) : 0.0f));
   }
 }
 

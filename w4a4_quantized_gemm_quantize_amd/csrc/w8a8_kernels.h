@@ -213,8 +213,7 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
       f = activate(p.act, f);
       if constexpr (EPI == EPI_GATED) f *= up;
       if (m < p.M && n < p.N && (EPI == EPI_ACT || !(c & 1))) {
-        if (p.res) f = plus(f, load16(p.res, p.ydtype, m * p.ldr + at));
-        store_y(p.y, p.ydtype, m * p.ldy + at, f);
+        store_y(p.y, p.ydtype, m * p.ldy + at, plus(f, p.res ? load16(p.res, p.ydtype, m * p.ldr + at) : 0.0f));
       }
     }
   }
