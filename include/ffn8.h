@@ -61,7 +61,7 @@ w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx,
  *             is output n's gate, 2n + 1 what it multiplies
  *   residual  NULL or [M][ldr] of y_dtype; may be y itself (same pointer and stride),
  *             else must not overlap y (nor may the other inputs)
- *   xq, xs, wq, ws, bias, M, K, y, ldy: as for w8a8_gemm (channels < 2^22)
+ *   xq, xs, wq, ws, bias, M, K, y, ldy: as for w8a8_gemm (channels <= 2^22 - 4)
  *   workspace at least w8a8_gemm_act_workspace(M, N, K, gated, wide) bytes, 16-byte
  *             aligned, overwritten; may be NULL when that is 0
  */

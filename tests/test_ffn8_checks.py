@@ -163,3 +163,17 @@ def test_rmsnorm_eps_is_a_normal_number():
     assert f(2.0 ** -126) == OK and f(1e-6) == OK
     for eps in (2.0 ** -127, 2.0 ** -149, 1e-40):
         assert f(eps) == E_SHAPE
+
+
+def test_act_channels_whose_padded_sums_reach_2_31_bytes():
+    """128 rows of 2^22 int32 sums are 2^31 bytes, more than a buffer resource spans: 2^22 - 3 channels pad to that."""
+    gemm, lin = _lib.load_library().w8a8_gemm_act_workspace, _lib.load_library().w8a8_linear_act_workspace
+    top = (1 << 22) - 4
+    for N, gated in [(top + 1, 0), (top + 3, 0), ((top + 2) // 2, 1)]:
+        assert gemm(32, N, 64, gated, 0) == -1 and lin(32, N, 64, gated, 0) == -1
+        for f in (gemm_act, linear_act):
+            assert f(N=N, ldy=N, gated=gated, wb=1 << 62) == E_SHAPE and f(M=0, N=N, ldy=N, gated=gated) == E_SHAPE
+    for N, gated in [(top, 0), (top // 2, 1)]:
+        assert gemm(32, N, 64, gated, 0) == 32 * top * 4
+        for f in (gemm_act, linear_act):
+            assert f(M=0, N=N, ldy=N, gated=gated) == OK

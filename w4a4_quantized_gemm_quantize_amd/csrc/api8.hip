@@ -318,9 +318,11 @@ w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx,
 
 // Channels of W for N outputs, and the extents of such a product.
 static int64_t act_channels(int64_t N, int32_t gated) { return gated ? 2 * N : N; }
-// Channels below 2^22: a tile's 128 rows of int32 sums span less than 2^31 bytes.
+// Channels up to 2^22 - 4: a tile's 128 rows of int32 sums, padded to multiples of 4, span
+// less than 2^31 bytes.
 static bool act_extents_ok(int64_t M, int64_t N, int64_t K, int32_t gated) {
-  return N >= 0 && N < kMaxW8Rows && act_channels(N, gated) < (int64_t{1} << 22) && w8_extents_ok(M, act_channels(N, gated), K);
+  return N >= 0 && N < kMaxW8Rows && act_channels(N, gated) <= (int64_t{1} << 22) - 4 &&
+         w8_extents_ok(M, act_channels(N, gated), K);
 }
 
 int64_t w8a8_gemm_act_workspace(int64_t M, int64_t N, int64_t K, int32_t gated, int32_t wide) {
