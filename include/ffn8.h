@@ -43,7 +43,8 @@ enum {
  *   xq, xs    out: int8 [M][K], 16-byte aligned; f32 [M] (the input of w8a8_gemm)
  *   h         out, with a residual: [M][ldh] as x; may be x or residual itself (same
  *             pointer and stride), else must not overlap them
- *   y         out: NULL or [M][ldy] as x, apart from the inputs
+ *   y         out: NULL or [M][ldy] as x
+ * The outputs lie apart from one another and, but for h, from the inputs.
  */
 w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx, const void* residual, int64_t ldr,
                                     const void* weight, int32_t w_dtype, float eps, int64_t M, int64_t K,
@@ -98,7 +99,7 @@ int64_t w8a8_linear_act_workspace(int64_t M, int64_t N, int64_t K, int32_t gated
  * finite value.
  *
  *   logits   [T][ldl] of dtype (any W4A4_Y_*), ldl >= E;  E <= 512, 0 < k <= 64, T < 2^24
- *   ids      out: int32 [T][k];  weights  out: f32 [T][k]
+ *   ids      out: int32 [T][k];  weights  out: f32 [T][k], apart and apart from logits
  */
 w4a4_status_t moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E, int64_t ldl, int64_t k,
                         int32_t renormalize, int32_t* ids, float* weights, void* stream);
@@ -117,7 +118,8 @@ w4a4_status_t moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E,
  *   ids, weights  int32, f32 [T][k], read on the device; T k <= 512
  *   w13, s13 int8 [E][2 I][H], f32 [E][2 I];  w2, s2  int8 [E][H][I], f32 [E][H]; E <= 512
  *   H, I     multiples of 16, <= 131056
- *   y        out: [T][ldy] of y_dtype W4A4_Y_F16 or W4A4_Y_BF16, ldy >= H
+ *   y        out: [T][ldy] of y_dtype W4A4_Y_F16 or W4A4_Y_BF16, ldy >= H, apart from ids,
+ *            weights, w2 and s2
  *   workspace at least w8a8_moe_workspace(T, k, E, H, I) bytes, 16-byte aligned,
  *            overwritten
  */

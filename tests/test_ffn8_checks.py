@@ -177,3 +177,26 @@ def test_act_channels_whose_padded_sums_reach_2_31_bytes():
         assert gemm(32, N, 64, gated, 0) == 32 * top * 4
         for f in (gemm_act, linear_act):
             assert f(M=0, N=N, ldy=N, gated=gated) == OK
+
+
+def test_outputs_apart_from_inputs_and_one_another():
+    t = torch.zeros((8, 64), dtype=torch.float16)
+    raw = torch.zeros(4096, dtype=torch.uint8)
+    codes, scales = raw[:512].view(torch.int8).view(8, 64), raw[512:544].view(torch.float32)
+    w = torch.zeros(64)
+    ops._apart({"xq": codes, "xs": scales}, {"x": t, "weight": w, "residual": None})
+    ops._apart({"a": t[:, :32], "b": t[:, 32:48]}, {"c": t[:, 48:], "d": t[:, 50:60]})     # inputs may meet
+    ops._apart({"a": t[:0], "b": raw[:0]}, {"c": t, "d": raw})
+    ops._apart({"h": t}, {"x": t}, in_place=(("h", "x"),))
+    x = raw[:1024].view(torch.float16).view(8, 64)
+    for outs, ins in [({"xq": codes}, {"x": x}),                                           # a row's codes over another row
+                      ({"xq": raw[1008:1520].view(torch.int8).view(8, 64)}, {"x": x}),     # the last row alone
+                      ({"xs": scales}, {"x": x}), ({"xs": raw[1020:1052].view(torch.float32)}, {"x": x}),
+                      ({"xq": codes, "xs": raw[:32].view(torch.float32)}, {"x": t}),       # outputs on one another
+                      ({"xq": codes, "xs": raw[508:540].view(torch.float32)}, {"x": t}),
+                      ({"xs": w[:8]}, {"x": t, "weight": w}), ({"h": x}, {"x": x}),
+                      ({"y": t[:, :32]}, {"x": t[:, 31:40]})]:
+        with pytest.raises(ValueError):
+            ops._apart(outs, ins)
+    with pytest.raises(ValueError):
+        ops._apart({"h": t[1:]}, {"x": t[:7]}, in_place=(("h", "x"),))

@@ -140,3 +140,52 @@ def test_act_bits_of_zeros(act, gated, residual):
     assert torch.equal(bits(call(M, narrow)), bits(tiles))
     for m in (3, 16):
         assert torch.equal(bits(call(m, None)), bits(tiles[:m]))
+
+
+# ------------------------------------------------------------------- refusals
+
+def test_outputs_on_other_rows_tokens_are_refused():
+    """Codes and scales over tokens that other workgroups still read, and outputs on one another."""
+    import torch
+    o = ops()
+    raw = torch.zeros(1 << 16, dtype=torch.uint8, device="cuda")
+    x = raw[:1024].view(torch.float16).view(8, 64)
+    x.fill_(1)
+    keep = raw.clone()
+    r, w = torch.ones_like(x), torch.ones(64, device="cuda")
+    codes = lambda at: raw[at:at + 512].view(torch.int8).view(8, 64)
+    floats = lambda at: raw[at:at + 32].view(torch.float32)
+    halfs = lambda at: raw[at:at + 1024].view(torch.float16).view(8, 64)
+    fine = (codes(2048), floats(4096), halfs(8192), halfs(16384))
+    for i, bad in [(0, codes(0)), (0, codes(1008)), (1, floats(512)), (1, floats(2048)), (2, halfs(2048)), (2, halfs(4000)),
+                   (3, halfs(2048)), (3, halfs(8192)), (3, halfs(0)), (0, codes(8192)), (1, floats(16384)), (1, w[:8])]:
+        with pytest.raises(ValueError):
+            o.w8a8_rmsnorm_quantize(x, w, residual=r, return_normed=True, out=(*fine[:i], bad, *fine[i + 1:]))
+    for bad in (halfs(0), halfs(512)):
+        with pytest.raises(ValueError):                              # no residual: normed over x
+            o.w8a8_rmsnorm_quantize(x, w, return_normed=True, out=(*fine[:2], bad))
+    q, s = codes(2048), floats(4096)
+    wq, ws = torch.ones((64, 64), dtype=torch.int8, device="cuda"), raw[32768:33024].view(torch.float32)
+    bias = raw[33024:33280].view(torch.float32)
+    for at in (1536, 2048, 2304, 3584, 32256, 33024):
+        with pytest.raises(ValueError):
+            o.w8a8_gemm_act(q, s, wq, ws, bias=bias, out=halfs(at))
+    for at in (0, 512, 32256, 33024):
+        with pytest.raises(ValueError):
+            o.w8a8_linear_act(x, wq, ws, bias=bias, out=halfs(at))
+    logits = raw[:2048].view(torch.float32).view(8, 64)
+    ids = lambda at: raw[at:at + 128].view(torch.int32).view(8, 4)
+    for a, b in [(256, 4096), (4096, 2016), (4096, 4096), (4096, 4160)]:
+        with pytest.raises(ValueError):
+            o.moe_route(logits, 4, out=(ids(a), ids(b).view(torch.float32)))
+    e = [torch.ones(s, dtype=d, device="cuda") for s, d in [((8, 64), torch.int8), ((8,), torch.float32)]]
+    w13, s13 = torch.ones((2, 64, 64), dtype=torch.int8, device="cuda"), torch.ones((2, 64), device="cuda")
+    w2, s2 = raw[40960:45056].view(torch.int8).view(2, 64, 32), raw[45056:45568].view(torch.float32).view(2, 64)
+    some, f = ids(4096), ids(4224).view(torch.float32)
+    for at in (3584, 4096, 4224, 40960, 44544, 45056):
+        with pytest.raises(ValueError):
+            o.w8a8_moe(*e, some, f, w13, s13, w2, s2, out=halfs(at))
+    assert torch.equal(raw, keep)                                    # nothing was launched
+    o.w8a8_rmsnorm_quantize(x, w, residual=r, return_normed=True, out=fine)
+    for a, b in zip(fine, o.w8a8_rmsnorm_quantize(x, w, residual=r, return_normed=True)):
+        assert torch.equal(a, b)

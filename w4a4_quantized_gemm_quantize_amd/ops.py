@@ -690,6 +690,29 @@ def _in_place_or_apart(out, t, names: str) -> None:
         raise ValueError(f"{names} overlap without being the same tensor")
 
 
+def _span(t):
+    """The addresses [first, end) of a tensor that is contiguous, or 2-D with contiguous rows."""
+    start, n = t.data_ptr(), t.numel()
+    if n and t.dim() == 2:
+        rows, cols = t.shape
+        n = (rows - 1) * t.stride(0) + cols
+    return start, start + n * t.element_size()
+
+
+def _apart(outs: dict, ins: dict, in_place=()) -> None:
+    """Refuses outputs that share memory with an input or with one another. ``in_place``:
+    the pairs of names that may also be the same tensor."""
+    rest = [(name, t, *_span(t)) for name, t in (*outs.items(), *ins.items()) if t is not None]
+    for _ in outs:
+        name, a, a0, a1 = rest.pop(0)
+        for other, b, b0, b1 in rest:
+            if a0 < b1 and b0 < a1:
+                if (name, other) in in_place:
+                    _in_place_or_apart(a, b, f"{name} and {other}")
+                elif a.dim() != 2 or b.dim() != 2 or _overlap(a, b):
+                    raise ValueError(f"{name} overlaps {other}")
+
+
 def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=None, return_normed: bool = False,
                           out=None):
     """RMS norm of fp16 or bf16 X[M, K] (row stride may exceed K) to INT8 codes and one
@@ -699,8 +722,8 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
     With ``residual`` (X's shape and type) h is x + residual, rounded to X's type, and
     comes third; with ``return_normed`` the normed rows in X's type come last. ``weight``:
     [K], float32 or X's type. ``out``: the tuple of outputs to fill instead; its h may
-    be ``x`` or ``residual`` itself (in place), else they lie apart. ``eps``: at least
-    2^-126. Rows that are not finite have NaN scales."""
+    be ``x`` or ``residual`` itself (in place), else the outputs lie apart from one another
+    and from the inputs. ``eps``: at least 2^-126. Rows that are not finite have NaN scales."""
     dt = _x_dtype8(x, "x")
     ldx = _rows_stride(x, "x")
     shape, device, dtype = x.shape, x.device, x.dtype
@@ -737,14 +760,11 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
         if residual is not None:
             ldh = _need_rows(out[2], "h", shape, dtype, device)
             h = out[2].data_ptr()
-            _in_place_or_apart(out[2], x, "h and x")
-            _in_place_or_apart(out[2], residual, "h and residual")
         if return_normed:
             ldy = _need_rows(out[-1], "normed", shape, dtype, device)
             y = out[-1].data_ptr()
-            for t in (x, *((residual, out[2]) if residual is not None else ())):
-                if _overlap(out[-1], t):
-                    raise ValueError("normed overlaps x, residual or h")
+        _apart({"h": out[2] if residual is not None else None, "xq": xq, "xs": xs, "normed": out[-1] if return_normed else None},
+               {"x": x, "residual": residual, "weight": weight}, in_place=(("h", "x"), ("h", "residual")))
     _call8("w8a8_rmsnorm_quantize", device, x.data_ptr(), dt, ldx, r, ldr, weight.data_ptr(), _DTYPE8[weight.dtype], eps,
            M, K, xq.data_ptr(), xs.data_ptr(), h, ldh, y, ldy)
     return out
@@ -794,7 +814,8 @@ def w8a8_gemm_act(xq, xs, wq, ws, bias=None, activation=None, gated: bool = Fals
 
     ``activation``: None, "relu", "silu", "gelu" or "gelu_tanh". ``gated``: ``wq`` [2 N, K] as
     :func:`w8a8_pack_gated` lays it out, and Y[m, n] = act(v[m, 2n]) * v[m, 2n + 1] +
-    residual; ``bias`` is interleaved alike. ``residual``: [M, N] of Y's type; ``out`` may be it."""
+    residual; ``bias`` is interleaved alike. ``residual``: [M, N] of Y's type; ``out`` may be
+    it, and lies apart from every other input."""
     _need(xq, torch.int8, "xq")
     _need(xs, torch.float32, "xs")
     if xq.dim() != 2 or not xq.is_contiguous() or not xs.is_contiguous():
@@ -808,6 +829,8 @@ def w8a8_gemm_act(xq, xs, wq, ws, bias=None, activation=None, gated: bool = Fals
     N, K, ldr, y, dt, ldy, wide = _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out)
     if xq.shape[1] != K:
         raise ValueError("K of xq and wq differ")
+    if out is not None:
+        _apart({"out": y}, {"xq": xq, "xs": xs, "wq": wq, "ws": ws, "bias": bias})
     held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_gemm_act_workspace", M, N, K, gated, wide), device)
     _call8("w8a8_gemm_act", device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
            0 if bias is None else bias.data_ptr(), act, gated, 0 if residual is None else residual.data_ptr(), ldr,
@@ -820,7 +843,7 @@ def w8a8_linear_act(x: torch.Tensor, wq, ws, bias=None, activation=None, gated: 
     """:func:`w8a8_linear` with the epilogue of :func:`w8a8_gemm_act`: fp16 or bf16
     activations [M, K] quantized per token, the product, bias, activation or gate, and
     residual, in one call. ``out`` may be ``residual`` but not overlap ``x``, which every
-    workgroup reads."""
+    workgroup reads, or another input."""
     xdt = _x_dtype8(x, "x")
     ld = _rows_stride(x, "x")
     M = x.shape[0]
@@ -829,8 +852,8 @@ def w8a8_linear_act(x: torch.Tensor, wq, ws, bias=None, activation=None, gated: 
     N, K, ldr, y, dt, ldy, wide = _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out)
     if x.shape[1] != K:
         raise ValueError("K of x and wq differ")
-    if out is not None and _overlap(x, out):
-        raise ValueError("out overlaps x")
+    if out is not None:
+        _apart({"out": y}, {"x": x, "wq": wq, "ws": ws, "bias": bias})
     held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_linear_act_workspace", M, N, K, gated, wide), device)
     _call8("w8a8_linear_act", device, x.data_ptr(), xdt, M, K, ld, wq.data_ptr(), ws.data_ptr(),
            0 if bias is None else bias.data_ptr(), act, gated, 0 if residual is None else residual.data_ptr(), ldr,
@@ -857,6 +880,7 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out=No
         ids, weights = out
         _check_out(ids, "ids", (T, k), torch.int32, logits.device)
         _check_out(weights, "weights", (T, k), torch.float32, logits.device)
+        _apart({"ids": ids, "weights": weights}, {"logits": logits})
     _call8("moe_route", logits.device, logits.data_ptr(), dt, T, E, ld, k, int(bool(renormalize)), ids.data_ptr(),
            weights.data_ptr())
     return ids, weights
@@ -917,6 +941,7 @@ def w8a8_moe(xq, xs, ids, weights, w13, s13, w2, s2, activation="silu", out_dtyp
     else:
         y = out
         _check_out(y, "out", (T, H), getattr(y, "dtype", None), device, row_stride_ok=True)
+        _apart({"out": y}, {"ids": ids, "weights": weights, "w2": w2, "s2": s2})       # read until the last store
     dt = _x_dtype8(y, "out")
     held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_moe_workspace", T, k, E, H, I), device)
     _call8("w8a8_moe", device, xq.data_ptr(), xs.data_ptr(), ids.data_ptr(), weights.data_ptr(), T, k, w13.data_ptr(),
