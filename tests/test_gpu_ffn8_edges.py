@@ -142,6 +142,23 @@ def test_act_bits_of_zeros(act, gated, residual):
         assert torch.equal(bits(call(m, None)), bits(tiles[:m]))
 
 
+# ------------------------------------------------ 9 to 16 tokens of few channels
+
+@pytest.mark.parametrize("M,N,K", [(9, 200, 33040), (16, 2048, 32784), (13, 17, 65536), (16, 640, 131056)])
+def test_few_channels_of_long_k(M, N, K):
+    """In tiles of K ranges, as 8 of the tokens from the streaming kernel."""
+    import torch
+    o = ops()
+    x, q, s, wq, ws, b, r, y = act_case(M, N, K, "silu", False, True, True, torch.float16, seed=K)
+    assert torch.equal(y[:8], o.w8a8_gemm_act(q[:8], s[:8], wq, ws, bias=b, activation="silu", residual=r[:8]))
+    for dtype in (torch.float32, torch.bfloat16):
+        full = o.w8a8_gemm(q, s, wq, ws, bias=b, out_dtype=dtype)
+        assert torch.equal(full[-8:], o.w8a8_gemm(q[-8:], s[-8:], wq, ws, bias=b, out_dtype=dtype))
+        assert torch.equal(full, o.w8a8_linear(x, wq, ws, bias=b, out_dtype=dtype))
+    if N % 2 == 0:
+        act_case(M, N // 2, K, "gelu", True, False, True, torch.bfloat16, seed=N)
+
+
 # ------------------------------------------------------------------- refusals
 
 def test_outputs_on_other_rows_tokens_are_refused():

@@ -140,3 +140,14 @@ def test_public_names():
     import w4a4_quantized_gemm_quantize_amd as pkg
     for name in ("w8a8_linear", "w8a8_gemm", "kv8_new_cache", "kv8_append", "kv8_gather", "kv8_attention"):
         assert getattr(pkg, name) is getattr(ops, name)
+
+
+def test_nine_to_sixteen_tokens_of_few_channels_and_long_k_split_k():
+    """Tiles in K ranges, which need a workspace, where 16 channels a workgroup would leave CUs idle."""
+    w = _lib.load_library().w8a8_gemm_workspace
+    for M in (9, 16):
+        for N, K in [(16, 131056), (640, 40960), (1024, 98304), (2048, 53248), (2048, 32784)]:
+            assert w(M, N, K) >= 2 * M * N * 4, (M, N, K)
+        for N, K in [(2048, 28672), (1024, 16384), (2064, 53248), (8192, 28672)]:
+            assert w(M, N, K) == 0, (M, N, K)
+    assert w(8, 1024, 98304) == 0

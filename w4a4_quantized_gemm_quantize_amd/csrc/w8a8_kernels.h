@@ -646,9 +646,14 @@ void k_w8a8_gemm_tiles(W8Params p) {
 //
 // Up to 16 tokens the W stream decides (k_w8a8_gemm_small; us there and in tiles, W
 // from HBM: 16 x 28672 x 8192 46 and 53, 16 x 8192 x 28672 45 and 50, 16 x 18944 x 3584
-// 16.5 and 19.4, 9 x the same 15.6 and 19.3, 16 x 4096 x 14336 15 both).
+// 16.5 and 19.4, 9 x the same 15.6 and 19.3, 16 x 4096 x 14336 15 both), but for 9 to 16
+// tokens of few channels and long K, whose 128 workgroups or fewer leave CUs idle while
+// tiles split K (16 x 2048 x 53248 37.6 and 31.5, 16 x 1024 x 98304 63.8 and 35.9, 9 x the
+// same 54.0 and 34.7, 9 x 2048 x 36864 27.8 and 24.1, 16 x 640 x 40960 26.9 and 19.8; shorter
+// or wider: 16 x 2048 x 28672 21.7 and 22.5, 9 x 2304 x 40960 28.8 and 31.1, 16 x 1024 x 16384
+// 12.2 and 15.0).
 //
-// Above 16 tokens, the tile whose estimated time is least: rounds of tiles over
+// Above 16 tokens and for those, the tile whose estimated time is least: rounds of tiles over
 // the CUs times (stages x the tile's time per 128-k stage + its start and
 // output). The times (us: 256 x 256 tiles 1.6 a stage, 256 x 128 0.95, 128 x 128
 // 0.55) are fitted to measured shapes, tokens x channels x K, among them those named
@@ -663,8 +668,9 @@ struct W8Plan {
   int tile, splits;
   double us;              // the estimate
 };
+constexpr int64_t kFewChannels = 8 * kCUs, kLongK = 32768;
 W8Plan plan_w8a8(int64_t M, int64_t N, int64_t K) {
-  if (M <= 16) return W8Plan{TILE_SMALL, 1, 4.0 + N * K / 5.2e6};
+  if (M <= 8 || (M <= 16 && (N > kFewChannels || K <= kLongK))) return W8Plan{TILE_SMALL, 1, 4.0 + N * K / 5.2e6};
   const int64_t nk = (K + 127) / 128;
   W8Plan best{TILE_256, 1, 1e30};
   auto consider = [&](int tile, int64_t bm, int64_t bn, double stage, double start, int splits) {
