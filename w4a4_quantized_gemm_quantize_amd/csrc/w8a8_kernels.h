@@ -705,23 +705,34 @@ W8Params params(const W8GemmArgs& a) {
   return p;
 }
 
-// 4 waves a workgroup where its count fills the CUs twice over, else 8 (one
-// token, W from HBM, us: 8192 x 8192 14.0 with 4 and 15.1 with 8, 4096 x 11008
-// 13.4 and 11.1, 1024 x 8192 9.2 and 6.8).
-bool four_waves(int64_t N) { return N >= 32 * kCUs; }
+// 4 or 8 waves a workgroup. With 16 channels each, more than one a CU are better of 4 (W
+// from HBM, us, 4 waves and 8: 9 x 6144 x 8192 13.4 and 14.7, 16 x 5120 x 27648 39.9 and
+// 42.9, one token 6144 x 8192 12.3 and 13.8, 16 x 8192 x 8192 15.8 and 16.7; 16 x 4096 x 8192
+// 11.6 and 10.0, one token 1024 x 8192 9.8 and 7.2), but for up to 4 tokens of the widest
+// and longest W, which more loads in flight stream faster (one token 28672 x 8192 45.9
+// and 42.2, 14336 x 8192 26.6 and 25.4, 28672 x 14336 79.9 and 75.2; 8 x 14336 x 8192 26.8 and
+// 27.0, 16 x 14336 x 8192 27.9 and 29.0, one token 11008 x 8192 19.4 and 19.9).
+bool four_waves(int64_t M, int64_t N, int64_t K) {
+  return N > 16 * kCUs && !(M <= 4 && N >= 56 * kCUs && K >= 8192);
+}
+// Where a workgroup quantizes the tokens too, 8 waves up to twice as many channels (one
+// token 5120 x 4096 7.4 with 8 and 7.8 with 4, 6144 x 28672 36.9 and 41.4).
+bool four_waves_quantizing(int64_t N) { return N >= 32 * kCUs; }
 
 template <int XT, int PIECES, int EPI = EPI_PLAIN>
 void launch_small(const W8Params& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.N + 15) / 16));
   const unsigned lds = XT ? (unsigned)(p.M * ((p.K + 63) / 64 * 64)) : 0;
-  if (four_waves(p.N)) hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 4, PIECES, EPI>), grid, dim3(256), lds, stream, p);
-  else hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 8, PIECES, EPI>), grid, dim3(512), lds, stream, p);
+  if (XT ? four_waves_quantizing(p.N) : four_waves(p.M, p.N, p.K))
+    hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 4, PIECES, EPI>), grid, dim3(256), lds, stream, p);
+  else
+    hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 8, PIECES, EPI>), grid, dim3(512), lds, stream, p);
 }
 
 // Pieces of 1024 elements per wave that a workgroup of k_w8a8_gemm_small has to
 // quantize for all tokens.
 int64_t pieces_per_wave(int64_t M, int64_t N, int64_t K) {
-  const int64_t nw = four_waves(N) ? 4 : 8;
+  const int64_t nw = four_waves_quantizing(N) ? 4 : 8;
   return (M * ((K + 1023) / 1024) + nw - 1) / nw;
 }
 
