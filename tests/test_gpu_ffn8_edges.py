@@ -159,6 +159,22 @@ def test_few_channels_of_long_k(M, N, K):
         act_case(M, N // 2, K, "gelu", True, False, True, torch.bfloat16, seed=N)
 
 
+# ------------------------------------------- few tokens quantized by every workgroup
+
+@pytest.mark.parametrize("M,N,K", [(4, 24600, 2064), (1, 30005, 4176), (8, 8200, 4096), (16, 9000, 512), (8, 8190, 4112)])
+def test_few_tokens_of_many_channels(M, N, K):
+    """One launch, W turned by LDS or not, or two: as the product on the tokens' codes."""
+    import torch
+    o = ops()
+    for i, xdtype in enumerate((torch.float16, torch.bfloat16)):
+        act_case(M, N, K, (None, "relu")[i], False, True, i == 0, (torch.bfloat16, torch.float16)[i], seed=N, xdtype=xdtype)
+        x, q, s, wq, ws, b, _, _ = act_case(M, N // 2, K, "silu", True, False, True, torch.float16, seed=K, xdtype=xdtype)
+        for bias in (None, torch.arange(len(ws), device="cuda").float()):
+            y = o.w8a8_linear(x, wq, ws, bias=bias)
+            assert torch.equal(y, o.w8a8_gemm(q, s, wq, ws, bias=bias))
+            assert torch.equal(y[:1], o.w8a8_linear(x[:1], wq, ws, bias=bias))
+
+
 # ------------------------------------------------------------------- refusals
 
 def test_outputs_on_other_rows_tokens_are_refused():

@@ -167,13 +167,14 @@ void launch_w8a8_gemm(const W8GemmArgs& a, hipStream_t stream) {
   }
 }
 
-// Every workgroup quantizes all tokens, so it pays up to 4 pieces a wave (W
-// from HBM, us, one launch and two): 1 x 11008 x 4096 10.6 and 14.2, 1 x 28672 x
-// 8192 43.7 and 47.5, 4 x 11008 x 4096 (4 pieces) 13.0 and 16.3, 8 x 4096 x 4096
-// (4) 10.1 and 9.8; with 7 and 8 pieces 1 x 8192 x 28672 47.0 and 46.7, 8 x 8192
-// x 4096 14.9 and 13.6.
+// Every workgroup quantizes all tokens, so it pays up to 4 pieces a wave and, of 4 waves,
+// up to 8 tokens (tokens x channels x K, W from HBM, us, one launch and two: 1 x 11008 x 4096
+// 10.4 and 13.4, 1 x 28672 x 8192 42.8 and 45.1, 4 x 11008 x 4096 (4 pieces) 13.0 and 14.2, 8 x
+// 4096 x 4096 (4) 9.2 and 9.3, 8 x 28672 x 1024 (2) 10.7 and 11.6; with 8 pieces 8 x 11008 x
+// 4096 17.6 and 14.6; 16 tokens in 4 waves, 16 x 11008 x 1024 9.4 and 7.9,
+// 16 x 128256 x 1024 57.9 and 36.3, 16 x 28672 x 128 13.5 and 7.7; in 8, 16 x 4096 x 1024 5.6 and 6.4).
 bool w8a8_one_launch(int64_t M, int64_t N, int64_t K) {
-  return plan_w8a8(M, N, K).tile == TILE_SMALL && pieces_per_wave(M, N, K) <= 4;
+  return plan_w8a8(M, N, K).tile == TILE_SMALL && pieces_per_wave(M, N, K) <= 4 && (M <= 8 || !four_waves_quantizing(N));
 }
 
 void launch_w8a8_small(const W8GemmArgs& a, const void* x, int bf16, int64_t ldx, hipStream_t stream) {

@@ -82,17 +82,19 @@ enum { EPI_PLAIN = 0, EPI_ACT = 1, EPI_GATED = 2 };
 // XT 0: the tokens' codes come from memory. XT 1, 2 (fp16, bf16 tokens): every
 // workgroup quantizes all of them itself, in pieces of 1024 elements per wave
 // (PIECES each, kept in registers), into LDS, while its first W loads are on
-// their way; that saves a launch and the wait for it.
+// their way; that saves a launch and the wait for it. Its time is mostly latency, so
+// where the blocks' LDS keeps workgroups from a CU that it could hold, W is loaded
+// straight into the operands (TURN false), a step's refill behind its use.
 //
 // Bound by the W stream: one token 4096 -> 128256 86.9 us, 6.0 TB/s of weights;
 // 8192 -> 28672 44 us, 5.3 TB/s; small ones by the launch and the loads' latency
 // (8192 -> 1024, 8 MB: 5.8 us).
-template <int XT, int NW, int PIECES, int EPI>
+template <int XT, int NW, int PIECES, int EPI, bool TURN>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
   constexpr bool BF = XT == 2;
-  __shared__ int red[NW - 1][4][64];
+  static_assert(TURN || XT > 0, "codes from memory are turned");
   __shared__ float row_scale[16];
-  __shared__ __align__(16) uint8_t turn[NW][4096];
+  __shared__ __align__(16) uint8_t turn[NW][TURN ? 4096 : 1024];   // a wave's block, then its sums
   __shared__ uint32_t row_max[16];
   extern __shared__ __align__(16) uint8_t codes[];     // XT > 0: [M][K rounded up to 64]
   const int lane = threadIdx.x & 63;
@@ -104,20 +106,21 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
   const int w_rows = min(16, p.N - n0);
   const __amdgpu_buffer_rsrc_t rA = buffer_rsrc(p.a, XT ? 0 : p.M * p.K);
   const __amdgpu_buffer_rsrc_t rW = buffer_rsrc(p.w + (int64_t)n0 * p.K, w_rows * p.K);
-  // load j of a block: row 4 j + lane / 16, 16 bytes of its 256
-  const int run_row = lane >> 4, run_k = 16 * (lane & 15);
+  // load j of a block: row 4 j + lane / 16, 16 bytes of its 256; or the operand of step j
+  const int run_row = TURN ? lane >> 4 : c, run_k = 16 * (TURN ? lane & 15 : g);
   v4i next_w[4], next_a[XT ? 1 : 4];
+  auto load1 = [&](int h, int j) {
+    const int row = TURN ? 4 * j + run_row : run_row, at = TURN ? h : h + j;
+    const int out = at < h1 && 64 * at + run_k < p.K ? 0 : kDroppedOffset;
+    next_w[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+        rW, (row < w_rows ? row * p.K + run_k : kDroppedOffset) | out, 64 * at, 0));
+    if constexpr (XT == 0)
+      next_a[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
+          rA, (row < p.M ? row * p.K + run_k : kDroppedOffset) | out, 64 * at, 0));
+  };
   auto load = [&](int h) {
-    const int out = h < h1 && 64 * h + run_k < p.K ? 0 : kDroppedOffset;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int row = 4 * j + run_row;
-      next_w[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
-          rW, (row < w_rows ? row * p.K + run_k : kDroppedOffset) | out, 64 * h, 0));
-      if constexpr (XT == 0)
-        next_a[j] = __builtin_bit_cast(v4i, __builtin_amdgcn_raw_buffer_load_b128(
-            rA, (row < p.M ? row * p.K + run_k : kDroppedOffset) | out, 64 * h, 0));
-    }
+    for (int j = 0; j < 4; ++j) load1(h, j);
   };
   const int KP = steps * 64;
   if constexpr (XT > 0) {
@@ -178,20 +181,26 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
   v4i acc = {0, 0, 0, 0};
   for (int h = h0; h < h1; h += 4) {
     v4i w[4], a[4];
-    operands(next_w, w);
+    if constexpr (TURN) operands(next_w, w);
     if constexpr (XT == 0) {
       operands(next_a, a);
     } else {
 #pragma unroll
       for (int u = 0; u < 4; ++u) a[u] = *reinterpret_cast<const v4i*>(la + 64 * min(h + u, steps - 1));
     }
-    load(h + 4);
+    if constexpr (TURN) load(h + 4);
 #pragma unroll
-    for (int u = 0; u < 4; ++u) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], w[u], acc, 0, 0, 0);
+    for (int u = 0; u < 4; ++u) {
+      if constexpr (!TURN) {
+        w[u] = next_w[u];
+        load1(h + 4, u);
+      }
+      acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[u], w[u], acc, 0, 0, 0);
+    }
   }
   if (wave > 0) {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) red[wave - 1][r][lane] = acc[r];
+    for (int r = 0; r < 4; ++r) reinterpret_cast<int*>(mine)[64 * r + lane] = acc[r];
   }
   __syncthreads();
   if (wave != 0) return;
@@ -202,7 +211,7 @@ __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
   for (int r = 0; r < 4; ++r) {
     int v = acc[r];
 #pragma unroll
-    for (int w = 0; w < NW - 1; ++w) v += red[w][r][lane];
+    for (int w = 1; w < NW; ++w) v += reinterpret_cast<const int*>(turn[w])[64 * r + lane];
     const int m = 4 * g + r;
     if constexpr (EPI == EPI_PLAIN) {
       if (m < p.M && n < p.N) store_y(p.y, p.ydtype, m * p.ldy + n, scaled(v, XT ? row_scale[m] : p.sa[m], sw, b));
@@ -719,14 +728,31 @@ bool four_waves(int64_t M, int64_t N, int64_t K) {
 // token 5120 x 4096 7.4 with 8 and 7.8 with 4, 6144 x 28672 36.9 and 41.4).
 bool four_waves_quantizing(int64_t N) { return N >= 32 * kCUs; }
 
+// Whether the blocks of a quantizing workgroup of 4 waves may take LDS: 8 fit a CU, or
+// all that there are (tokens x channels x K, us, turned and straight: 1 x 11008 x 4096 10.4
+// and 11.1, 3 x 18944 x 4096 17.4 and 19.6, 4 x 18944 x 3584 16.7 and 18.4, 1 x 128256 x 512
+// 17.6 and 18.9; where fewer fit, 4 x 18944 x 4096 21.0 and 20.2, 2 x 18944 x 8192 33.9 and
+// 32.5, 8 x 28672 x 1024 12.3 and 10.7, 1 x 28672 x 8192 45.2 and 43.5).
+bool turns_blocks(int64_t M, int64_t N, int64_t K) {
+  const int64_t lds = 4 * 4096 + 128 + M * ((K + 63) / 64 * 64), fit = 160 * 1024 / lds;
+  return fit >= 8 || (N + 15) / 16 <= fit * kCUs;
+}
+
 template <int XT, int PIECES, int EPI = EPI_PLAIN>
 void launch_small(const W8Params& p, hipStream_t stream) {
   const dim3 grid((unsigned)((p.N + 15) / 16));
   const unsigned lds = XT ? (unsigned)(p.M * ((p.K + 63) / 64 * 64)) : 0;
-  if (XT ? four_waves_quantizing(p.N) : four_waves(p.M, p.N, p.K))
-    hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 4, PIECES, EPI>), grid, dim3(256), lds, stream, p);
-  else
-    hipLaunchKernelGGL((k_w8a8_gemm_small<XT, 8, PIECES, EPI>), grid, dim3(512), lds, stream, p);
+#define W8A8_STREAM(NW, TURN) \
+  hipLaunchKernelGGL((k_w8a8_gemm_small<XT, NW, PIECES, EPI, TURN>), grid, dim3(64 * NW), lds, stream, p)
+  if constexpr (XT == 0) {
+    if (four_waves(p.M, p.N, p.K)) W8A8_STREAM(4, true);
+    else W8A8_STREAM(8, true);
+  } else {
+    if (!four_waves_quantizing(p.N)) W8A8_STREAM(8, true);
+    else if (turns_blocks(p.M, p.N, p.K)) W8A8_STREAM(4, true);
+    else W8A8_STREAM(4, false);
+  }
+#undef W8A8_STREAM
 }
 
 // Pieces of 1024 elements per wave that a workgroup of k_w8a8_gemm_small has to
