@@ -1,5 +1,6 @@
 """Edges of what surrounds the W8A8 products: scales of a few subnormal units, rows of
-2^20 values and more, zeros' signs, GELU's tail, launches whose last tokens go apart.
+2^20 values and more, zeros' signs, GELU's tail, launches whose last tokens go apart, 9 to
+16 tokens of few channels, tokens quantized by every workgroup, outputs on inputs.
 
 Tolerances as in test_gpu_ffn8.py (u = 2^-24), whose references are used here."""
 import math
@@ -7,7 +8,7 @@ import math
 import numpy as np
 import pytest
 
-from test_gpu_ffn8 import U, act_case, assert_within, check_epilogue, gen, half_of, norm_ref, ops
+from test_gpu_ffn8 import U, act_case, assert_within, gen, half_of, norm_ref, ops
 
 from w4a4_quantized_gemm_quantize_amd import _lib
 
@@ -140,6 +141,78 @@ def test_act_bits_of_zeros(act, gated, residual):
     assert torch.equal(bits(call(M, narrow)), bits(tiles))
     for m in (3, 16):
         assert torch.equal(bits(call(m, None)), bits(tiles[:m]))
+
+
+# ------------------------------------------------------------------ GELU's tail
+
+@pytest.mark.parametrize("dtype", ["float16", "bfloat16"])
+def test_gelu_tail(dtype):
+    """v Phi(v) from -13 up, without a residual and with one that takes its leading bits away."""
+    import torch
+    o, N, K = ops(), 4096, 16
+    dtype = getattr(torch, dtype)
+    v = torch.linspace(-13, 6, N, device="cuda")
+    wq = torch.zeros((N, K), dtype=torch.int8, device="cuda")
+    wq[:, 0] = torch.where(v < 0, -1, 1).to(torch.int8)
+    ws = v.abs()
+    v = v.double()
+    r = v.abs() * torch.special.erfc(v.abs() / math.sqrt(2)) / 2      # |v| Phi(-|v|)
+    y = v.clamp_min(0) - r
+    z = v.abs().clamp_max(16)
+    bound = r * (z * z + 32) * 2 * U + U * y.abs()                    # v itself is exact
+    rel, tiny = half_of(dtype)
+    back = -y.to(dtype)                                               # with it: act(v) - rounded act(v)
+    for M in (1, 16, 40):
+        q = torch.zeros((M, K), dtype=torch.int8, device="cuda")
+        q[:, 0] = 1
+        s = torch.ones(M, device="cuda")
+        got = o.w8a8_gemm_act(q, s, wq, ws, activation="gelu", out_dtype=dtype)
+        assert_within(got, y.expand(M, N), bound * (1 + rel) + rel * y.abs() + tiny, "Y")
+        got = o.w8a8_gemm_act(q, s, wq, ws, activation="gelu", residual=back.expand(M, N).contiguous(), out_dtype=dtype)
+        left = y + back.double()
+        assert_within(got, left.expand(M, N), (bound + U * left.abs()) * (1 + rel) + rel * left.abs() + tiny, "Y - round(Y)")
+        odd = torch.empty((M, N + 1), dtype=dtype, device="cuda")[:, :N]
+        assert torch.equal(o.w8a8_gemm_act(q, s, wq, ws, activation="gelu", out=odd),
+                           o.w8a8_gemm_act(q, s, wq, ws, activation="gelu", out_dtype=dtype))
+
+
+# ------------------------------------- the last tokens in a launch of their own
+
+# (tokens, outputs, K, gated, bytes of int32 sums): the tail in 8 K ranges behind whole tiles; in whole tiles itself; both
+# launches in K ranges, 2 of them for the first one's 512 tokens, in one workspace
+TAILS = [(2070, 4096, 4096, False, 8 * 22 * 4096 * 4), (1185, 16192, 1760, True, 0),
+         (530, 3840, 23888, False, 2 * 512 * 3840 * 4)]
+
+
+@pytest.mark.parametrize("M,N,K,gated,sums", TAILS)
+def test_act_last_tokens_in_tiles_of_their_own(M, N, K, gated, sums):
+    import torch
+    o = ops()
+    dtype = torch.bfloat16
+    need = _lib.workspace_bytes("w8a8_gemm_act_workspace", M, N, K, int(gated), 1)
+    assert need == sums                                              # the launch that is meant
+    x, q, s, wq, ws, b, r, y = act_case(M, N, K, "silu", gated, True, True, dtype, seed=3)
+    guard = 1 << 16
+    space = torch.full((need + guard,), 0x5A, dtype=torch.uint8, device="cuda")
+    out = r.clone()
+    o.w8a8_gemm_act(q, s, wq, ws, bias=b, activation="silu", gated=gated, residual=out, out=out, workspace=space[:need])
+    assert torch.equal(out, y) and bool((space[need:] == 0x5A).all())
+    m = M // 256 * 256
+    for rows in (slice(0, m), slice(m, M)):                          # each part as a call of its own
+        assert torch.equal(o.w8a8_gemm_act(q[rows].contiguous(), s[rows].contiguous(), wq, ws, bias=b, activation="silu",
+                                           gated=gated, residual=r[rows], out_dtype=dtype), y[rows])
+    total = _lib.workspace_bytes("w8a8_linear_act_workspace", M, N, K, int(gated), 1)
+    space = torch.full((total + guard,), 0x5A, dtype=torch.uint8, device="cuda")
+    out.copy_(r)
+    o.w8a8_linear_act(x, wq, ws, bias=b, activation="silu", gated=gated, residual=out, out=out, workspace=space[:total])
+    assert torch.equal(out, y) and bool((space[total:] == 0x5A).all())
+    wide = torch.full((M + 2, N + 24), 7.0, dtype=dtype, device="cuda")
+    view = wide[1:M + 1, 8:8 + N]
+    view.copy_(r)
+    o.w8a8_gemm_act(q, s, wq, ws, bias=b, activation="silu", gated=gated, residual=view, out=view)
+    assert torch.equal(view, y)
+    view.fill_(7)
+    assert bool((wide == 7).all())
 
 
 # ------------------------------------------------ 9 to 16 tokens of few channels
