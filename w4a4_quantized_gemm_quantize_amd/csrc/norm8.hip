@@ -14,9 +14,9 @@
 // addition carried along (a row of 2^24 equal values was off by 6e-5 in one chain of 2^15
 // squares a lane), then a tree. A row with a NaN or an infinity (in h or t) has scale NaN.
 //
-// Bound by HBM: 4096 x 8192 bf16 with a residual, 7 bytes per element, 47.7 us, 4.9 TB/s (a
-// copy by PyTorch 5.3); without, 3 bytes, 24 us, 4.2 TB/s (w8a8_quantize_act, which has no
-// weights to read, 20.7 in the same loop); one row of 4096 2.7 us, a launch. Tried: weights
+// Bound by HBM: 4096 x 8192 bf16 with a residual, 7 bytes per element, 42 to 48 us from card
+// to card, 4.9 to 5.6 TB/s (a copy by PyTorch 5.3); without, 3 bytes, 24 to 27 us, 3.8 to 4.2
+// TB/s (w8a8_quantize_act, which has no weights to read, 20.7 in the same loop); one row of 4096 2.7 us, a launch. Tried: weights
 // kept in registers over several rows with the next row on its way 45.5 and 24.2 us, rows of
 // 28672 slower (24.1 -> 27.3), not kept; non-temporal stores 46.9 and 20.0, but what reads
 // the codes next pays more (the norm and a reader of the codes 122.8 -> 152.8).

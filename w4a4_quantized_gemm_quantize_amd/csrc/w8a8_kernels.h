@@ -76,8 +76,8 @@ enum { EPI_PLAIN = 0, EPI_ACT = 1, EPI_GATED = 2 };
 // pieces of 16 bytes, and the cache serves about 0.65 of them a clock. Blocks are
 // loaded in whole runs of a row, 256 bytes for 16 lanes, and turned by LDS (us, W from
 // HBM, tokens x channels x K, loads straight into the operands and these: 16 x 8192 x 8192
-// 20 and 15; 8 x 28672 x 8192 57 and 43; 16 x 4096 x 11008 17.2 and 13; 8 x 11008 x 4096 15.0 and
-// 12.1; one token 4096 x 11008 11.9 and 11.7, 1024 x 8192 7.3 and 5.8).
+// 20.5 and 15.7; 8 x 28672 x 8192 54 and 45; 16 x 4096 x 11008 17.9 and 13.9; 8 x 11008 x 4096 14.3
+// and 11.7; one token 4096 x 11008 12.4 and 12.1, 1024 x 8192 7.4 and 6.8).
 //
 // XT 0: the tokens' codes come from memory. XT 1, 2 (fp16, bf16 tokens): every
 // workgroup quantizes all of them itself, in pieces of 1024 elements per wave
@@ -87,8 +87,8 @@ enum { EPI_PLAIN = 0, EPI_ACT = 1, EPI_GATED = 2 };
 // straight into the operands (TURN false), a step's refill behind its use.
 //
 // Bound by the W stream: one token 4096 -> 128256 86.9 us, 6.0 TB/s of weights;
-// 8192 -> 28672 44 us, 5.3 TB/s; small ones by the launch and the loads' latency
-// (8192 -> 1024, 8 MB: 5.8 us).
+// 8192 -> 28672 42.3 us, 5.6 TB/s; small ones by the launch and the loads' latency
+// (8192 -> 1024, 8 MB: 6.8 us).
 template <int XT, int NW, int PIECES, int EPI, bool TURN>
 __global__ __launch_bounds__(64 * NW) void k_w8a8_gemm_small(W8Params p) {
   constexpr bool BF = XT == 2;
@@ -654,13 +654,15 @@ void k_w8a8_gemm_tiles(W8Params p) {
 // Which kernel, and into how many K ranges.
 //
 // Up to 16 tokens the W stream decides (k_w8a8_gemm_small; us there and in tiles, W
-// from HBM: 16 x 28672 x 8192 46 and 53, 16 x 8192 x 28672 45 and 50, 16 x 18944 x 3584
-// 16.5 and 19.4, 9 x the same 15.6 and 19.3, 16 x 4096 x 14336 15 both), but for 9 to 16
-// tokens of few channels and long K, whose 128 workgroups or fewer leave CUs idle while
-// tiles split K (16 x 2048 x 53248 37.6 and 31.5, 16 x 1024 x 98304 63.8 and 35.9, 9 x the
-// same 54.0 and 34.7, 9 x 2048 x 36864 27.8 and 24.1, 16 x 640 x 40960 26.9 and 19.8; shorter
-// or wider: 16 x 2048 x 28672 21.7 and 22.5, 9 x 2304 x 40960 28.8 and 31.1, 16 x 1024 x 16384
-// 12.2 and 15.0).
+// from HBM: 16 x 28672 x 8192 48 and 57, 16 x 8192 x 28672 47.5 both, 16 x 18944 x 3584
+// 16.9 and 20.0, 9 x the same 16.2 and 19.6, 16 x 4096 x 14336 15.5 and 22.4). Of 9 to 16
+// tokens, few channels of long K go to tiles: 128 workgroups or fewer leave CUs idle
+// while tiles split K (16 x 2048 x 53248 37.6 and 31.5, 16 x 1024 x 98304 63.8 and 35.9, 9 x
+// the same 54.0 and 34.7, 9 x 2048 x 36864 27.8 and 24.1, 16 x 640 x 40960 26.9 and 19.8;
+// shorter or wider: 16 x 2048 x 28672 21.7 and 22.5, 9 x 2304 x 40960 28.8 and 31.1, 16 x 1024
+// x 16384 12.2 and 15.0). Some wide and long ones would gain in tiles, those that one round
+// fills to 7/8, but their neighbours lose more (16 x 14336 x 20480 66.9 and 57.8, 28672 x
+// 14336 83.5 and 74.8; 28672 x 11008 65.6 and 75.4, 27648 x 20480 119 and 128).
 //
 // Above 16 tokens and for those, the tile whose estimated time is least: rounds of tiles over
 // the CUs times (stages x the tile's time per 128-k stage + its start and
