@@ -200,3 +200,10 @@ def test_outputs_apart_from_inputs_and_one_another():
             ops._apart(outs, ins)
     with pytest.raises(ValueError):
         ops._apart({"h": t[1:]}, {"x": t[:7]}, in_place=(("h", "x"),))
+
+
+def test_inputs_may_meet_where_an_output_is_absent():
+    t, codes = torch.zeros((8, 64), dtype=torch.float16), torch.zeros((8, 64), dtype=torch.int8)
+    ops._apart({"h": None, "xq": codes, "normed": None}, {"x": t, "residual": t, "weight": t[0]})
+    with pytest.raises(ValueError):
+        ops._apart({"h": None, "xq": codes, "normed": t}, {"x": t, "residual": None})

@@ -295,3 +295,20 @@ def test_outputs_on_other_rows_tokens_are_refused():
     o.w8a8_rmsnorm_quantize(x, w, residual=r, return_normed=True, out=fine)
     for a, b in zip(fine, o.w8a8_rmsnorm_quantize(x, w, residual=r, return_normed=True)):
         assert torch.equal(a, b)
+
+
+def test_norm_of_a_residual_that_is_x():
+    """Inputs may be the same tensor, whichever outputs are given."""
+    import torch
+    o = ops()
+    x = torch.randn(5, 96, generator=gen(4), device="cuda").half()
+    w = torch.rand(96, generator=gen(5), device="cuda").half()
+    for normed in (False, True):
+        want = o.w8a8_rmsnorm_quantize(x, w, residual=x, return_normed=normed)
+        out = tuple(torch.empty_like(t) for t in want)
+        for a, b in zip(o.w8a8_rmsnorm_quantize(x, w, residual=x, return_normed=normed, out=out), want):
+            assert torch.equal(a, b)
+        keep = x.clone()
+        for a, b in zip(o.w8a8_rmsnorm_quantize(x, w, residual=x, return_normed=normed, out=(*out[:2], x, *out[3:])), want):
+            assert torch.equal(a, b)
+        x.copy_(keep)

@@ -700,12 +700,13 @@ def _span(t):
 
 
 def _apart(outs: dict, ins: dict, in_place=()) -> None:
-    """Refuses outputs that share memory with an input or with one another. ``in_place``:
-    the pairs of names that may also be the same tensor."""
-    rest = [(name, t, *_span(t)) for name, t in (*outs.items(), *ins.items()) if t is not None]
-    for _ in outs:
-        name, a, a0, a1 = rest.pop(0)
-        for other, b, b0, b1 in rest:
+    """Refuses outputs that share memory with an input or with one another (None: absent;
+    inputs may meet). ``in_place``: the pairs of names that may also be the same tensor."""
+    given = [(name, t, *_span(t)) for name, t in (*outs.items(), *ins.items()) if t is not None]
+    for i, (name, a, a0, a1) in enumerate(given):
+        if name not in outs:
+            break
+        for other, b, b0, b1 in given[i + 1:]:
             if a0 < b1 and b0 < a1:
                 if (name, other) in in_place:
                     _in_place_or_apart(a, b, f"{name} and {other}")
