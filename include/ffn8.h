@@ -44,7 +44,8 @@ enum {
  *   h         out, with a residual: [M][ldh] as x; may be x or residual itself (same
  *             pointer and stride), else must not overlap them
  *   y         out: NULL or [M][ldy] as x
- * The outputs lie apart from one another and, but for h, from the inputs.
+ * The outputs lie apart from one another and, but for h, from the inputs
+ * (W4A4_E_OVERLAP; here and below).
  */
 w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx, const void* residual, int64_t ldr,
                                     const void* weight, int32_t w_dtype, float eps, int64_t M, int64_t K,

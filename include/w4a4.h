@@ -65,7 +65,8 @@ typedef enum {
   W4A4_E_ALIGN = 4,  /* a pointer or leading dimension breaks the alignment rule of the call */
   W4A4_E_DTYPE = 5,  /* unknown output dtype */
   W4A4_E_HIP = 6,    /* the HIP runtime reported an error for the launch */
-  W4A4_E_SCRATCH = 7 /* the call needs more than the library's static scratch buffer */
+  W4A4_E_SCRATCH = 7, /* the call needs more than the library's static scratch buffer */
+  W4A4_E_OVERLAP = 8 /* an output or the workspace shares memory with another buffer (the calls of ffn8.h check) */
 } w4a4_status_t;
 
 typedef enum {

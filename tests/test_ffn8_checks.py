@@ -179,31 +179,72 @@ def test_act_channels_whose_padded_sums_reach_2_31_bytes():
             assert f(M=0, N=N, ldy=N, gated=gated) == OK
 
 
-def test_outputs_apart_from_inputs_and_one_another():
-    t = torch.zeros((8, 64), dtype=torch.float16)
-    raw = torch.zeros(4096, dtype=torch.uint8)
-    codes, scales = raw[:512].view(torch.int8).view(8, 64), raw[512:544].view(torch.float32)
-    w = torch.zeros(64)
-    ops._apart({"xq": codes, "xs": scales}, {"x": t, "weight": w, "residual": None})
-    ops._apart({"a": t[:, :32], "b": t[:, 32:48]}, {"c": t[:, 48:], "d": t[:, 50:60]})     # inputs may meet
-    ops._apart({"a": t[:0], "b": raw[:0]}, {"c": t, "d": raw})
-    ops._apart({"h": t}, {"x": t}, in_place=(("h", "x"),))
-    x = raw[:1024].view(torch.float16).view(8, 64)
-    for outs, ins in [({"xq": codes}, {"x": x}),                                           # a row's codes over another row
-                      ({"xq": raw[1008:1520].view(torch.int8).view(8, 64)}, {"x": x}),     # the last row alone
-                      ({"xs": scales}, {"x": x}), ({"xs": raw[1020:1052].view(torch.float32)}, {"x": x}),
-                      ({"xq": codes, "xs": raw[:32].view(torch.float32)}, {"x": t}),       # outputs on one another
-                      ({"xq": codes, "xs": raw[508:540].view(torch.float32)}, {"x": t}),
-                      ({"xs": w[:8]}, {"x": t, "weight": w}), ({"h": x}, {"x": x}),
-                      ({"y": t[:, :32]}, {"x": t[:, 31:40]})]:
-        with pytest.raises(ValueError):
-            ops._apart(outs, ins)
-    with pytest.raises(ValueError):
-        ops._apart({"h": t[1:]}, {"x": t[:7]}, in_place=(("h", "x"),))
+E_OVERLAP = 8
+FAR = 1 << 20        # between the fake buffers below
 
 
-def test_inputs_may_meet_where_an_output_is_absent():
-    t, codes = torch.zeros((8, 64), dtype=torch.float16), torch.zeros((8, 64), dtype=torch.int8)
-    ops._apart({"h": None, "xq": codes, "normed": None}, {"x": t, "residual": t, "weight": t[0]})
-    with pytest.raises(ValueError):
-        ops._apart({"h": None, "xq": codes, "normed": t}, {"x": t, "residual": None})
+def test_norm_outputs_that_meet_buffers():
+    """Codes, scales, sums and normed rows apart from one another and from the inputs, whatever is absent."""
+    M, K = 8, 64
+    base = dict(x=P, ldx=64, r=P + FAR, ldr=64, w=P + 2 * FAR, q=P + 3 * FAR, s=P + 4 * FAR, h=P + 5 * FAR, ldh=64,
+                y=P + 6 * FAR, ldy=64)
+
+    def f(**k):
+        a = dict(base, **k)
+        return _lib.status_of("w8a8_rmsnorm_quantize", a["x"], F16, a["ldx"], a["r"], a["ldr"], a["w"], F32, 1e-6, M, K,
+                              a["q"], a["s"], a["h"], a["ldh"], a["y"], a["ldy"], None)
+    inputs = [base[n] for n in ("x", "r", "w")]
+    for name in ("q", "s", "y"):
+        for at in inputs + [base[n] for n in ("q", "s", "h", "y") if n != name]:
+            assert f(**{name: at}) == E_OVERLAP, (name, at)
+    assert f(q=P + 1008) == E_OVERLAP and f(q=P - 496) == E_OVERLAP and f(s=P + 1020) == E_OVERLAP     # by their ends
+    assert f(h=P + 16) == E_OVERLAP and f(h=P + 2 * FAR) == E_OVERLAP and f(h=P + FAR + 128) == E_OVERLAP
+    assert f(h=P, ldh=72) == E_OVERLAP                                          # x itself, at another stride
+    assert f(r=None, h=None, q=P) == E_OVERLAP and f(r=None, h=None, y=None, s=P) == E_OVERLAP
+    # columns of one buffer that touch by one
+    assert f(ldx=200, r=P + 126, ldr=200, h=P + 240, ldh=200) == E_ALIGN and f(ldx=200, h=P + 112, ldh=200) == E_OVERLAP
+    assert f(ldx=200, h=P + 384, ldh=200) == E_OVERLAP                          # round the row's end
+
+
+def test_act_outputs_that_meet_buffers():
+    for gated in (0, 1):
+        C = 8 << gated
+        for f, tokens in ((gemm_act, "xq"), (linear_act, "x")):
+            base = {tokens: P, "wq": P + FAR, "ws": P + 2 * FAR, "bias": P + 3 * FAR, "res": P + 4 * FAR, "ldr": 8,
+                    "wsp": P + 5 * FAR, "y": P + 6 * FAR, "gated": gated}
+            if tokens == "xq":
+                base["xs"] = P + 7 * FAR
+            call = lambda **k: f(**dict(base, **k))
+            for name in (tokens, "wq", "ws", "bias", *(["xs"] if tokens == "xq" else [])):
+                assert call(y=base[name]) == E_OVERLAP, name
+            assert call(y=P + FAR + C * 64 - 2) == E_OVERLAP and call(y=P + FAR - 2) == E_OVERLAP
+            assert call(y=P + 4 * FAR + 16) == E_OVERLAP and call(y=P + 4 * FAR, ldy=16) == E_OVERLAP
+            # the workspace, where there is one
+            big = dict(M=64, N=8192 >> gated, K=8192, ldy=8192 >> gated, ldr=8192 >> gated)
+            big = {n: big[n] for n in big} | ({"ldx": 8192} if tokens == "x" else {})
+            far = {n: P + i * (1 << 34) for i, n in enumerate(n for n in base if n not in ("ldr", "gated"))}
+            for name in far:
+                if name != "wsp":
+                    assert f(**dict(far, gated=gated, wsp=far[name], **big)) == E_OVERLAP, name
+
+
+def test_route_and_moe_outputs_that_meet_buffers():
+    def route(x=P, ids=P + FAR, w=P + 2 * FAR, ld=64):
+        return _lib.status_of("moe_route", x, F32, 4, 64, ld, 8, 1, ids, w, None)
+    assert route(ids=P) == E_OVERLAP and route(w=P + 1020) == E_OVERLAP and route(w=P + FAR + 124) == E_OVERLAP
+    assert route(ids=P + 3 * 400 + 252, ld=100) == E_OVERLAP and route(ids=P - 4, ld=100) == E_OVERLAP
+    T, k, E, H, I = 4, 2, 8, 64, 32
+    names = ("xq", "xs", "ids", "w", "w13", "s13", "w2", "s2", "wsp", "y")
+    base = {n: P + i * FAR for i, n in enumerate(names)}
+
+    def moe(**a):
+        a = dict(base, **a)
+        return _lib.status_of("w8a8_moe", a["xq"], a["xs"], a["ids"], a["w"], T, k, a["w13"], a["s13"], a["w2"], a["s2"], E,
+                              H, I, 2, a["wsp"], 1 << 30, a["y"], F16, 64, None)
+    for name in ("ids", "w", "w2", "s2", "wsp"):
+        assert moe(y=base[name]) == E_OVERLAP, name
+    for name in names:
+        if name != "wsp":
+            assert moe(wsp=base[name]) == E_OVERLAP, name
+    assert moe(y=base["w2"] + E * H * I - 2) == E_OVERLAP and moe(y=base["ids"] - 2) == E_OVERLAP
+    assert _lib.load_library().w4a4_status_str(E_OVERLAP) != b"unknown status"

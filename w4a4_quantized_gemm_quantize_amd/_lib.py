@@ -17,6 +17,7 @@ W4A4_OK = 0
 STATUS_NAMES = {
     0: "W4A4_OK", 1: "W4A4_E_NULL", 2: "W4A4_E_SHAPE", 3: "W4A4_E_GROUP",
     4: "W4A4_E_ALIGN", 5: "W4A4_E_DTYPE", 6: "W4A4_E_HIP", 7: "W4A4_E_SCRATCH",
+    8: "W4A4_E_OVERLAP",
 }
 Y_F32 = 0
 Y_F16 = 1

@@ -74,6 +74,7 @@ const char* w4a4_status_str(int status) {
     case W4A4_E_DTYPE: return "unknown output dtype";
     case W4A4_E_HIP: return "HIP launch error";
     case W4A4_E_SCRATCH: return "needs more scratch memory than the library's static buffer holds";
+    case W4A4_E_OVERLAP: return "an output or the workspace overlaps another buffer";
     default: return "unknown status";
   }
 }

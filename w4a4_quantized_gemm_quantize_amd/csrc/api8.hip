@@ -96,6 +96,34 @@ w4a4_status_t kv_pointers(const KvPool& c, const KvBatch& b) {
   return W4A4_OK;
 }
 
+// Rows of a buffer: `rows` of `width` bytes, `pitch` bytes apart.
+struct Rows {
+  const void* at;
+  int64_t rows, pitch, width;
+  uintptr_t first() const { return reinterpret_cast<uintptr_t>(at); }
+  uintptr_t end() const { return first() + (uintptr_t)(rows - 1) * (uintptr_t)pitch + (uintptr_t)width; }
+};
+Rows flat(const void* at, int64_t bytes) { return Rows{at, 1, bytes, bytes}; }
+
+// Whether two buffers share memory (absent ones do not; neither do columns apart in rows of
+// one pitch, nor a run between two rows).
+bool meet(const Rows& a, const Rows& b) {
+  if (!a.at || !b.at || a.rows == 0 || b.rows == 0 || a.width == 0 || b.width == 0) return false;
+  if (a.first() >= b.end() || b.first() >= a.end()) return false;
+  if ((a.rows == 1 && b.rows == 1) || (a.rows > 1 && b.rows > 1 && a.pitch != b.pitch)) return true;
+  const int64_t pitch = a.rows > 1 ? a.pitch : b.pitch;
+  const int64_t d = (int64_t)(b.first() - a.first()) % pitch, apart = d < 0 ? d + pitch : d;
+  return apart < a.width || apart + b.width > pitch;
+}
+// An output that may also be the input itself.
+bool meet_elsewhere(const Rows& out, const Rows& in) {
+  return meet(out, in) && !(out.at == in.at && (out.rows == 1 || out.pitch == in.pitch));
+}
+template <class... R>
+bool meets_any(const Rows& a, const R&... others) {
+  return (meet(a, others) || ...);
+}
+
 }  // namespace
 
 extern "C" {
@@ -306,6 +334,12 @@ w4a4_status_t w8a8_rmsnorm_quantize(const void* x, int32_t x_dtype, int64_t ldx,
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(xq, 16) || !aligned(xs, 4) ||
       (residual && !aligned(h, 16)) || !aligned(y, 16))
     return W4A4_E_ALIGN;
+  const Rows rx{x, M, 2 * ldx, 2 * K}, rr{residual, M, 2 * ldr, 2 * K}, rw = flat(weight, K * (w_dtype == W4A4_Y_F32 ? 4 : 2));
+  const Rows rq = flat(xq, M * K), rs = flat(xs, 4 * M), ry{y, M, 2 * ldy, 2 * K};
+  const Rows rh{residual ? h : nullptr, M, 2 * ldh, 2 * K};
+  if (meets_any(rq, rx, rr, rw, rs, rh, ry) || meets_any(rs, rx, rr, rw, rh, ry) || meets_any(ry, rx, rr, rw, rh) ||
+      meet(rh, rw) || meet_elsewhere(rh, rx) || meet_elsewhere(rh, rr))
+    return W4A4_E_OVERLAP;
   w4a4::W8NormArgs a = {};
   a.x = x; a.residual = residual; a.weight = weight; a.h = h; a.y = y; a.q = xq; a.s = xs;
   a.ldx = ldx; a.ldr = ldr; a.ldh = ldh; a.ldy = ldy; a.M = M; a.K = K;
@@ -336,6 +370,16 @@ int64_t w8a8_linear_act_workspace(int64_t M, int64_t N, int64_t K, int32_t gated
   if (gemm < 0) return -1;
   if (M == 0 || N == 0 || w4a4::w8a8_one_launch(M, act_channels(N, gated), K)) return 0;
   return align256(M * K) + align256(4 * M) + gemm;
+}
+
+// Whether y or the workspace meets another buffer of such a product (y may be the
+// residual itself). in: the tokens or their codes; xs: their scales, or absent.
+static bool act_meets(const Rows& in, const float* xs, const w4a4::W8GemmArgs& g, const w4a4::W8Epilogue& e,
+                      const void* workspace, int64_t need) {
+  const int64_t outs = e.gated ? g.N / 2 : g.N;
+  const Rows y{g.y, g.M, 2 * g.ldy, 2 * outs}, r{e.residual, g.M, 2 * e.ldr, 2 * outs}, space = flat(workspace, need);
+  const Rows s = flat(xs, 4 * g.M), w = flat(g.w, g.N * g.K), sw = flat(g.sw, 4 * g.N), b = flat(g.bias, 4 * g.N);
+  return meets_any(y, in, s, w, sw, b, space) || meet_elsewhere(y, r) || meets_any(space, in, s, w, sw, b, r);
 }
 
 // The checks and the descriptions that the two calls share.
@@ -375,6 +419,7 @@ w4a4_status_t w8a8_gemm_act(const int8_t* xq, const float* xs, const int8_t* wq,
   const int64_t need = w8a8_gemm_act_workspace(M, N, K, gated, e.wide);
   if (workspace_bytes < need) return W4A4_E_SHAPE;
   if (need > 0 && !workspace) return W4A4_E_NULL;
+  if (act_meets(flat(xq, M * K), xs, g, e, workspace, need)) return W4A4_E_OVERLAP;
   g.a = xq; g.sa = xs;
   g.workspace = workspace;
   w4a4::launch_w8a8_gemm_act(g, e, as_stream(stream));
@@ -399,6 +444,7 @@ w4a4_status_t w8a8_linear_act(const void* x, int32_t x_dtype, int64_t M, int64_t
   const int64_t need = w8a8_linear_act_workspace(M, N, K, gated, e.wide);
   if (workspace_bytes < need) return W4A4_E_SHAPE;
   if (need > 0 && !workspace) return W4A4_E_NULL;
+  if (act_meets(Rows{x, M, 2 * ldx, 2 * K}, nullptr, g, e, workspace, need)) return W4A4_E_OVERLAP;
   const int bf16 = x_dtype == W4A4_Y_BF16;
   if (w4a4::w8a8_one_launch(M, g.N, K)) {
     w4a4::launch_w8a8_small_act(g, e, x, bf16, ldx, as_stream(stream));
@@ -421,6 +467,9 @@ w4a4_status_t moe_route(const void* logits, int32_t dtype, int64_t T, int64_t E,
   if (T == 0) return W4A4_OK;
   if (!logits || !ids || !weights) return W4A4_E_NULL;
   if (!aligned(logits, dtype == W4A4_Y_F32 ? 4 : 2) || !aligned(ids, 4) || !aligned(weights, 4)) return W4A4_E_ALIGN;
+  const int64_t size = dtype == W4A4_Y_F32 ? 4 : 2;
+  const Rows rl{logits, T, size * ldl, size * E}, ri = flat(ids, 4 * T * k), rw = flat(weights, 4 * T * k);
+  if (meets_any(ri, rl, rw) || meet(rw, rl)) return W4A4_E_OVERLAP;
   w4a4::launch_moe_route(logits, dtype, T, E, ldl, (int)k, renormalize != 0, ids, weights, as_stream(stream));
   return launched();
 }
@@ -449,6 +498,12 @@ w4a4_status_t w8a8_moe(const int8_t* xq, const float* xs, const int32_t* ids, co
   if (!aligned(xq, 16) || !aligned(w13, 16) || !aligned(w2, 16) || !aligned(workspace, 16) || !aligned(xs, 4) ||
       !aligned(ids, 4) || !aligned(weights, 4) || !aligned(s13, 4) || !aligned(s2, 4) || !aligned(y, 2))
     return W4A4_E_ALIGN;
+  // y is written while the last launch still reads the others
+  const Rows ry{y, T, 2 * ldy, 2 * H}, space = flat(workspace, need), ri = flat(ids, 4 * T * k), rf = flat(weights, 4 * T * k);
+  const Rows r2 = flat(w2, E * H * I), rs2 = flat(s2, 4 * E * H);
+  if (meets_any(ry, ri, rf, r2, rs2, space) ||
+      meets_any(space, flat(xq, T * H), flat(xs, 4 * T), ri, rf, flat(w13, 2 * E * I * H), flat(s13, 8 * E * I), r2, rs2))
+    return W4A4_E_OVERLAP;
   w4a4::MoeArgs a = {};
   a.xq = xq; a.xs = xs; a.ids = ids; a.weights = weights;
   a.w13 = w13; a.s13 = s13; a.w2 = w2; a.s2 = s2;

@@ -690,30 +690,6 @@ def _in_place_or_apart(out, t, names: str) -> None:
         raise ValueError(f"{names} overlap without being the same tensor")
 
 
-def _span(t):
-    """The addresses [first, end) of a tensor that is contiguous, or 2-D with contiguous rows."""
-    start, n = t.data_ptr(), t.numel()
-    if n and t.dim() == 2:
-        rows, cols = t.shape
-        n = (rows - 1) * t.stride(0) + cols
-    return start, start + n * t.element_size()
-
-
-def _apart(outs: dict, ins: dict, in_place=()) -> None:
-    """Refuses outputs that share memory with an input or with one another (None: absent;
-    inputs may meet). ``in_place``: the pairs of names that may also be the same tensor."""
-    given = [(name, t, *_span(t)) for name, t in (*outs.items(), *ins.items()) if t is not None]
-    for i, (name, a, a0, a1) in enumerate(given):
-        if name not in outs:
-            break
-        for other, b, b0, b1 in given[i + 1:]:
-            if a0 < b1 and b0 < a1:
-                if (name, other) in in_place:
-                    _in_place_or_apart(a, b, f"{name} and {other}")
-                elif a.dim() != 2 or b.dim() != 2 or _overlap(a, b):
-                    raise ValueError(f"{name} overlaps {other}")
-
-
 def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=None, return_normed: bool = False,
                           out=None):
     """RMS norm of fp16 or bf16 X[M, K] (row stride may exceed K) to INT8 codes and one
@@ -761,11 +737,14 @@ def w8a8_rmsnorm_quantize(x: torch.Tensor, weight, eps: float = 1e-6, residual=N
         if residual is not None:
             ldh = _need_rows(out[2], "h", shape, dtype, device)
             h = out[2].data_ptr()
+            _in_place_or_apart(out[2], x, "h and x")
+            _in_place_or_apart(out[2], residual, "h and residual")
         if return_normed:
             ldy = _need_rows(out[-1], "normed", shape, dtype, device)
             y = out[-1].data_ptr()
-        _apart({"h": out[2] if residual is not None else None, "xq": xq, "xs": xs, "normed": out[-1] if return_normed else None},
-               {"x": x, "residual": residual, "weight": weight}, in_place=(("h", "x"), ("h", "residual")))
+            for t in (x, *((residual, out[2]) if residual is not None else ())):
+                if _overlap(out[-1], t):
+                    raise ValueError("normed overlaps x, residual or h")
     _call8("w8a8_rmsnorm_quantize", device, x.data_ptr(), dt, ldx, r, ldr, weight.data_ptr(), _DTYPE8[weight.dtype], eps,
            M, K, xq.data_ptr(), xs.data_ptr(), h, ldh, y, ldy)
     return out
@@ -830,8 +809,6 @@ def w8a8_gemm_act(xq, xs, wq, ws, bias=None, activation=None, gated: bool = Fals
     N, K, ldr, y, dt, ldy, wide = _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out)
     if xq.shape[1] != K:
         raise ValueError("K of xq and wq differ")
-    if out is not None:
-        _apart({"out": y}, {"xq": xq, "xs": xs, "wq": wq, "ws": ws, "bias": bias})
     held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_gemm_act_workspace", M, N, K, gated, wide), device)
     _call8("w8a8_gemm_act", device, xq.data_ptr(), xs.data_ptr(), wq.data_ptr(), ws.data_ptr(),
            0 if bias is None else bias.data_ptr(), act, gated, 0 if residual is None else residual.data_ptr(), ldr,
@@ -853,8 +830,8 @@ def w8a8_linear_act(x: torch.Tensor, wq, ws, bias=None, activation=None, gated: 
     N, K, ldr, y, dt, ldy, wide = _act_operands(device, M, wq, ws, bias, gated, residual, out_dtype, out)
     if x.shape[1] != K:
         raise ValueError("K of x and wq differ")
-    if out is not None:
-        _apart({"out": y}, {"x": x, "wq": wq, "ws": ws, "bias": bias})
+    if out is not None and _overlap(x, out):
+        raise ValueError("out overlaps x")
     held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_linear_act_workspace", M, N, K, gated, wide), device)
     _call8("w8a8_linear_act", device, x.data_ptr(), xdt, M, K, ld, wq.data_ptr(), ws.data_ptr(),
            0 if bias is None else bias.data_ptr(), act, gated, 0 if residual is None else residual.data_ptr(), ldr,
@@ -881,7 +858,6 @@ def moe_route(logits: torch.Tensor, top_k: int, renormalize: bool = True, out=No
         ids, weights = out
         _check_out(ids, "ids", (T, k), torch.int32, logits.device)
         _check_out(weights, "weights", (T, k), torch.float32, logits.device)
-        _apart({"ids": ids, "weights": weights}, {"logits": logits})
     _call8("moe_route", logits.device, logits.data_ptr(), dt, T, E, ld, k, int(bool(renormalize)), ids.data_ptr(),
            weights.data_ptr())
     return ids, weights
@@ -942,7 +918,6 @@ def w8a8_moe(xq, xs, ids, weights, w13, s13, w2, s2, activation="silu", out_dtyp
     else:
         y = out
         _check_out(y, "out", (T, H), getattr(y, "dtype", None), device, row_stride_ok=True)
-        _apart({"out": y}, {"ids": ids, "weights": weights, "w2": w2, "s2": s2})       # read until the last store
     dt = _x_dtype8(y, "out")
     held, wptr, wbytes = _workspace8(workspace, _workspace_size("w8a8_moe_workspace", T, k, E, H, I), device)
     _call8("w8a8_moe", device, xq.data_ptr(), xs.data_ptr(), ids.data_ptr(), weights.data_ptr(), T, k, w13.data_ptr(),
